@@ -1898,6 +1898,7 @@ extern "C" const char* jca_status_string(int code) {
     case JCA_ERR_DEVICE: return "the current device is not sm_100 (B200)";
     case JCA_ERR_SCRATCH_LIMIT:
       return "problem needs more scratch than the library's static array holds";
+    case JCA_ERR_DTYPE: return "unsupported element type";
     case JCA_STATUS_BAD_LENGTH: return "negative length or offsets overflow the index type";
     case JCA_STATUS_BAD_OFFSETS: return "offsets do not start at 0, decrease, or do not end at rows";
     case JCA_STATUS_BAD_CAND_START: return "candidate_start outside [0, row length]";
@@ -1906,6 +1907,8 @@ extern "C" const char* jca_status_string(int code) {
     case JCA_STATUS_QUEUE_OVERFLOW: return "work queue overflow";
     case JCA_STATUS_BAD_SPLIT:
       return "history/candidate token counts differ from the totals given to the stack";
+    case JCA_STATUS_BAD_TREE:
+      return "a drafted token's parent is not an earlier token of its run, or a run is too long";
     case JCA_STATUS_TIMEOUT: return "an attention pipeline wait timed out";
     default: return "unknown code";
   }

@@ -77,6 +77,23 @@ _SIGNATURES = {
     "jca_stack_fwd": (c_i32, [c_vp, c_vp, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64,
                               c_i64, c_i32, c_i32, c_f32, c_i64, c_f32, c_i32, c_vp, c_sz, c_vp,
                               c_vp]),
+    "jca_rope_axes_fwd": (c_i32, [c_vp] * 6 + [c_i32, c_i32, c_i64, c_i32, c_i32, c_i32] +
+                          [c_i64] * 4 + [c_f32, c_i32, c_i32, c_vp]),
+    "jca_rope_axes_bwd": (c_i32, [c_vp] * 6 + [c_i32, c_i32, c_i64, c_i32, c_i32, c_i32] +
+                          [c_i64] * 4 + [c_f32, c_i32, c_i32, c_vp]),
+    "jca_window_workspace_bytes": (c_sz, [c_i64, c_i64, c_i32, c_i32, c_i32, c_i32]),
+    "jca_window_bwd_workspace_bytes": (c_sz, [c_i64, c_i64, c_i32, c_i32, c_i32, c_i32]),
+    "jagged_window_attn_fwd": (c_i32, [c_vp] * 7 + [c_i64, c_i64, c_i32, c_i32, c_i32, c_i64, c_i32,
+                                                    c_i64, c_i64, c_i64, c_f32, c_i32, c_vp, c_sz,
+                                                    c_vp, c_vp]),
+    "jagged_window_attn_bwd": (c_i32, [c_vp] * 11 + [c_i64, c_i64, c_i32, c_i32, c_i32, c_i64,
+                                                     c_i32, c_i64, c_i64, c_i64, c_f32, c_i32,
+                                                     c_vp, c_sz, c_vp, c_vp]),
+    "jagged_window_decode_fwd": (c_i32, [c_vp] * 8 + [c_i64, c_i64, c_i32, c_i32, c_i32, c_i64,
+                                                      c_i64, c_i64, c_i64, c_i64, c_f32, c_i32,
+                                                      c_vp, c_vp]),
+    "cand_tree_attn_fwd": (c_i32, [c_vp] * 10 + [c_i64, c_i64, c_i64, c_i32, c_i32, c_i32, c_i32,
+                                                 c_i64, c_i64, c_i64, c_f32, c_i32, c_vp, c_vp]),
     "jca_noalloc_scratch_bytes": (c_sz, []),
     "jca_noalloc_prepare": (c_i32, []),
     "jca_user_tile_cost": (c_i64, [c_i64, c_i64]),
@@ -554,6 +571,236 @@ def jca_stack_fwd(x, x_out, weights, n_cand_only: int, offsets, candidate_start=
         _ptr(candidate_start), _ptr(seg), B, T, int(Nc), int(Th), int(H), d, float(scale),
         -1 if history_end is None else int(history_end), float(rope_base), _idx_bits(offsets),
         _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream)), "jca_stack_fwd")
+
+
+# Rotary positions with several axes, windowed attention, and attention over a cache. These check
+# shapes, types, devices and strides here, run on the tensors' own device (its current stream,
+# unless a stream is given) and accept rows that are apart (slices of a fused projection).
+
+_ROPE_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _rows(name: str, t: torch.Tensor, rows: int, heads: int, d: int, dtype, device) -> int:
+    """Checks a [rows, heads, d] tensor with packed heads; returns its row stride in elements."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.dim() != 3 or t.shape[0] != rows or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{name} must be [{rows}, {heads}, {d}], got {list(t.shape)}")
+    if rows == 0:
+        return heads * d
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != d):
+        raise ValueError(f"{name}: the heads of a row must be packed")
+    return s0 if rows > 1 else heads * d
+
+
+def _packed(name: str, t: torch.Tensor, rows: int, heads: int, d: int, dtype, device) -> None:
+    if _rows(name, t, rows, heads, d, dtype, device) != heads * d:
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _vector(name: str, t: Optional[torch.Tensor], n: int, dtype, device) -> None:
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {n} elements, got {list(t.shape)}")
+
+
+def _heads(name: str, t: torch.Tensor):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have three dimensions, got {list(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.shape
+
+
+def _call(fn: str, device, stream, *args) -> int:
+    """The C entry point `fn` with `device` current, on its current stream unless one is given."""
+    f = getattr(lib(), fn)
+    if torch.cuda.current_device() == device.index:
+        return _check(f(*args, _stream(stream)), fn)
+    with torch.cuda.device(device):
+        return _check(f(*args, _stream(stream)), fn)
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _rope_axes(fn, q, k, q_out, k_out, positions, sections, base, per_axis, stream) -> int:
+    T, H, d = _heads("q", q)
+    dev, dtype = q.device, q.dtype
+    if dtype not in _ROPE_TYPES:
+        raise TypeError(f"q must be bfloat16, float16 or float32, got {dtype}")
+    qs, qo = _rows("q", q, T, H, d, dtype, dev), _rows("q_out", q_out, T, H, d, dtype, dev)
+    Hkv, ks, ko = 0, 0, 0
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    if k is not None:
+        Hkv = _heads("k", k)[1]
+        ks, ko = _rows("k", k, T, Hkv, d, dtype, dev), _rows("k_out", k_out, T, Hkv, d, dtype, dev)
+    n_axes = len(sections)
+    if positions.dim() == 1:
+        positions = positions[:, None]
+    if list(positions.shape) != [T, n_axes] or not positions.is_contiguous():
+        raise ValueError(f"positions must be contiguous [{T}, {n_axes}], got "
+                         f"{list(positions.shape)}")
+    if positions.device != dev:
+        raise ValueError(f"positions is on {positions.device}, not on {dev}")
+    sec = (c_i32 * n_axes)(*[int(x) for x in sections])
+    return _call(fn, dev, stream, _at(q), _at(k), _at(q_out), _at(k_out), _at(positions), sec,
+                 n_axes, int(bool(per_axis)), T, H, Hkv, d, qs, ks, qo, ko, float(base),
+                 _ROPE_TYPES[dtype], _idx_bits(positions))
+
+
+def jca_rope_axes_fwd(q, k, q_out, k_out, positions, sections, base: float = 10000.0,
+                      per_axis: bool = False, stream=None) -> int:
+    """Rotates q [T, H, d] and k [T, Hkv, d] (k may be None) by several axes of positions
+    [T, n_axes] (int32 or int64): the first sections[0] pairs (j, j + d/2) of every head by axis 0,
+    the next sections[1] by axis 1, ...; the rest stays. Frequencies run over the head, or over
+    each axis' own pairs with per_axis. bf16, fp16 or fp32; outputs may be the inputs."""
+    return _rope_axes("jca_rope_axes_fwd", q, k, q_out, k_out, positions, sections, base, per_axis,
+                      stream)
+
+
+def jca_rope_axes_bwd(dq_out, dk_out, dq, dk, positions, sections, base: float = 10000.0,
+                      per_axis: bool = False, stream=None) -> int:
+    """Gradient of jca_rope_axes_fwd: dq, dk from the gradients of its outputs."""
+    return _rope_axes("jca_rope_axes_bwd", dq_out, dk_out, dq, dk, positions, sections, base,
+                      per_axis, stream)
+
+
+def jca_window_workspace_bytes(B: int, T: int, H: int, Hkv: int, d_head: int, n_sinks: int) -> int:
+    return int(lib().jca_window_workspace_bytes(B, T, H, Hkv, d_head, n_sinks))
+
+
+def jca_window_bwd_workspace_bytes(B: int, T: int, H: int, Hkv: int, d_head: int,
+                                   n_sinks: int) -> int:
+    return int(lib().jca_window_bwd_workspace_bytes(B, T, H, Hkv, d_head, n_sinks))
+
+
+def _window_scratch(workspace, status, nbytes, dev):
+    if workspace is None:
+        workspace = torch.empty(nbytes(), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {dev}")
+    if status is None:
+        status = new_status(dev)
+    else:
+        _vector("status", status, 1, torch.int32, dev)
+    return workspace, status
+
+
+def jagged_window_attn_fwd(q, k, v, out, offsets, window: int, n_sinks: int = 0, valid=None,
+                           lse=None, scale: float = 0.0,
+                           workspace: Optional[torch.Tensor] = None,
+                           status: Optional[torch.Tensor] = None, stream=None) -> int:
+    """Per-user causal attention with a sliding window and the first n_sinks tokens of every row
+    visible: q [T, H, d], k and v [T, Hkv, d] bf16, out [T, H, d] bf16; valid [T] uint8 (1 = real
+    token) and lse [T, H] fp32 are optional."""
+    T, H, d = _heads("q", q)
+    Hkv, dev, t16 = _heads("k", k)[1], q.device, torch.bfloat16
+    B = offsets.numel() - 1
+    qs, ks = _rows("q", q, T, H, d, t16, dev), _rows("k", k, T, Hkv, d, t16, dev)
+    vs = _rows("v", v, T, Hkv, d, t16, dev)
+    _packed("out", out, T, H, d, t16, dev)
+    _vector("offsets", offsets, B + 1, offsets.dtype, dev)
+    _vector("valid", valid, T, torch.uint8, dev)
+    _vector("lse", lse, T * H, torch.float32, dev)
+    workspace, status = _window_scratch(
+        workspace, status, lambda: jca_window_workspace_bytes(B, T, H, Hkv, d, n_sinks), dev)
+    return _call("jagged_window_attn_fwd", dev, stream, _at(q), _at(k), _at(v), _at(out), _at(lse),
+                 _at(offsets), _at(valid), B, T, H, Hkv, d, int(window), int(n_sinks), qs, ks, vs,
+                 float(scale), _idx_bits(offsets), _at(workspace),
+                 workspace.numel() * workspace.element_size(), _at(status))
+
+
+def jagged_window_attn_bwd(q, k, v, out, dout, lse, dq, dk, dv, offsets, window: int,
+                           n_sinks: int = 0, valid=None, scale: float = 0.0,
+                           workspace: Optional[torch.Tensor] = None,
+                           status: Optional[torch.Tensor] = None, stream=None) -> int:
+    """Gradients dq [T, H, d], dk and dv [T, Hkv, d] (bf16) of jagged_window_attn_fwd for the
+    upstream gradient dout; out and lse are the forward's."""
+    T, H, d = _heads("q", q)
+    Hkv, dev, t16 = _heads("k", k)[1], q.device, torch.bfloat16
+    B = offsets.numel() - 1
+    qs, ks = _rows("q", q, T, H, d, t16, dev), _rows("k", k, T, Hkv, d, t16, dev)
+    vs = _rows("v", v, T, Hkv, d, t16, dev)
+    for name, x, n in (("out", out, H), ("dout", dout, H), ("dq", dq, H), ("dk", dk, Hkv),
+                       ("dv", dv, Hkv)):
+        _packed(name, x, T, n, d, t16, dev)
+    _vector("offsets", offsets, B + 1, offsets.dtype, dev)
+    _vector("valid", valid, T, torch.uint8, dev)
+    _vector("lse", lse, T * H, torch.float32, dev)
+    workspace, status = _window_scratch(
+        workspace, status, lambda: jca_window_bwd_workspace_bytes(B, T, H, Hkv, d, n_sinks), dev)
+    return _call("jagged_window_attn_bwd", dev, stream, _at(q), _at(k), _at(v), _at(out), _at(dout),
+                 _at(lse), _at(dq), _at(dk), _at(dv), _at(offsets), _at(valid), B, T, H, Hkv, d,
+                 int(window), int(n_sinks), qs, ks, vs, float(scale), _idx_bits(offsets),
+                 _at(workspace), workspace.numel() * workspace.element_size(), _at(status))
+
+
+def jagged_window_decode_fwd(q, k_new, v_new, k_cache, v_cache, out, cache_offsets, cache_len,
+                             window: int, n_sinks: int = 0, scale: float = 0.0,
+                             status: Optional[torch.Tensor] = None, stream=None) -> int:
+    """One new token per user over a cache: q [B, H, d], k_new and v_new [B, Hkv, d] are written
+    behind the cache_len[b] tokens of user b's region [cache_offsets[b], cache_offsets[b+1]) of
+    k_cache, v_cache [R, Hkv, d], and attended with them under jagged_window_attn_fwd's mask.
+    cache_len[b] = -1 marks an empty slot."""
+    B, H, d = _heads("q", q)
+    Hkv, dev, t16 = _heads("k_new", k_new)[1], q.device, torch.bfloat16
+    R = _heads("k_cache", k_cache)[0]
+    qs, ks = _rows("q", q, B, H, d, t16, dev), _rows("k_new", k_new, B, Hkv, d, t16, dev)
+    vs = _rows("v_new", v_new, B, Hkv, d, t16, dev)
+    _packed("k_cache", k_cache, R, Hkv, d, t16, dev)
+    _packed("v_cache", v_cache, R, Hkv, d, t16, dev)
+    _packed("out", out, B, H, d, t16, dev)
+    _vector("cache_offsets", cache_offsets, B + 1, cache_offsets.dtype, dev)
+    _vector("cache_len", cache_len, B, cache_offsets.dtype, dev)
+    if status is None:
+        status = new_status(dev)
+    else:
+        _vector("status", status, 1, torch.int32, dev)
+    return _call("jagged_window_decode_fwd", dev, stream, _at(q), _at(k_new), _at(v_new),
+                 _at(k_cache), _at(v_cache), _at(out), _at(cache_offsets), _at(cache_len), B, R, H,
+                 Hkv, d, int(window), int(n_sinks), qs, ks, vs, float(scale),
+                 _idx_bits(cache_offsets), _at(status))
+
+
+def cand_tree_attn_fwd(cand_q, own_k, own_v, cand_offsets, parent, hist_k, hist_v, hist_offsets,
+                       out, max_cand: int, hist_len=None, scale: float = 0.0,
+                       status: Optional[torch.Tensor] = None, stream=None) -> int:
+    """Trees of drafted candidate tokens over cached histories: cand_q [Nc, H, d], own_k and own_v
+    [Nc, Hkv, d]; parent [Nc] int32 is the parent's index in the user's run or -1. Each token sees
+    its user's history (the first hist_len[b] rows of region [hist_offsets[b], hist_offsets[b+1])
+    of hist_k, hist_v [R, Hkv, d]), its ancestors and itself. No run is longer than max_cand."""
+    N, H, d = _heads("cand_q", cand_q)
+    Hkv, dev, t16 = _heads("own_k", own_k)[1], cand_q.device, torch.bfloat16
+    R = _heads("hist_k", hist_k)[0]
+    B = cand_offsets.numel() - 1
+    qs, ks = _rows("cand_q", cand_q, N, H, d, t16, dev), _rows("own_k", own_k, N, Hkv, d, t16, dev)
+    vs = _rows("own_v", own_v, N, Hkv, d, t16, dev)
+    _packed("hist_k", hist_k, R, Hkv, d, t16, dev)
+    _packed("hist_v", hist_v, R, Hkv, d, t16, dev)
+    _packed("out", out, N, H, d, t16, dev)
+    _vector("cand_offsets", cand_offsets, B + 1, cand_offsets.dtype, dev)
+    _vector("hist_offsets", hist_offsets, B + 1, cand_offsets.dtype, dev)
+    _vector("hist_len", hist_len, B, cand_offsets.dtype, dev)
+    _vector("parent", parent, N, torch.int32, dev)
+    if status is None:
+        status = new_status(dev)
+    else:
+        _vector("status", status, 1, torch.int32, dev)
+    return _call("cand_tree_attn_fwd", dev, stream, _at(cand_q), _at(own_k), _at(own_v),
+                 _at(cand_offsets), _at(parent), _at(hist_k), _at(hist_v), _at(hist_offsets),
+                 _at(hist_len), _at(out), B, N, R, H, Hkv, d, int(max_cand), qs, ks, vs,
+                 float(scale), _idx_bits(cand_offsets), _at(status))
 
 
 def jca_noalloc_scratch_bytes() -> int:

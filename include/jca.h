@@ -59,6 +59,7 @@ enum jca_code {
   JCA_ERR_DEVICE = -8,      /* current device is not sm_100 */
   JCA_ERR_SCRATCH_LIMIT = -9, /* jagged_cand_attn_fwd_noalloc: problem needs more scratch than
                                  the library's static array (jca_noalloc_scratch_bytes()) */
+  JCA_ERR_DTYPE = -10,      /* an element type other than those of enum jca_dtype */
   /* device-side data errors (written to *status) */
   JCA_STATUS_BAD_LENGTH = 1,     /* a sequence length is negative, or offsets overflow int32 */
   JCA_STATUS_BAD_OFFSETS = 2,    /* offsets[0] != 0, offsets decrease, or offsets[B] != rows */
@@ -68,6 +69,8 @@ enum jca_code {
   JCA_STATUS_QUEUE_OVERFLOW = 6, /* more work items than the workspace bound (internal) */
   JCA_STATUS_BAD_SPLIT = 7,      /* jca_stack_fwd: the segment IDs hold a different number of
                                     history or candidate tokens than the caller's Th / Nc */
+  JCA_STATUS_BAD_TREE = 8,       /* cand_tree_attn_fwd: a parent outside [-1, its token), or a run
+                                    of more than max_cand tokens */
   JCA_STATUS_TIMEOUT = 16        /* a pipeline wait in the attention kernel gave up */
 };
 
@@ -535,6 +538,149 @@ int jca_stack_fwd(const void* x, void* x_out, const void* weights, int n_layers,
                   int64_t T, int64_t Nc, int64_t Th, int H, int d_head, float scale,
                   int64_t history_end, float rope_base, int idx_bits, void* workspace,
                   size_t workspace_bytes, int32_t* status, jca_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Rotary positions with several axes: an event of a user's history has an order in the row, a time,
+ * a session, ... (an image or video token a time, a row and a column). Each axis turns its own
+ * pairs of a head, by that axis' position of the token. Beside jca_apply_rope, which is the case of
+ * one axis that owns every pair.
+ *
+ * Pairs are (j, j + d_head/2), j in [0, d_head/2). The first sections[0] pairs belong to axis 0, the
+ * next sections[1] to axis 1, and so on; pairs past the sections' sum are left as they are. Pair j
+ * turns by the angle positions[t, axis] * theta:
+ *   per_axis = 0:  theta = base^(-2 j / d_head), one row of frequencies over the whole head;
+ *   per_axis = 1:  theta = base^(-i / sections[axis]) for the i-th pair of its axis.
+ * (a, b) -> (a cos - b sin, a sin + b cos). Angles are formed and reduced in more than fp64 (positions
+ * of 2^31 lose nothing), the rotation is fp32 and each result is rounded once to the element type.
+ *   q [T, H, d_head] and k [T, Hkv, d_head] of `dtype` (JCA_BF16, JCA_FP16, JCA_FP32), read; k may
+ *     be NULL (Hkv is then ignored). Heads are packed (head stride d_head); consecutive tokens are
+ *     q_stride / k_stride elements apart (>= heads * d_head), so slices of a fused projection work.
+ *   q_out, k_out: the same shapes, rows q_out_stride / k_out_stride apart, written. q_out may be q
+ *     with the same stride (in place), and k_out k; other overlaps are not allowed.
+ *   positions [T, n_axes] int32 or int64 (idx_bits), packed, read. Any value is valid.
+ *   sections  [n_axes] HOST memory, read before the call returns; n_axes in 1..4, each >= 0, sum
+ *     <= d_head/2. base > 1.
+ * jca_rope_axes_bwd is its gradient: given the gradients of q_out and k_out it writes those of q and
+ * k, the rotation by the opposite angles; the arguments are otherwise the same.
+ * All pointers 16-byte aligned, strides multiples of 16 bytes.
+ * Errors: JCA_ERR_IDX_BITS, JCA_ERR_HEAD_DIM, JCA_ERR_SHAPE, JCA_ERR_DTYPE, JCA_ERR_NULL,
+ * JCA_ERR_ALIGN, JCA_ERR_DEVICE, JCA_ERR_CUDA. Nothing is reported through a status word.
+ * ------------------------------------------------------------------------------------------- */
+enum jca_dtype { JCA_BF16 = 0, JCA_FP16 = 1, JCA_FP32 = 2 };
+
+int jca_rope_axes_fwd(const void* q, const void* k, void* q_out, void* k_out,
+                      const void* positions, const int32_t* sections, int n_axes, int per_axis,
+                      int64_t T, int H, int Hkv, int d_head, int64_t q_stride, int64_t k_stride,
+                      int64_t q_out_stride, int64_t k_out_stride, float base, int dtype,
+                      int idx_bits, jca_stream_t stream);
+
+int jca_rope_axes_bwd(const void* dq_out, const void* dk_out, void* dq, void* dk,
+                      const void* positions, const int32_t* sections, int n_axes, int per_axis,
+                      int64_t T, int H, int Hkv, int d_head, int64_t dq_out_stride,
+                      int64_t dk_out_stride, int64_t dq_stride, int64_t dk_stride, float base,
+                      int dtype, int idx_bits, jca_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Causal attention over long histories: a sliding window, and the first tokens of every row (the
+ * user prefix) that stay visible. Beside jagged_causal_attn_fwd, which is the case of a window as
+ * long as the row. Row i of user b (both counted from the row's start) sees the keys j <= i with
+ *   j > i - window  or  j < n_sinks,
+ * padding left out. Query heads share key heads: head h reads key head h / (H / Hkv).
+ *   q        [T, H, d_head] bf16, k and v [T, Hkv, d_head] bf16, read. Heads are packed; tokens are
+ *            q_stride / k_stride / v_stride elements apart (multiples of 8, >= heads * d_head).
+ *   out      [T, H, d_head] bf16, packed, written.
+ *   lse      [T, H] fp32 or NULL, written: the natural-log softmax denominator of every row and head
+ *            (-inf for a padding row), for the backward pass.
+ *   offsets  [B+1] (idx_bits type), read. offsets[0] = 0 and offsets[B] = T.
+ *   valid    [T] uint8 (1 = real token) or NULL (every token is real), read. A padding token is seen
+ *            by no row, its own output is 0, and its q, k and v may hold anything.
+ *   window   >= 1 (longer than every row: plain causal); 0 <= n_sinks <= 128.
+ *   scale    <= 0 selects 1/sqrt(d_head). H a multiple of Hkv.
+ *   workspace >= jca_window_workspace_bytes(...) bytes, 256-byte aligned, no part of it needs to
+ *            start at zero. Calls that may overlap on the GPU need a workspace each.
+ * Device errors: bad offsets -> JCA_STATUS_BAD_OFFSETS (nothing is written then);
+ * JCA_STATUS_TIMEOUT.
+ * ------------------------------------------------------------------------------------------- */
+size_t jca_window_workspace_bytes(int64_t B, int64_t T, int H, int Hkv, int d_head, int n_sinks);
+
+int jagged_window_attn_fwd(const void* q, const void* k, const void* v, void* out, float* lse,
+                           const void* offsets, const uint8_t* valid, int64_t B, int64_t T, int H,
+                           int Hkv, int d_head, int64_t window, int n_sinks, int64_t q_stride,
+                           int64_t k_stride, int64_t v_stride, float scale, int idx_bits,
+                           void* workspace, size_t workspace_bytes, int32_t* status,
+                           jca_stream_t stream);
+
+/* Gradients of jagged_window_attn_fwd for the upstream gradient dout, as jagged_cand_attn_bwd: with P
+ * the forward's probabilities, dV = P^T dO, dS = P * (dO V^T - rowsum(dO * O)), dQ = scale dS K,
+ * dK = scale dS^T Q, where dK and dV of a key head collect those of its query heads. Sums run in a
+ * fixed order, so equal calls give equal bits.
+ *   out, lse from the forward on the same inputs; dout [T, H, d_head] bf16, packed, read (rows of
+ *   padding may hold anything in out, dout and lse too).
+ *   dq [T, H, d_head], dk and dv [T, Hkv, d_head] bf16, packed, written: every row, 0 for padding.
+ *   workspace >= jca_window_bwd_workspace_bytes(...) bytes, 256-byte aligned.
+ * Other arguments and errors as the forward. */
+size_t jca_window_bwd_workspace_bytes(int64_t B, int64_t T, int H, int Hkv, int d_head, int n_sinks);
+
+int jagged_window_attn_bwd(const void* q, const void* k, const void* v, const void* out,
+                           const void* dout, const float* lse, void* dq, void* dk, void* dv,
+                           const void* offsets, const uint8_t* valid, int64_t B, int64_t T, int H,
+                           int Hkv, int d_head, int64_t window, int n_sinks, int64_t q_stride,
+                           int64_t k_stride, int64_t v_stride, float scale, int idx_bits,
+                           void* workspace, size_t workspace_bytes, int32_t* status,
+                           jca_stream_t stream);
+
+/* One new token per user over a cache, with the forward's mask: user b's region of the cache is rows
+ * [cache_offsets[b], cache_offsets[b+1]) and holds cache_len[b] tokens from its start. The call
+ * writes the new token's key and value behind them (row cache_offsets[b] + cache_len[b]) and
+ * attends from it: it sees itself, the window - 1 tokens before it and the first n_sinks tokens.
+ * cache_len is not changed: the caller counts.
+ *   q [B, H, d_head], k_new and v_new [B, Hkv, d_head] bf16, read; heads packed, users q_stride /
+ *     k_stride / v_stride elements apart.
+ *   k_cache, v_cache [R, Hkv, d_head] bf16, packed, read; one row per user written. Rows of a region
+ *     behind its tokens may hold anything and stay as they are.
+ *   out [B, H, d_head] bf16, packed, written.
+ *   cache_offsets [B+1] and cache_len [B] in the idx_bits type, read; cache_offsets never falls,
+ *     and lies in [0, R]. cache_len[b] = -1 marks an empty slot of the batch: out is 0 there and no
+ *     row is written.
+ *   window, n_sinks, scale as above, with any n_sinks >= 0.
+ * Device errors, each for its own user, whose rows are then not written while the other users' may
+ * be: cache_offsets that fall or leave [0, R] -> JCA_STATUS_BAD_OFFSETS; cache_len[b] < -1, or no room for
+ * the new token -> JCA_STATUS_BAD_LENGTH. */
+int jagged_window_decode_fwd(const void* q, const void* k_new, const void* v_new, void* k_cache,
+                             void* v_cache, void* out, const void* cache_offsets,
+                             const void* cache_len, int64_t B, int64_t R, int H, int Hkv,
+                             int d_head, int64_t window, int64_t n_sinks, int64_t q_stride,
+                             int64_t k_stride, int64_t v_stride, float scale, int idx_bits,
+                             int32_t* status, jca_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Candidates that are drafted token by token (items named by a few tokens each, or a drafted
+ * continuation to be checked): the candidate-only layer over trees. User b's candidate tokens
+ * [cand_offsets[b], cand_offsets[b+1]) form a forest; each token attends to the user's cached
+ * history, to its ancestors and to itself, and to nothing else. With every parent -1 this is
+ * cand_only_attn_fwd.
+ *   cand_q [Nc, H, d_head], own_k and own_v [Nc, Hkv, d_head] bf16, read; heads packed, tokens
+ *     q_stride / k_stride / v_stride elements apart. Head h reads key head h / (H / Hkv).
+ *   parent [Nc] int32, read: the parent's index in the user's run, before the token's own, or -1 for
+ *     a token that hangs on the history.
+ *   hist_k, hist_v [R, Hkv, d_head] bf16, packed, read: user b's region is rows [hist_offsets[b],
+ *     hist_offsets[b+1]) of it, of which the first hist_len[b] hold its history (hist_len NULL: the
+ *     whole region). Rows behind them may hold anything.
+ *   out [Nc, H, d_head] bf16, packed, written.
+ *   cand_offsets, hist_offsets [B+1], hist_len [B] in the idx_bits type, read; cand_offsets starts
+ *     at 0 and ends at Nc, hist_offsets never falls and lies in [0, R].
+ *   max_cand: no run is longer; 1 <= max_cand <= 1024. scale <= 0 selects 1/sqrt(d_head).
+ * Device errors, each for its own user, whose rows are then not written while the other users' may
+ * be: bad offsets -> JCA_STATUS_BAD_OFFSETS; hist_len[b] outside
+ * its region -> JCA_STATUS_BAD_LENGTH; a bad parent or a run longer than max_cand ->
+ * JCA_STATUS_BAD_TREE. No workspace.
+ * ------------------------------------------------------------------------------------------- */
+int cand_tree_attn_fwd(const void* cand_q, const void* own_k, const void* own_v,
+                       const void* cand_offsets, const int32_t* parent, const void* hist_k,
+                       const void* hist_v, const void* hist_offsets, const void* hist_len,
+                       void* out, int64_t B, int64_t Nc, int64_t R, int H, int Hkv, int d_head,
+                       int max_cand, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                       float scale, int idx_bits, int32_t* status, jca_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,669 @@
+"""GPU parity of the long-history operators against oracle/long_history.py (fp64).
+
+Tolerances, stated per element from the rounding points (half a bf16 step is 2^-8 of the value):
+* attention: the weights P enter the value product as bf16, which spreads to 2^-8 P|V|; the result
+  is rounded once, 2^-8 |ref|; the fp32 scores, exponentials and sums take 2^-11 P|V| (a score of
+  128 products of magnitude up to a few tens carries at most about 128 2^-24 60 = 2^-11);
+* lse: 2^-11 on the scores as above, in fp32;
+* gradients: dS and P enter their products as bf16 (2^-8 |dS|), the forward's bf16 output enters
+  rowsum(dO * O) (2^-8 P |dO||O|), the result is rounded once, and the fp32 part takes 2^-11 of the
+  absolute terms before cancellation;
+* rotation: one rounding to the type, 2^-22 of the two terms for the fp32 sine, cosine and products
+  (each within 2^-23), summed over both.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import oracle.long_history as lh
+from candidate_isolated_jagged_b200 import jca
+from helpers import dev
+
+pytestmark = pytest.mark.gpu
+
+HALF = {torch.bfloat16: 2.0**-8, torch.float16: 2.0**-11, torch.float32: 2.0**-24}
+EDGES = [1, 5, 0, 17, 64, 127, 128, 129, 255, 256, 257, 300, 513, 2]
+
+
+def near(got, ref, tol, what):
+    got = got.double().cpu().numpy()
+    assert got.shape == ref.shape
+    assert np.all(np.isfinite(got)), f"{what}: not finite"
+    over = np.abs(got - ref) - tol
+    at = np.unravel_index(np.argmax(over), over.shape) if over.size else ()
+    assert over.size == 0 or over[at] <= 0, f"{what}: {got[at]} against {ref[at]} +- {tol[at]} at {at}"
+
+
+class Window:
+    """A batch for the windowed attention, on the GPU, and the oracle's view of it."""
+
+    def __init__(self, lengths, H, Hkv, d, seed=0, valid=None, idx=torch.int64, fused=False, junk=None):
+        g = torch.Generator().manual_seed(seed)
+        self.off_np = np.concatenate([[0], np.cumsum(lengths)]).astype(np.int64)
+        T = self.T = int(self.off_np[-1])
+        x = torch.randn(T, H + 2 * Hkv, d, generator=g).to(torch.bfloat16)
+        self.do = torch.randn(T, H, d, generator=g).to(torch.bfloat16)
+        self.valid_np = None if valid is None else np.asarray(valid, dtype=np.uint8)
+        self.valid = None
+        if valid is not None:
+            self.valid = torch.tensor(self.valid_np, device=dev())
+            if junk is not None:
+                x[self.valid_np == 0] = junk
+                self.do[self.valid_np == 0] = junk
+        self.H, self.Hkv, self.d, self.scale = H, Hkv, d, 1.0 / np.sqrt(d)
+        self.q_cpu, self.k_cpu, self.v_cpu = x.split([H, Hkv, Hkv], 1)
+        on = x.to(dev()).split([H, Hkv, Hkv], 1)
+        self.q, self.k, self.v = on if fused else [t.contiguous() for t in on]
+        self.dout = self.do.to(dev())
+        self.off = torch.tensor(self.off_np, dtype=idx, device=dev())
+        self.st = jca.new_status(dev())
+
+    def forward(self, window, sinks, lse=True, **kw):
+        self.out = torch.full((self.T, self.H, self.d), float("nan"), dtype=torch.bfloat16, device=dev())
+        self.lse = torch.full((self.T, self.H), float("nan"), device=dev()) if lse else None
+        jca.jagged_window_attn_fwd(self.q, self.k, self.v, self.out, self.off, window, sinks,
+                                   valid=self.valid, lse=self.lse, status=self.st, **kw)
+        return self.out
+
+    def users(self, window, sinks):
+        for s, e in zip(self.off_np[:-1], self.off_np[1:]):
+            if e > s:
+                va = None if self.valid_np is None else self.valid_np[s:e]
+                yield slice(int(s), int(e)), lh.window_mask(int(e - s), window, sinks, va)
+
+    def check_forward(self, window, sinks, what=""):
+        torch.cuda.synchronize()
+        jca.check_status(self.st, what)
+        for r, mask in self.users(window, sinks):
+            ref, lse, _, A = lh.masked(self.q_cpu[r], self.k_cpu[r], self.v_cpu[r], mask, self.scale)
+            near(self.out[r], ref, (2.0**-8 + 2.0**-11) * A + 2.0**-8 * np.abs(ref) + 1e-30, what)
+            if self.lse is not None:
+                live = mask.any(1)
+                got = self.lse[r].double().cpu().numpy()
+                assert np.all(got[~live] == -np.inf), what
+                assert np.max(np.abs(got[live] - lse[live]), initial=0.0) <= 2.0**-11, what
+
+    def backward(self, window, sinks, **kw):
+        """The gradients for the oracle's output and log-sum-exp, rounded to the stored types."""
+        out = np.zeros((self.T, self.H, self.d))
+        lse = np.full((self.T, self.H), -np.inf)
+        for r, mask in self.users(window, sinks):
+            out[r], lse[r], _, _ = lh.masked(self.q_cpu[r], self.k_cpu[r], self.v_cpu[r], mask, self.scale)
+        self.out = torch.tensor(out).to(torch.bfloat16).to(dev())
+        self.lse = torch.tensor(lse).float().to(dev())
+        if self.valid_np is not None:
+            self.out[self.valid == 0] = float("nan")
+            self.lse[self.valid == 0] = float("nan")
+        n = dict(dtype=torch.bfloat16, device=dev())
+        self.grads = [torch.full((self.T, h, self.d), float("nan"), **n) for h in (self.H, self.Hkv, self.Hkv)]
+        jca.jagged_window_attn_bwd(self.q, self.k, self.v, self.out, self.dout, self.lse, *self.grads,
+                                   self.off, window, sinks, valid=self.valid, status=self.st, **kw)
+        return self.grads
+
+    def check_backward(self, window, sinks, what=""):
+        torch.cuda.synchronize()
+        jca.check_status(self.st, what)
+        for r, mask in self.users(window, sinks):
+            ref, tol = lh.gradients(self.q_cpu[r], self.k_cpu[r], self.v_cpu[r], self.do[r], mask, self.scale)
+            for name, got, x, (soft, hard) in zip(("dq", "dk", "dv"), self.grads, ref, tol):
+                near(got[r], x, 2.0**-8 * soft + 2.0**-11 * hard + 2.0**-8 * np.abs(x) + 1e-30,
+                     f"{what} {name}")
+
+
+# ------------------------------------------------------------------------------------------------
+# Windowed attention
+# ------------------------------------------------------------------------------------------------
+
+WINDOWS = [(1, 0), (1, 3), (2, 1), (40, 0), (100, 4), (128, 128), (129, 16), (1 << 40, 0), (300, 1)]
+
+
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("window,sinks", WINDOWS)
+def test_window_forward_edges(d, window, sinks):
+    b = Window(EDGES, 2, 2, d, seed=d)
+    b.forward(window, sinks)
+    b.check_forward(window, sinks, f"d={d} w={window} s={sinks}")
+
+
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("window,sinks", WINDOWS)
+def test_window_backward_edges(d, window, sinks):
+    b = Window(EDGES, 2, 2, d, seed=d + 1)
+    b.backward(window, sinks)
+    b.check_backward(window, sinks, f"d={d} w={window} s={sinks}")
+
+
+@pytest.mark.parametrize("lengths", [[1], [1] * 300, [3, 2] * 90, [700], [0, 0, 5, 0], [2000]])
+@pytest.mark.parametrize("H,Hkv", [(4, 1), (6, 2)])
+def test_window_shapes(lengths, H, Hkv):
+    b = Window(lengths, H, Hkv, 32, seed=len(lengths), idx=torch.int32)
+    b.forward(70, 2)
+    b.check_forward(70, 2)
+    b.backward(70, 2)
+    b.check_backward(70, 2)
+
+
+@pytest.mark.parametrize("fill", [float("nan"), float("inf"), -3e38])
+@pytest.mark.parametrize("d", [16, 64, 128])
+def test_window_padding_holds_anything(d, fill):
+    """Padding in front, in holes, at the end, a user of padding alone; its q, k, v, dO, O and lse are
+    not finite."""
+    lengths = [40, 200, 16, 513, 130]
+    rng = np.random.default_rng(5)
+    valid = (rng.random(sum(lengths)) > 0.3).astype(np.uint8)
+    valid[:9] = 0
+    valid[240:256] = 0
+    valid[-70:] = 0
+    b = Window(lengths, 4, 2, d, seed=2, valid=valid, junk=fill)
+    out = b.forward(90, 5)
+    b.check_forward(90, 5)
+    assert bool((out[b.valid == 0] == 0).all())
+    grads = b.backward(90, 5)
+    b.check_backward(90, 5)
+    for g in grads:
+        assert bool((g[b.valid == 0] == 0).all())
+
+
+def test_window_fused_projection_rows():
+    b = Window([100, 31, 260], 4, 2, 64, seed=3, fused=True)
+    assert not b.q.is_contiguous()
+    b.forward(50, 3)
+    b.check_forward(50, 3)
+    b.backward(50, 3)
+    b.check_backward(50, 3)
+
+
+def test_window_as_long_as_the_row_is_the_causal_layer():
+    b = Window([300, 7, 129, 650], 4, 4, 128, seed=4)
+    got = b.forward(650, 0, lse=False)
+    ref = torch.empty_like(got)
+    st = jca.new_status(dev())
+    jca.jagged_causal_attn_fwd(b.q, b.k, b.v, ref, b.off, status=st)
+    jca.check_status(st)
+    torch.testing.assert_close(got.float(), ref.float(), atol=3e-2, rtol=2.0**-6)
+
+
+def test_window_scale_and_equal_bits():
+    b = Window([90, 400], 2, 1, 64, seed=6)
+    b.scale = 0.05
+    b.forward(64, 2, scale=0.05)
+    b.check_forward(64, 2)
+    g1 = [g.clone() for g in b.backward(64, 2, scale=0.05)]
+    b.check_backward(64, 2)
+    for _ in range(3):
+        for x, y in zip(g1, b.backward(64, 2, scale=0.05)):
+            assert torch.equal(x, y)
+
+
+def test_window_large_scores():
+    """Scores of some hundreds: the running maximum moves by more than any rescaling threshold."""
+    b = Window([400, 30], 2, 2, 64, seed=7)
+    ramp = torch.linspace(0.05, 6.0, b.T)[:, None, None]
+    b.k_cpu = (b.k_cpu.float() * ramp).to(torch.bfloat16)
+    b.k = b.k_cpu.to(dev())
+    b.forward(1000, 0, lse=False)
+    torch.cuda.synchronize()
+    # a score of 64 products of magnitude up to 6 * 4 * 4 carries up to 64 2^-24 100 = 2^-11 as well
+    b.check_forward(1000, 0)
+    b.backward(1000, 0)
+    b.check_backward(1000, 0)
+
+
+def test_window_empty_batches():
+    for lengths in ([], [0], [0, 0, 0]):
+        b = Window(lengths, 2, 2, 16)
+        b.forward(4, 1)
+        b.backward(4, 1)
+        torch.cuda.synchronize()
+        jca.check_status(b.st)
+
+
+@pytest.mark.parametrize("off", [[0, 10, 9], [1, 5, 13], [0, 5, 12], [0, -3, 13], [0, 5, 1 << 40]])
+def test_window_bad_offsets_write_nothing(off):
+    b = Window([4, 9], 2, 2, 16)
+    b.off = torch.tensor(off, device=dev())
+    out = torch.full((13, 2, 16), 7.0, dtype=torch.bfloat16, device=dev())
+    lse = torch.full((13, 2), 7.0, device=dev())
+    grads = [torch.full_like(out, 7.0) for _ in range(3)]
+    jca.jagged_window_attn_fwd(b.q, b.k, b.v, out, b.off, 4, 1, lse=lse, status=b.st)
+    torch.cuda.synchronize()
+    assert int(b.st.item()) == 2
+    st = jca.new_status(dev())
+    jca.jagged_window_attn_bwd(b.q, b.k, b.v, out, out, lse, *grads, b.off, 4, 1, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 2
+    for x in [out, lse] + grads:
+        assert bool((x == 7.0).all())
+
+
+def test_window_captured_and_replayed_with_an_eager_call_between():
+    """One graph of forward and backward, replayed on new inputs; an eager call of another batch
+    with its own workspace runs between the replays."""
+    b = Window([200, 33, 300], 4, 2, 64, seed=8)
+    other = Window([77, 500], 4, 2, 64, seed=9)
+    ws = torch.empty(jca.jca_window_workspace_bytes(3, b.T, 4, 2, 64, 2), dtype=torch.uint8, device=dev())
+    wb = torch.empty(jca.jca_window_bwd_workspace_bytes(3, b.T, 4, 2, 64, 2), dtype=torch.uint8, device=dev())
+    out, lse = torch.empty_like(b.q), torch.empty(b.T, 4, device=dev())
+    grads = [torch.empty_like(x) for x in (b.q, b.k, b.v)]
+
+    def step():
+        jca.jagged_window_attn_fwd(b.q, b.k, b.v, out, b.off, 60, 2, lse=lse, workspace=ws, status=b.st)
+        jca.jagged_window_attn_bwd(b.q, b.k, b.v, out, b.dout, lse, *grads, b.off, 60, 2, workspace=wb,
+                                   status=b.st)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (1, 2):
+        g = torch.Generator().manual_seed(seed)
+        for x in (b.q, b.k, b.v, b.dout):
+            x.copy_(torch.randn(x.shape, generator=g).to(torch.bfloat16))
+        other.forward(60, 2)
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = [x.clone() for x in [out, lse] + grads]
+        step()
+        torch.cuda.synchronize()
+        for x, y in zip(kept, [out, lse] + grads):
+            assert torch.equal(x, y)
+    other.check_forward(60, 2)
+
+
+def test_window_two_streams():
+    batches = [Window([150, 420, 64], 4, 4, 64, seed=s) for s in (11, 12)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in batches]
+    for _ in range(3):
+        for b, s in zip(batches, streams):
+            with torch.cuda.stream(s):
+                b.forward(100, 4)
+    torch.cuda.synchronize()
+    for b in batches:
+        b.check_forward(100, 4)
+
+
+def test_window_rows_beyond_32_bit_offsets():
+    """2^31 elements and more in q and out; sampled users at both ends."""
+    lengths = [1000] * 1050
+    H, d = 16, 128
+    T = sum(lengths)
+    assert T * H * d > 2**31
+    off = torch.arange(1051, device=dev()) * 1000
+    g = torch.Generator(device=dev()).manual_seed(0)
+    q = torch.empty(T, H, d, dtype=torch.bfloat16, device=dev()).normal_(generator=g)
+    k, v = (torch.empty(T, 1, d, dtype=torch.bfloat16, device=dev()).normal_(generator=g) for _ in range(2))
+    out, lse, st = torch.empty_like(q), torch.empty(T, H, device=dev()), jca.new_status(dev())
+    jca.jagged_window_attn_fwd(q, k, v, out, off, 64, 4, lse=lse, status=st)
+    jca.check_status(st)
+    mask, ends = lh.window_mask(1000, 64, 4), [slice(0, 1000), slice(T - 1000, T)]
+    for r in ends:
+        ref, _, _, A = lh.masked(q[r], k[r], v[r], mask, d**-0.5)
+        near(out[r], ref, (2.0**-8 + 2.0**-11) * A + 2.0**-8 * np.abs(ref), f"rows {r}")
+        out[r] = torch.tensor(ref).to(torch.bfloat16)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    jca.jagged_window_attn_bwd(q, k, v, out, q, lse, dq, dk, dv, off, 64, 4, status=st)
+    jca.check_status(st)
+    for r in ends:
+        ref, tol = lh.gradients(q[r], k[r], v[r], q[r], mask, d**-0.5)
+        for name, got, x, (soft, hard) in zip(("dq", "dk", "dv"), (dq, dk, dv), ref, tol):
+            near(got[r], x, 2.0**-8 * soft + 2.0**-11 * hard + 2.0**-8 * np.abs(x), f"rows {r} {name}")
+
+
+# ------------------------------------------------------------------------------------------------
+# One token over a cache
+# ------------------------------------------------------------------------------------------------
+
+class Decode:
+    def __init__(self, lens, caps, H, Hkv, d, seed=0, idx=torch.int64, junk=float("nan"), spare=3):
+        g = torch.Generator().manual_seed(seed)
+        self.lens, B = list(lens), len(lens)
+        self.off_np = np.concatenate([[0], np.cumsum(caps)]).astype(np.int64)
+        R = int(self.off_np[-1]) + spare
+        self.q_cpu, self.kn_cpu, self.vn_cpu = (torch.randn(B, h, d, generator=g).to(torch.bfloat16)
+                                                for h in (H, Hkv, Hkv))
+        self.kc_cpu, self.vc_cpu = (torch.randn(R, Hkv, d, generator=g).to(torch.bfloat16) for _ in range(2))
+        used = np.zeros(R, bool)
+        for b, n in enumerate(self.lens):
+            used[self.off_np[b]:self.off_np[b] + max(n, 0)] = True
+        self.kc_cpu[~used] = junk
+        self.vc_cpu[~used] = junk
+        to = lambda x: x.to(dev())                                  # noqa: E731
+        self.q, self.kn, self.vn = to(self.q_cpu), to(self.kn_cpu), to(self.vn_cpu)
+        self.kc, self.vc = to(self.kc_cpu), to(self.vc_cpu)
+        self.off = torch.tensor(self.off_np, dtype=idx, device=dev())
+        self.len = torch.tensor(self.lens, dtype=idx, device=dev())
+        self.out = torch.full((B, H, d), float("nan"), dtype=torch.bfloat16, device=dev())
+        self.scale, self.st = d**-0.5, jca.new_status(dev())
+
+    def run(self, window, sinks):
+        jca.jagged_window_decode_fwd(self.q, self.kn, self.vn, self.kc, self.vc, self.out, self.off, self.len,
+                                     window, sinks, status=self.st)
+
+    def check(self, window, sinks):
+        torch.cuda.synchronize()
+        jca.check_status(self.st)
+        kc, vc = self.kc_cpu.clone(), self.vc_cpu.clone()
+        for b, p in enumerate(self.lens):
+            if p < 0:
+                assert bool((self.out[b] == 0).all())
+                continue
+            s = int(self.off_np[b])
+            kc[s + p], vc[s + p] = self.kn_cpu[b], self.vn_cpu[b]
+            mask = lh.window_mask(p + 1, window, sinks)[-1:]
+            ref, _, _, A = lh.masked(self.q_cpu[b:b + 1], kc[s:s + p + 1], vc[s:s + p + 1], mask, self.scale)
+            near(self.out[b:b + 1], ref, (2.0**-8 + 2.0**-11) * A + 2.0**-8 * np.abs(ref) + 1e-30, f"user {b}")
+        for got, want in ((self.kc, kc), (self.vc, vc)):     # every other row as it was, bit for bit
+            assert torch.equal(got.cpu().view(torch.int16), want.view(torch.int16))
+
+
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (8, 2), (16, 1), (40, 2), (3, 1)])
+def test_decode_edges(d, H, Hkv):
+    lens = [0, 1, 15, 16, 17, -1, 63, 64, 65, 127, 128, 129, 300, 1000]
+    for window, sinks in ((1, 0), (2, 5), (64, 4), (100, 0), (1 << 40, 0), (17, 500)):
+        b = Decode(lens, [max(n, 0) + 1 + (i % 3) for i, n in enumerate(lens)], H, Hkv, d, seed=d)
+        b.run(window, sinks)
+        b.check(window, sinks)
+
+
+@pytest.mark.parametrize("n", [0, 5, 130, 5000, 20000])
+def test_decode_one_user(n):
+    b = Decode([n], [n + 1], 8, 8, 128, seed=n, idx=torch.int32, spare=0)
+    b.run(1 << 20, 0)
+    b.check(1 << 20, 0)
+    b = Decode([n], [n + 9], 8, 2, 64, seed=n)
+    b.run(4000, 4)
+    b.check(4000, 4)
+
+
+def test_decode_strided_rows():
+    b = Decode([30, 7, 90], [40, 40, 100], 4, 2, 64, seed=1)
+    x = torch.cat([b.q, b.kn, b.vn], 1)
+    b.q, b.kn, b.vn = x.split([4, 2, 2], 1)
+    b.run(20, 3)
+    b.check(20, 3)
+
+
+def test_decode_follows_the_forward():
+    """A row's tokens decoded one after another give the rows of the forward."""
+    w = Window([70], 4, 2, 64, seed=5)
+    w.forward(16, 3)
+    kc, vc = (torch.full((75, 2, 64), float("nan"), dtype=torch.bfloat16, device=dev()) for _ in range(2))
+    off, n = torch.tensor([2, 74], device=dev()), torch.zeros(1, dtype=torch.int64, device=dev())
+    out, st = torch.empty(1, 4, 64, dtype=torch.bfloat16, device=dev()), jca.new_status(dev())
+    rows = []
+    for i in range(70):
+        jca.jagged_window_decode_fwd(w.q[i:i + 1], w.k[i:i + 1], w.v[i:i + 1], kc, vc, out, off, n, 16, 3, status=st)
+        rows.append(out.clone())
+        n += 1
+    jca.check_status(st)
+    w.out = torch.cat(rows)
+    w.lse = None
+    w.check_forward(16, 3)
+    assert torch.equal(kc[2:72], w.k) and torch.equal(vc[2:72], w.v)
+
+
+def test_decode_bad_users_leave_the_others():
+    b = Decode([5, 6, 7], [8, 8, 8], 2, 2, 16, seed=2)
+    for off, n, code in (([0, 8, 4, 24], [5, 6, 7], 2), ([0, 8, 16, 28], [5, 6, 7], 2), ([-8, 8, 16, 24], [5, 6, 7], 2),
+                         ([0, 8, 16, 24], [5, 8, 7], 1), ([0, 8, 16, 24], [5, -2, 7], 1)):
+        b.off, b.len = torch.tensor(off, device=dev()), torch.tensor(n, device=dev())
+        st = jca.new_status(dev())
+        kc = b.kc.clone()
+        out = torch.full_like(b.out, 7.0)
+        jca.jagged_window_decode_fwd(b.q, b.kn, b.vn, kc, b.vc, out, b.off, b.len, 4, 1, status=st)
+        torch.cuda.synchronize()
+        assert int(st.item()) == code
+        bad = [u for u in range(3) if not (0 <= off[u] <= off[u + 1] <= 27 and -1 <= n[u] < off[u + 1] - off[u])]
+        assert bool((out[bad] == 7.0).all())
+
+
+# ------------------------------------------------------------------------------------------------
+# Trees of drafted tokens
+# ------------------------------------------------------------------------------------------------
+
+class Tree:
+    def __init__(self, counts, hist, H, Hkv, d, seed=0, idx=torch.int64, shape="random", hist_len=None):
+        g = torch.Generator().manual_seed(seed)
+        rng = np.random.default_rng(seed)
+        self.counts, self.hist = counts, hist
+        self.use = list(hist if hist_len is None else hist_len)
+        N, R = sum(counts), sum(hist) + 5
+        self.coff = np.concatenate([[0], np.cumsum(counts)]).astype(np.int64)
+        self.hoff = np.concatenate([[0], np.cumsum(hist)]).astype(np.int64)
+        self.cpu = [torch.randn(N, h, d, generator=g).to(torch.bfloat16) for h in (H, Hkv, Hkv)]
+        self.cache = [torch.randn(R, Hkv, d, generator=g).to(torch.bfloat16) for _ in range(2)]
+        used = np.zeros(R, bool)
+        for b, n in enumerate(self.use):
+            used[self.hoff[b]:self.hoff[b] + n] = True
+        for x in self.cache:
+            x[~used] = float("nan")
+        par = []
+        for n in counts:
+            i = np.arange(n)
+            if shape == "chain":
+                par.append(i - 1)
+            elif shape == "star":
+                par.append(np.full(n, -1))
+            else:
+                par.append(np.array([rng.integers(-1, t) if t else -1 for t in range(n)], dtype=np.int64))
+        self.par = par
+        self.parent = torch.tensor(np.concatenate(par) if par else [], dtype=torch.int32, device=dev())
+        self.q, self.k, self.v = (x.to(dev()) for x in self.cpu)
+        self.hk, self.hv = (x.to(dev()) for x in self.cache)
+        self.off, self.ho = (torch.tensor(x, dtype=idx, device=dev()) for x in (self.coff, self.hoff))
+        self.hl = None if hist_len is None else torch.tensor(hist_len, dtype=idx, device=dev())
+        self.out = torch.full((N, H, d), float("nan"), dtype=torch.bfloat16, device=dev())
+        self.scale, self.st = d**-0.5, jca.new_status(dev())
+
+    def run(self, max_cand=None):
+        jca.cand_tree_attn_fwd(self.q, self.k, self.v, self.off, self.parent, self.hk, self.hv, self.ho, self.out,
+                               max_cand or max(max(self.counts), 1), hist_len=self.hl, status=self.st)
+
+    def check(self):
+        torch.cuda.synchronize()
+        jca.check_status(self.st)
+        for b, n in enumerate(self.counts):
+            if n == 0:
+                continue
+            c, h0 = slice(int(self.coff[b]), int(self.coff[b + 1])), int(self.hoff[b])
+            k, v = (torch.cat([x[h0:h0 + self.use[b]], y[c]]) for x, y in zip(self.cache, self.cpu[1:]))
+            ref, _, _, A = lh.masked(self.cpu[0][c], k, v, lh.tree_mask(self.par[b], self.use[b]), self.scale)
+            near(self.out[c], ref, (2.0**-8 + 2.0**-11) * A + 2.0**-8 * np.abs(ref) + 1e-30, f"user {b}")
+
+
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (8, 2), (5, 1), (16, 1), (40, 1)])
+def test_tree_edges(d, H, Hkv):
+    b = Tree([1, 0, 7, 16, 17, 33, 64, 65, 3], [0, 12, 1, 63, 64, 65, 130, 300, 128], H, Hkv, d, seed=d)
+    b.run()
+    b.check()
+
+
+@pytest.mark.parametrize("shape", ["chain", "star", "random"])
+def test_tree_large(shape):
+    b = Tree([1024, 700], [40, 0], 2, 1, 64, seed=1, shape=shape, idx=torch.int32)
+    b.run()
+    b.check()
+
+
+def test_tree_long_history_of_one_user():
+    b = Tree([9], [6000], 8, 8, 128, seed=2)
+    b.run(64)
+    b.check()
+
+
+def test_tree_regions_with_room():
+    b = Tree([5, 12, 4], [100, 70, 40], 8, 4, 128, seed=3, hist_len=[64, 0, 39])
+    b.run()
+    b.check()
+
+
+def test_tree_strided_rows_and_graph():
+    b = Tree([9, 20], [200, 77], 4, 2, 64, seed=4)
+    x = torch.cat([b.q, b.k, b.v], 1)
+    b.q, b.k, b.v = x.split([4, 2, 2], 1)
+    b.run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.run()
+    b.out.fill_(float("nan"))
+    graph.replay()
+    b.check()
+
+
+def test_star_tree_is_the_candidate_only_layer():
+    b = Tree([40, 3, 100], [90, 500, 17], 4, 4, 64, seed=6, shape="star")
+    b.run()
+    out = torch.empty_like(b.out)
+    st = jca.new_status(dev())
+    jca.cand_only_attn_fwd(b.q, b.k, b.v, b.off, b.hk[:607], b.hv[:607], b.ho, out, status=st)
+    jca.check_status(st)
+    b.check()
+    torch.testing.assert_close(b.out.float(), out.float(), atol=3e-2, rtol=2.0**-6)
+
+
+def test_tree_bad_users_leave_the_others():
+    def code(**kw):
+        b = Tree([4, 6, 3], [20, 30, 10], 2, 2, 16, seed=5, hist_len=[20, 30, 10])
+        b.out.fill_(7.0)
+        for name, (i, x) in kw.items():
+            getattr(b, name)[i] = x
+        b.run(6)
+        torch.cuda.synchronize()
+        assert bool((b.out[4:10] == 7.0).all())
+        return int(b.st.item())
+
+    assert code(parent=(4, 0)) == 8            # its own parent
+    assert code(parent=(6, 3)) == 8            # a later token
+    assert code(parent=(9, -2)) == 8
+    assert code(hl=(1, 31)) == 1
+    assert code(hl=(1, -1)) == 1
+    assert code(ho=(2, 200)) == 2
+    assert code(off=(1, 11)) == 2
+    b = Tree([4, 6, 3], [20, 30, 10], 2, 2, 16, seed=5)
+    b.out.fill_(7.0)
+    b.run(5)                                   # a run longer than max_cand
+    torch.cuda.synchronize()
+    assert int(b.st.item()) == 8 and bool((b.out[4:10] == 7.0).all())
+
+
+# ------------------------------------------------------------------------------------------------
+# Rotary positions with several axes
+# ------------------------------------------------------------------------------------------------
+
+def _rope_check(x, got, pos, sections, per_axis, sign, what, base=10000.0):
+    ref = lh.rope_axes(x, pos, sections, base, per_axis, sign)
+    a = np.abs(lh.f64(x))
+    half = a.shape[2] // 2
+    both = np.concatenate([a[..., :half] + a[..., half:]] * 2, -1)
+    near(got, ref, HALF[x.dtype] * np.abs(ref) + 2.0**-22 * both + 1e-30, what)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("d,sections", [(16, [8]), (16, [3, 2, 2]), (32, [0, 16]), (64, [9, 10, 10]),
+                                        (128, [16, 24, 24]), (128, [1, 0, 20, 30]), (128, [0])])
+def test_rope_axes(dtype, d, sections):
+    g = torch.Generator().manual_seed(d)
+    T, A = 77, len(sections)
+    q, k = torch.randn(T, 5, d, generator=g).to(dtype), torch.randn(T, 2, d, generator=g).to(dtype)
+    pos = torch.randint(-40, 5000, (T, A), generator=g)
+    pos[:, -1] = torch.randint(1 << 30, 1 << 31, (T,), generator=g) - (1 << 20)    # seconds since an epoch
+    for per_axis in (False, True):
+        for idx in (torch.int32, torch.int64):
+            for fn, sign in ((jca.jca_rope_axes_fwd, 1.0), (jca.jca_rope_axes_bwd, -1.0)):
+                qo, ko = torch.empty_like(q, device=dev()), torch.empty_like(k, device=dev())
+                p = pos.to(idx).to(dev())
+                fn(q.to(dev()), k.to(dev()), qo, ko, p, sections, per_axis=per_axis)
+                _rope_check(q, qo, pos, sections, per_axis, sign, "q")
+                _rope_check(k, ko, pos, sections, per_axis, sign, "k")
+
+
+def test_rope_axes_in_place_strided_and_alone():
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(200, 8, 64, generator=g).to(torch.bfloat16)
+    pos = torch.randint(0, 4096, (200, 2), generator=g)
+    y = x.to(dev())
+    q, k = y[:, :4], y[:, 4:6]
+    jca.jca_rope_axes_fwd(q, k, q, k, pos.to(dev()), [20, 8])
+    _rope_check(x[:, :4], q, pos, [20, 8], False, 1.0, "q")
+    _rope_check(x[:, 4:6], k, pos, [20, 8], False, 1.0, "k")
+    assert torch.equal(y[:, 6:].cpu(), x[:, 6:])
+    alone = torch.empty(200, 4, 64, dtype=torch.bfloat16, device=dev())
+    jca.jca_rope_axes_fwd(x.to(dev())[:, :4], None, alone, None, pos.to(dev()), [20, 8])
+    assert torch.equal(alone, q)
+
+
+def test_rope_one_axis_is_jca_apply_rope():
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(300, 3, 128, generator=g).to(torch.bfloat16).to(dev())
+    pos = torch.randint(0, 4096, (300,), generator=g).to(torch.int32).to(dev())
+    a, b = torch.empty_like(x), torch.empty_like(x)
+    jca.jca_apply_rope(x, a, pos)
+    jca.jca_rope_axes_fwd(x, None, b, None, pos, [64])
+    torch.testing.assert_close(a.float(), b.float(), atol=1e-5, rtol=2.0**-7)
+
+
+def test_rope_other_pairs_hold_anything():
+    """Pairs past the sections are copied bit for bit, whatever they hold."""
+    x = torch.randn(9, 2, 32).to(torch.bfloat16)
+    x[..., 10:16] = float("inf")
+    x[..., 26:32] = float("nan")
+    y = torch.empty_like(x, device=dev())
+    jca.jca_rope_axes_fwd(x.to(dev()), None, y, None, torch.arange(18, device=dev()).view(9, 2), [5, 5])
+    got = y.cpu()
+    keep = list(range(10, 16)) + list(range(26, 32))
+    assert torch.equal(got[..., keep].view(torch.int16), x[..., keep].view(torch.int16))
+    assert bool(torch.isfinite(got[..., :10].float()).all())
+
+
+# ------------------------------------------------------------------------------------------------
+# Together
+# ------------------------------------------------------------------------------------------------
+
+def test_layer_of_a_training_step_and_its_serving():
+    """Rotation, windowed attention, its gradient and the rotation's, against the composed fp64
+    formulas; then the cache that serving builds from the same rows: prefill, decoded tokens, drafts."""
+    H, Hkv, d, W, S, sections = 4, 2, 64, 24, 2, [12, 10, 10]
+    lengths = [60, 9, 131]
+    b = Window(lengths, H, Hkv, d, seed=20)
+    g = torch.Generator().manual_seed(3)
+    pos = torch.randint(0, 3000, (b.T, 3), generator=g)
+    p = pos.to(dev())
+    qr, kr = torch.empty_like(b.q), torch.empty_like(b.k)
+    jca.jca_rope_axes_fwd(b.q, b.k, qr, kr, p, sections)
+    q0, k0 = b.q_cpu, b.k_cpu
+    b.q, b.k, b.q_cpu, b.k_cpu = qr, kr, qr.cpu(), kr.cpu()
+    _rope_check(q0, qr, pos, sections, False, 1.0, "q")
+    b.forward(W, S)
+    b.check_forward(W, S)
+    b.backward(W, S)
+    b.check_backward(W, S)
+    dq, dk = torch.empty_like(b.q), torch.empty_like(b.k)
+    jca.jca_rope_axes_bwd(b.grads[0], b.grads[1], dq, dk, p, sections)
+    _rope_check(b.grads[0].cpu(), dq, pos, sections, False, -1.0, "dq")
+    _rope_check(b.grads[1].cpu(), dk, pos, sections, False, -1.0, "dk")
+    # serving: every row but its last token is prefilled, the last is decoded
+    b.forward(W, S)
+    n = torch.tensor([x - 1 for x in lengths], device=dev())
+    last = (b.off[1:] - 1)
+    kc, vc = b.k.clone(), b.v.clone()
+    kc[last], vc[last] = float("nan"), float("nan")
+    out, st = torch.empty(3, H, d, dtype=torch.bfloat16, device=dev()), jca.new_status(dev())
+    jca.jagged_window_decode_fwd(b.q[last], b.k[last], b.v[last], kc, vc, out, b.off, n, W, S, status=st)
+    jca.check_status(st)
+    assert torch.equal(kc, b.k) and torch.equal(vc, b.v)
+    torch.testing.assert_close(out.float(), b.out[last].float(), atol=3e-2, rtol=2.0**-6)
+    # drafts over the same cache: a chain is a causal continuation of it
+    t = Tree([5, 5, 5], lengths, H, Hkv, d, seed=21, shape="chain")
+    t.hk[: b.T], t.hv[: b.T] = kc, vc
+    t.cache[0][: b.T], t.cache[1][: b.T] = kc.cpu(), vc.cpu()
+    t.run()
+    t.check()
