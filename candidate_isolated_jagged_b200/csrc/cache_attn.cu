@@ -1,10 +1,32 @@
 // Attention of a few new tokens per user over the user's cached history: one new token with a sliding
 // window and visible first tokens (jagged_window_decode_fwd), and a tree of drafted tokens
 // (cand_tree_attn_fwd); include/jca.h states both.
+//
+// Mathematics: softmax(scale q K^T) V over the list of keys a user's tokens see, with a running
+// maximum m and sum l in fp32 (p = 2^(s - m) in log2 units), so the keys are read once.
+//
+// What bounds it: reading the cache. A user's n tokens times the G = H / Hkv query heads of a key
+// head are the rows of one product against that head's keys, so a key's 4 d bytes (K and V) serve
+// n G rows. Up to 64 rows the product stays far below what the warp-level tensor instruction
+// (m16n8k16, fp32 accumulators in registers) does in the time the bytes take: 64 rows cost about 16
+// of the 22 cycles that a key of d = 128 takes an SM at the copy bandwidth. A 128-row tcgen05 tile
+// would leave half or more of its rows empty here and would have to mask the ends of the cache in
+// shared memory; with registers the copies zero-fill what lies behind the last key.
+//
+// Shape: a block of 4 warps takes up to 64 rows of one (user, key head) and walks 64-key tiles
+// through a ring of stages filled by 16-byte asynchronous copies. With 64 rows each warp owns 16 of
+// them and sees all 64 keys; with at most 16 rows (one token, shared heads) the four warps take 16
+// keys each and their partial results are joined at the end. When there are few (user, head) pairs,
+// the key list is split further over a cluster of up to 8 blocks, which join through distributed
+// shared memory in rank order: one launch, no workspace, equal bits for equal calls.
+// The keys of a tile that a copy does not reach (behind the list) are zeros, so whatever the cache
+// holds there never meets a weight.
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
 
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -14,9 +36,14 @@
 namespace jca {
 namespace {
 
+namespace cg = cooperative_groups;
 using bf16 = __nv_bfloat16;
 
 constexpr int kMaxTree = 1024;
+constexpr int kThr = 128;          // threads of a block
+constexpr int kBK = 64;            // keys of a tile
+constexpr int kMaxSplit = 8;       // blocks of a cluster
+constexpr int kTreeWords = kMaxTree / 32;
 
 struct CacheArgs {
   const bf16* q;
@@ -31,140 +58,479 @@ struct CacheArgs {
   const int32_t* parent;
   int32_t* status;
   int64_t B, N, R, window, n_sinks, q_stride, k_stride, v_stride;
-  int H, Hkv, max_cand;
-  float scale;
-};
-
-template <int D>
-struct Vecs {
-  static constexpr int EPL = D >= 32 ? D / 32 : 1;
-  float q[EPL], acc[EPL], m, l;
-  __device__ __forceinline__ void see(const bf16* k, const bf16* v, float scale, int lane) {
-    float s = 0.f;
-    if (lane * EPL < D)
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) s = fmaf(q[i], __bfloat162float(k[lane * EPL + i]), s);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= scale;
-    const float mn = fmaxf(m, s), al = m == -INFINITY ? 0.f : __expf(m - mn), p = __expf(s - mn);
-    if (lane * EPL < D)
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        acc[i] = fmaf(p, __bfloat162float(v[lane * EPL + i]), acc[i] * al);
-    l = l * al + p;
-    m = mn;
-  }
-  __device__ __forceinline__ void start(const bf16* p, int lane) {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      q[i] = lane * EPL < D ? __bfloat162float(p[lane * EPL + i]) : 0.f;
-      acc[i] = 0.f;
-    }
-    m = -INFINITY;
-    l = 0.f;
-  }
-  __device__ __forceinline__ void store(bf16* p, int lane) const {
-    if (lane * EPL < D)
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) p[lane * EPL + i] = __float2bfloat16(l > 0.f ? acc[i] / l : 0.f);
-  }
+  int H, Hkv, max_cand, row_blocks, split;
+  float scale_log2;
 };
 
 __device__ __forceinline__ void set_status(int32_t* status, int code) {
   atomicCAS(status, 0, (int32_t)code);
 }
 
-// One warp per (user, head).
-template <int D, typename IdxT>
-__global__ void __launch_bounds__(128) decode_kernel(const CacheArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t w = blockIdx.x * (int64_t)4 + (threadIdx.x >> 5);
-  if (w >= a.B * a.H || *a.status != 0) return;
-  const int64_t b = w / a.H;
-  const int h = (int)(w % a.H), G = a.H / a.Hkv, hk = h / G;
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool real) {
+  const int n = real ? 16 : 0;   // 0: the 16 bytes are zero-filled, nothing is read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+template <int D, int RW, bool TREE>
+struct CCfg {
+  static constexpr int CH = D / 8;                        // 16-byte chunks of a row
+  static constexpr int RB = 16 * RW;                      // rows of a block
+  static constexpr int KW = 4 / RW;                       // warps that share rows, by keys
+  static constexpr int KPW = kBK / KW;                    // keys of a tile per warp
+  static constexpr int TILE = kBK * D * 2;                // bytes of a K or V tile
+  static constexpr int STAGE = 2 * TILE;
+  static constexpr int STAGES = D == 128 ? 3 : 4;
+  static constexpr int OFF_ML = STAGES * STAGE;           // [KW][RB] m and l, then [RB] joined
+  static constexpr int OFF_BITS = OFF_ML + (2 * KW + 2) * RB * 4;
+  static constexpr int OFF_PAR = OFF_BITS + (TREE ? RB * kTreeWords * 4 : 0);
+  static constexpr int OFF_TILES = OFF_PAR + (TREE ? kMaxTree * 2 : 0);
+  static constexpr int SMEM = OFF_TILES + (TREE ? 128 : 16);
+  // Partial results [KW][RB][D] fp32 reuse the ring.
+  static_assert(KW * RB * D * 4 <= STAGES * STAGE, "partials fit the ring");
+  static_assert(RB * D * 2 <= STAGE, "Q fits one stage");
+  static_assert(SMEM <= 113 * 1024, "two blocks per SM");
+};
+
+// Shared-memory byte offset of chunk c of row r: chunks are XORed with the row so that eight rows'
+// chunks of one column fall into different banks.
+template <int D>
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  constexpr int CH = D / 8;
+  constexpr int RPL = CH >= 8 ? 1 : 8 / CH;               // rows of a 128-byte line
+  constexpr int MASK = (CH >= 8 ? 8 : CH) - 1;
+  return (uint32_t)(r * CH + (c ^ ((r / RPL) & MASK))) * 16u;
+}
+
+// The keys a block walks: rows of the cache and the new tokens' own rows.
+struct Keys {
+  int64_t base;       // first cache row of the list
+  int64_t base2;      // decode: first cache row behind the visible first tokens
+  int n1, n2;         // decode: first tokens, window tokens before the new one; tree: history, 0
+  int64_t own;        // first own row
+  int n_own;          // own rows
+  int own_tile;       // tree: first tile of own rows
+};
+
+template <int D, int RW, bool TREE, typename IdxT>
+__global__ void __launch_bounds__(kThr, 2) cache_attn_kernel(const CacheArgs a) {
+  using C = CCfg<D, RW, TREE>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const uint32_t sb = smem_u32(smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = (int)(blockIdx.x % (unsigned)a.split);
+  int64_t unit = blockIdx.x / (unsigned)a.split;
+  const int rb = (int)(unit % a.row_blocks);
+  unit /= a.row_blocks;
+  const int hk = (int)(unit % a.Hkv);
+  const int64_t b = unit / a.Hkv;
+  const int G = a.H / a.Hkv;
   const IdxT* off = static_cast<const IdxT*>(a.off);
-  const int64_t s = off[b], e = off[b + 1], p = static_cast<const IdxT*>(a.len)[b];
-  if (s < 0 || s > e || e > a.R) {
-    if (lane == 0) set_status(a.status, JCA_STATUS_BAD_OFFSETS);
-    return;
-  }
-  if (p < -1 || (p >= 0 && p >= e - s)) {
-    if (lane == 0) set_status(a.status, JCA_STATUS_BAD_LENGTH);
-    return;
-  }
-  Vecs<D> x;
-  x.start(a.q + b * a.q_stride + (int64_t)h * D, lane);
-  if (p >= 0) {
-    const bf16* kn = a.k + b * a.k_stride + (int64_t)hk * D;
-    const bf16* vn = a.v + b * a.v_stride + (int64_t)hk * D;
-    const int64_t lo = max((int64_t)0, p - a.window + 1), first = min(a.n_sinks, lo);
-    for (int64_t j = 0; j < p; ++j) {
-      if (j == first && first < lo) j = lo;
-      if (j >= p) break;
-      const int64_t at = ((s + j) * a.Hkv + hk) * D;
-      x.see(a.kc + at, a.vc + at, a.scale, lane);
+
+  // An error recorded earlier makes the call a no-op. Blocks of a cluster could see a status that
+  // another user's block sets meanwhile at different times, so a block that sees one keeps in step
+  // with its cluster and only tells the others, at the joining, that it has nothing to add.
+  const bool skip = __syncthreads_or(tid == 0 && *a.status != 0);
+  if (skip && a.split == 1) return;
+
+  // The user's keys and rows; every block of a user takes the same decisions.
+  Keys k;
+  int rows = 0;                       // rows of this block
+  int nt = 0;                         // key tiles
+  int64_t row0 = 0;                   // token of row 0 of the user in q
+  if constexpr (TREE) {
+    const IdxT* ho = static_cast<const IdxT*>(a.hist_off);
+    const int64_t s = off[b], e = off[b + 1], hs = ho[b], he = ho[b + 1];
+    int bad = 0;
+    int64_t hl = he - hs;
+    if (s < 0 || s > e || e > a.N || (b == 0 && s != 0) || (b == a.B - 1 && e != a.N) || hs < 0 ||
+        hs > he || he > a.R) {
+      bad = JCA_STATUS_BAD_OFFSETS;
+    } else if (e - s > a.max_cand) {
+      bad = JCA_STATUS_BAD_TREE;
+    } else if (a.len) {
+      hl = static_cast<const IdxT*>(a.len)[b];
+      if (hl < 0 || hl > he - hs) bad = JCA_STATUS_BAD_LENGTH;
     }
-    x.see(kn, vn, a.scale, lane);
-    if (h == hk * G && lane * Vecs<D>::EPL < D) {
-      const int64_t at = ((s + p) * a.Hkv + hk) * D;
+    const int n = bad ? 0 : (int)(e - s);
+    // Every block looks at all parents of its user, so that all of them see a bad one.
+    int16_t* par = reinterpret_cast<int16_t*>(smem + C::OFF_PAR);
+    int wrong = 0;
+    for (int i = tid; i < n; i += kThr) {
+      const int p = a.parent[s + i];
+      wrong |= p < -1 || p >= i;
+      par[i] = (int16_t)p;
+    }
+    if (__syncthreads_or(wrong)) bad = JCA_STATUS_BAD_TREE;
+    if (bad) {
+      if (tid == 0 && !skip) set_status(a.status, bad);
+      return;
+    }
+    rows = min(C::RB, n * G - rb * C::RB);
+    if (rows <= 0) return;
+    row0 = s;
+    k.base = hs;
+    k.n1 = (int)hl;
+    k.own = s;
+    k.n_own = n;
+    k.own_tile = (int)((hl + kBK - 1) / kBK);
+    // Ancestors of the block's tokens, a bit per drafted token, and the own tiles that hold any.
+    uint32_t* bits = reinterpret_cast<uint32_t*>(smem + C::OFF_BITS);
+    int* tiles = reinterpret_cast<int*>(smem + C::OFF_TILES);   // [16] tiles, [16] count, [17] flags
+    const int tok0 = rb * C::RB / G, ntok = (rb * C::RB + rows - 1) / G - tok0 + 1;
+    for (int i = tid; i < ntok * kTreeWords; i += kThr) bits[i] = 0;
+    if (tid == 0) tiles[17] = 0;
+    __syncthreads();
+    if (tid < ntok) {
+      int flags = 0;
+      for (int j = tok0 + tid; j >= 0; j = par[j]) {
+        bits[tid * kTreeWords + (j >> 5)] |= 1u << (j & 31);
+        flags |= 1 << (j / kBK);
+      }
+      atomicOr(&tiles[17], flags);
+    }
+    __syncthreads();
+    if (tid == 0) {
+      int c = 0;
+      for (int f = tiles[17]; f; f &= f - 1) tiles[c++] = __ffs(f) - 1;
+      tiles[16] = c;
+    }
+    __syncthreads();
+    nt = k.own_tile + tiles[16];
+  } else {
+    const int64_t s = off[b], e = off[b + 1], p = static_cast<const IdxT*>(a.len)[b];
+    int bad = 0;
+    if (s < 0 || s > e || e > a.R) bad = JCA_STATUS_BAD_OFFSETS;
+    else if (p < -1 || (p >= 0 && p >= e - s)) bad = JCA_STATUS_BAD_LENGTH;
+    if (bad) {
+      if (tid == 0 && !skip) set_status(a.status, bad);
+      return;
+    }
+    rows = min(C::RB, G - rb * C::RB);
+    row0 = b;
+    if (p < 0) {   // an empty slot of the batch
+      if (rank == 0 && !skip)
+        for (int i = tid; i < rows * C::CH; i += kThr)
+          reinterpret_cast<uint4*>(a.out + (b * a.H + (int64_t)hk * G + rb * C::RB) * D)[i] =
+              make_uint4(0u, 0u, 0u, 0u);
+      return;
+    }
+    const int64_t lo = max((int64_t)0, p - a.window + 1);
+    k.n1 = (int)min(a.n_sinks, lo);
+    k.n2 = (int)(p - lo);
+    k.base = s;
+    k.base2 = s + lo;
+    k.own = b;
+    k.n_own = 1;
+    nt = (k.n1 + k.n2 + 1 + kBK - 1) / kBK;
+    // The new token's key and value go behind the cached ones; no block reads them from there.
+    if (rank == 0 && rb == 0 && !skip && tid < 2 * C::CH) {
+      const int c = tid % C::CH;
+      const bool is_k = tid < C::CH;
+      const bf16* src = is_k ? a.k + b * a.k_stride : a.v + b * a.v_stride;
+      bf16* dst = (is_k ? a.kc : a.vc) + ((s + p) * a.Hkv + hk) * D;
+      reinterpret_cast<uint4*>(dst)[c] = reinterpret_cast<const uint4*>(src + (int64_t)hk * D)[c];
+    }
+  }
+  const int per = (nt + a.split - 1) / a.split;
+  const int t0 = min(nt, rank * per), t1 = skip ? t0 : min(nt, t0 + per);
+
+  const int64_t cstride = (int64_t)a.Hkv * D, hoff = (int64_t)hk * D;
+  auto load_tile = [&](int t) {
+    const uint32_t st = sb + (uint32_t)(t - t0) % C::STAGES * C::STAGE;
+    const int c = tid % C::CH;
+#pragma unroll 4
+    for (int i = 0; i < C::CH / 2; ++i) {
+      const int r = tid / C::CH + i * (kThr / C::CH);
+      const bf16 *pk = a.k, *pv = a.v;
+      bool real;
+      if constexpr (TREE) {
+        if (t < k.own_tile) {
+          const int x = t * kBK + r;
+          real = x < k.n1;
+          const int64_t at = (k.base + x) * cstride + hoff;
+          if (real) pk = a.kc + at, pv = a.vc + at;
+        } else {
+          const int x = reinterpret_cast<const int*>(smem + C::OFF_TILES)[t - k.own_tile] * kBK + r;
+          real = x < k.n_own;
+          if (real) {
+            pk = a.k + (k.own + x) * a.k_stride + hoff;
+            pv = a.v + (k.own + x) * a.v_stride + hoff;
+          }
+        }
+      } else {
+        const int x = t * kBK + r;
+        real = x <= k.n1 + k.n2;
+        if (x < k.n1 + k.n2) {
+          const int64_t row = x < k.n1 ? k.base + x : k.base2 + (x - k.n1);
+          pk = a.kc + row * cstride + hoff;
+          pv = a.vc + row * cstride + hoff;
+        } else if (real) {
+          pk = a.k + k.own * a.k_stride + hoff;
+          pv = a.v + k.own * a.v_stride + hoff;
+        }
+      }
+      cp16(st + swz<D>(r, c), pk + (real ? c * 8 : 0), real);
+      cp16(st + C::TILE + swz<D>(r, c), pv + (real ? c * 8 : 0), real);
+    }
+  };
+
+  // Q through the last stage's memory into registers, behind it the first tiles.
+  const uint32_t q_at = sb + (C::STAGES - 1) * C::STAGE;
+  for (int i = tid; i < C::RB * C::CH; i += kThr) {
+    const int r = i / C::CH, c = i % C::CH, g = rb * C::RB + r;
+    const bool real = r < rows;
+    const bf16* src = real ? a.q + (row0 + g / G) * a.q_stride + (int64_t)(hk * G + g % G) * D + c * 8
+                           : a.q;
+    cp16(q_at + swz<D>(r, c), src, real);
+  }
+  cp_commit();
 #pragma unroll
-      for (int i = 0; i < Vecs<D>::EPL; ++i) {
-        a.kc[at + lane * Vecs<D>::EPL + i] = kn[lane * Vecs<D>::EPL + i];
-        a.vc[at + lane * Vecs<D>::EPL + i] = vn[lane * Vecs<D>::EPL + i];
+  for (int i = 0; i < C::STAGES - 1; ++i) {
+    if (t0 + i < t1) load_tile(t0 + i);
+    cp_commit();
+  }
+  cp_wait<C::STAGES - 1>();
+  __syncthreads();
+  const int wr = warp / C::KW, wk = warp % C::KW;   // row group and key group of the warp
+  uint32_t qf[D / 16][4];
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk)
+    ldsm4(q_at + swz<D>(wr * 16 + (lane & 15), 2 * kk + (lane >> 4)), qf[kk]);
+
+  float o[D / 8][4];
+#pragma unroll
+  for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  const int ra = wr * 16 + (lane >> 2);             // this thread's rows: ra and ra + 8
+
+  for (int t = t0; t < t1; ++t) {
+    cp_wait<C::STAGES - 2>();
+    __syncthreads();
+    if (t + C::STAGES - 1 < t1) load_tile(t + C::STAGES - 1);
+    cp_commit();
+    const uint32_t st = sb + (uint32_t)(t - t0) % C::STAGES * C::STAGE;
+    // S = Q K^T of the warp's keys, 16 at a time.
+    float s[C::KPW / 8][4];
+#pragma unroll
+    for (int n = 0; n < C::KPW / 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+    for (int n = 0; n < C::KPW / 16; ++n) {
+      const int key = wk * C::KPW + n * 16 + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t f[4];
+        ldsm4(st + swz<D>(key, 2 * kk + ((lane >> 3) & 1)), f);
+        mma16816(s[2 * n], qf[kk], f[0], f[1]);
+        mma16816(s[2 * n + 1], qf[kk], f[2], f[3]);
+      }
+    }
+    // Scores in log2 units; keys behind the list, and drafted tokens off the path, drop out.
+    const int col0 = wk * C::KPW + 2 * (lane & 3);  // this thread's columns: col0 + 8 n + {0, 1}
+    int limit = kBK;                                // visible columns of a tile of cached keys
+    uint64_t path[2] = {~0ull, ~0ull};
+    if constexpr (TREE) {
+      if (t < k.own_tile) {
+        limit = min(kBK, k.n1 - t * kBK);
+      } else {
+        const uint32_t* bits = reinterpret_cast<const uint32_t*>(smem + C::OFF_BITS);
+        const int w = 2 * reinterpret_cast<const int*>(smem + C::OFF_TILES)[t - k.own_tile];
+        const int tok0 = rb * C::RB / G;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int r = min(ra + 8 * h, rows - 1);
+          const uint32_t* x = bits + ((rb * C::RB + r) / G - tok0) * kTreeWords + w;
+          path[h] = (uint64_t)x[0] | ((uint64_t)x[1] << 32);
+        }
+      }
+    } else {
+      limit = min(kBK, k.n1 + k.n2 + 1 - t * kBK);
+    }
+    const bool whole = limit == kBK && (!TREE || t < k.own_tile);
+    float mx[2] = {m[0], m[1]};
+#pragma unroll
+    for (int n = 0; n < C::KPW / 8; ++n) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[n][j] *= a.scale_log2;
+        const int col = col0 + 8 * n + (j & 1);
+        if (!whole && (col >= limit || !((path[j >> 1] >> col) & 1))) s[n][j] = -INFINITY;
+        mx[j >> 1] = fmaxf(mx[j >> 1], s[n][j]);
+      }
+    }
+    float al[2], ref[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+      mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+      al[h] = m[h] == -INFINITY ? 0.f : fast_exp2(m[h] - mx[h]);
+      ref[h] = mx[h] == -INFINITY ? 0.f : mx[h];
+      m[h] = mx[h];
+      l[h] *= al[h];
+    }
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) {
+      o[n][0] *= al[0];
+      o[n][1] *= al[0];
+      o[n][2] *= al[1];
+      o[n][3] *= al[1];
+    }
+    // O += P V, P rounded to bf16 as the tensor instruction's operand; l sums it in fp32.
+#pragma unroll
+    for (int n = 0; n < C::KPW / 16; ++n) {
+      uint32_t p[4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float* x = s[2 * n + j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = fast_exp2(x[i] - ref[i >> 1]);
+        l[0] += x[0] + x[1];
+        l[1] += x[2] + x[3];
+        p[2 * j] = pack_bf16x2(x[0], x[1]);
+        p[2 * j + 1] = pack_bf16x2(x[2], x[3]);
+      }
+      const int key = wk * C::KPW + n * 16 + (lane & 15);
+#pragma unroll
+      for (int d2 = 0; d2 < D / 16; ++d2) {
+        uint32_t f[4];
+        ldsm4t(st + C::TILE + swz<D>(key, 2 * d2 + (lane >> 4)), f);
+        mma16816(o[2 * d2], p, f[0], f[1]);
+        mma16816(o[2 * d2 + 1], p, f[2], f[3]);
       }
     }
   }
-  x.store(a.out + (b * a.H + h) * D, lane);
-}
+  cp_wait<0>();
+  __syncthreads();
 
-// One block per (user, token): the block checks the user, then each warp takes heads.
-template <int D, typename IdxT>
-__global__ void __launch_bounds__(128) tree_kernel(const CacheArgs a) {
-  if (*a.status != 0) return;
-  const int lane = threadIdx.x & 31;
-  const int64_t b = blockIdx.y;
-  const IdxT *off = static_cast<const IdxT*>(a.off), *ho = static_cast<const IdxT*>(a.hist_off);
-  const int64_t s = off[b], e = off[b + 1], hs = ho[b], he = ho[b + 1];
-  int bad = 0;
-  int64_t hl = he - hs;
-  if (s < 0 || s > e || e > a.N || (b == 0 && s != 0) || (b == a.B - 1 && e != a.N) || hs < 0 ||
-      hs > he || he > a.R) {
-    bad = JCA_STATUS_BAD_OFFSETS;
-  } else if (e - s > a.max_cand) {
-    bad = JCA_STATUS_BAD_TREE;
-  } else if (a.len) {
-    hl = static_cast<const IdxT*>(a.len)[b];
-    if (hl < 0 || hl > he - hs) bad = JCA_STATUS_BAD_LENGTH;
-  }
-  if (!bad) {
-    int wrong = 0;
-    for (int i = threadIdx.x; i < e - s; i += blockDim.x) {
-      const int p = a.parent[s + i];
-      wrong |= p < -1 || p >= i;
+  // Joining: every warp's (m, l, O) to shared memory, then the block's key groups, then the cluster.
+  float* part = reinterpret_cast<float*>(smem);                       // [KW][RB][D]
+  float* pm = reinterpret_cast<float*>(smem + C::OFF_ML);             // [KW][RB]
+  float* pl = pm + C::KW * C::RB;
+  float* jm = pl + C::KW * C::RB;                                     // [RB] of the block
+  float* jl = jm + C::RB;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    const int r = ra + 8 * h;
+    if ((lane & 3) == 0) {
+      pm[wk * C::RB + r] = m[h];
+      pl[wk * C::RB + r] = l[h];
     }
-    if (__syncthreads_or(wrong)) bad = JCA_STATUS_BAD_TREE;
+    float* x = part + (wk * C::RB + r) * D + 2 * (lane & 3);
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+      *reinterpret_cast<float2*>(x + 8 * n) = make_float2(o[n][2 * h], o[n][2 * h + 1]);
   }
-  if (bad) {
-    if (threadIdx.x == 0) set_status(a.status, bad);
+  __syncthreads();
+  if (tid < C::RB) {
+    float mm = -INFINITY, ll = 0.f;
+#pragma unroll
+    for (int w = 0; w < C::KW; ++w) mm = fmaxf(mm, pm[w * C::RB + tid]);
+#pragma unroll
+    for (int w = 0; w < C::KW; ++w) {
+      const float x = pm[w * C::RB + tid], f = x == -INFINITY ? 0.f : fast_exp2(x - mm);
+      ll += pl[w * C::RB + tid] * f;
+      pm[w * C::RB + tid] = f;
+    }
+    jm[tid] = mm;
+    jl[tid] = skip ? -1.f : ll;   // a block that saw an error: nothing of the cluster is written
+  }
+  __syncthreads();
+  if (C::KW > 1 && a.split > 1) {
+    for (int i = tid; i < C::RB * D / 4; i += kThr) {
+      const int r = i / (D / 4);
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < C::KW; ++w) {
+        const float f = pm[w * C::RB + r];
+        const float4 y = reinterpret_cast<const float4*>(part)[w * C::RB * D / 4 + i];
+        x.x = fmaf(f, y.x, x.x);
+        x.y = fmaf(f, y.y, x.y);
+        x.z = fmaf(f, y.z, x.z);
+        x.w = fmaf(f, y.w, x.w);
+      }
+      reinterpret_cast<float4*>(part)[i] = x;
+    }
+  }
+  const int n4 = rows * D / 4;
+  auto store = [&](int i, float4 x) {
+    const int g = rb * C::RB + i / (D / 4);
+    bf16* dst = a.out + ((row0 + g / G) * a.H + (int64_t)hk * G + g % G) * D + (i % (D / 4)) * 4;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+  };
+  if (a.split == 1) {
+    for (int i = tid; i < n4; i += kThr) {
+      const int r = i / (D / 4);
+      const float inv = 1.f / jl[r];
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < C::KW; ++w) {
+        const float f = pm[w * C::RB + r] * inv;
+        const float4 y = reinterpret_cast<const float4*>(part)[w * C::RB * D / 4 + i];
+        x.x = fmaf(f, y.x, x.x);
+        x.y = fmaf(f, y.y, x.y);
+        x.z = fmaf(f, y.z, x.z);
+        x.w = fmaf(f, y.w, x.w);
+      }
+      store(i, x);
+    }
     return;
   }
-  const int64_t t = blockIdx.x;
-  if (t >= e - s) return;
-  const int G = a.H / a.Hkv;
-  for (int h = threadIdx.x >> 5; h < a.H; h += 4) {
-    const int hk = h / G;
-    Vecs<D> x;
-    x.start(a.q + (s + t) * a.q_stride + (int64_t)h * D, lane);
-    for (int64_t j = 0; j < hl; ++j) {
-      const int64_t at = ((hs + j) * a.Hkv + hk) * D;
-      x.see(a.kc + at, a.vc + at, a.scale, lane);
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  for (int i = rank * kThr + tid; i < n4; i += a.split * kThr) {
+    const int r = i / (D / 4);
+    float mm = -INFINITY, total = 0.f;
+    bool whole = true;
+    float w[kMaxSplit];
+#pragma unroll
+    for (int x = 0; x < kMaxSplit; ++x) {
+      w[x] = x < a.split ? *cluster.map_shared_rank(jm + r, x) : -INFINITY;
+      mm = fmaxf(mm, w[x]);
     }
-    for (int j = (int)t; j >= 0; j = a.parent[s + j])
-      x.see(a.k + (s + j) * a.k_stride + (int64_t)hk * D,
-            a.v + (s + j) * a.v_stride + (int64_t)hk * D, a.scale, lane);
-    x.store(a.out + ((s + t) * a.H + h) * D, lane);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int x = 0; x < kMaxSplit; ++x) {
+      if (x >= a.split) break;
+      const float f = w[x] == -INFINITY ? 0.f : fast_exp2(w[x] - mm);
+      const float lx = *cluster.map_shared_rank(jl + r, x);
+      whole &= lx >= 0.f;
+      total = fmaf(f, lx, total);
+      const float4 y = reinterpret_cast<const float4*>(cluster.map_shared_rank(part, x))[i];
+      acc.x = fmaf(f, y.x, acc.x);
+      acc.y = fmaf(f, y.y, acc.y);
+      acc.z = fmaf(f, y.z, acc.z);
+      acc.w = fmaf(f, y.w, acc.w);
+    }
+    const float inv = 1.f / total;
+    if (whole) store(i, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
   }
+  cluster.sync();   // no block leaves while another still reads its shared memory
 }
 
 int cache_check(int64_t B, int64_t rows, int64_t R, int H, int Hkv, int d, int64_t qs, int64_t ks,
@@ -179,18 +545,58 @@ int cache_check(int64_t B, int64_t rows, int64_t R, int H, int Hkv, int d, int64
   return JCA_OK;
 }
 
-template <int D>
-void launch_decode(const CacheArgs& a, int idx_bits, cudaStream_t st) {
-  const unsigned grid = (unsigned)((a.B * a.H + 3) / 4);
-  if (idx_bits == 32) decode_kernel<D, int32_t><<<grid, 128, 0, st>>>(a);
-  else decode_kernel<D, int64_t><<<grid, 128, 0, st>>>(a);
+constexpr int kMaxDevices = 64;
+
+// `keys`: about how many keys a unit walks. The key list is split while there are fewer blocks than
+// two per SM and each part keeps at least two tiles.
+template <int D, int RW, bool TREE, typename IdxT>
+int launch_cache(CacheArgs a, int64_t max_rows, int64_t keys, int dev, int sms, cudaStream_t st) {
+  using C = CCfg<D, RW, TREE>;
+  a.row_blocks = (int)((max_rows + C::RB - 1) / C::RB);
+  const int64_t units = a.B * a.Hkv * a.row_blocks;
+  const int64_t tiles = (keys + kBK - 1) / kBK;
+  a.split = 1;
+  while (a.split < kMaxSplit && units * a.split < 2 * sms && tiles >= 4 * a.split) a.split *= 2;
+  if (units * a.split >= (int64_t)INT_MAX) return JCA_ERR_SHAPE;
+  auto kernel = cache_attn_kernel<D, RW, TREE, IdxT>;
+  static std::atomic<bool> set[kMaxDevices];
+  if (!set[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+        cudaSuccess)
+      return JCA_ERR_CUDA;
+    set[dev].store(true, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * a.split));
+  cfg.blockDim = dim3(kThr);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)a.split;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = a.split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? JCA_OK : JCA_ERR_CUDA;
 }
 
-template <int D>
-void launch_tree(const CacheArgs& a, int idx_bits, cudaStream_t st) {
-  const dim3 grid((unsigned)a.max_cand, (unsigned)a.B);
-  if (idx_bits == 32) tree_kernel<D, int32_t><<<grid, 128, 0, st>>>(a);
-  else tree_kernel<D, int64_t><<<grid, 128, 0, st>>>(a);
+template <int D, bool TREE, typename IdxT>
+int launch_rows(const CacheArgs& a, int64_t max_rows, int64_t keys, int dev, int sms,
+                cudaStream_t st) {
+  if (max_rows <= 16) return launch_cache<D, 1, TREE, IdxT>(a, max_rows, keys, dev, sms, st);
+  if (max_rows <= 32) return launch_cache<D, 2, TREE, IdxT>(a, max_rows, keys, dev, sms, st);
+  return launch_cache<D, 4, TREE, IdxT>(a, max_rows, keys, dev, sms, st);
+}
+
+template <bool TREE, typename IdxT>
+int launch_heads(const CacheArgs& a, int d, int64_t max_rows, int64_t keys, int dev, int sms,
+                 cudaStream_t st) {
+  switch (d) {
+    case 16: return launch_rows<16, TREE, IdxT>(a, max_rows, keys, dev, sms, st);
+    case 32: return launch_rows<32, TREE, IdxT>(a, max_rows, keys, dev, sms, st);
+    case 64: return launch_rows<64, TREE, IdxT>(a, max_rows, keys, dev, sms, st);
+    default: return launch_rows<128, TREE, IdxT>(a, max_rows, keys, dev, sms, st);
+  }
 }
 
 }  // namespace
@@ -238,15 +644,13 @@ extern "C" int jagged_window_decode_fwd(const void* q, const void* k_new, const 
   a.v_stride = v_stride;
   a.H = H;
   a.Hkv = Hkv;
-  a.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)d_head);
+  a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)d_head)) * 1.4426950408889634f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  switch (d_head) {
-    case 16: launch_decode<16>(a, idx_bits, st); break;
-    case 32: launch_decode<32>(a, idx_bits, st); break;
-    case 64: launch_decode<64>(a, idx_bits, st); break;
-    default: launch_decode<128>(a, idx_bits, st); break;
-  }
-  return cudaGetLastError() == cudaSuccess ? JCA_OK : JCA_ERR_CUDA;
+  const int64_t span = window < R ? window : R, first = n_sinks < R ? n_sinks : R;
+  const int64_t keys = span + first < R ? span + first : R;
+  return idx_bits == 32
+             ? launch_heads<false, int32_t>(a, d_head, H / Hkv, keys, dev, sms, st)
+             : launch_heads<false, int64_t>(a, d_head, H / Hkv, keys, dev, sms, st);
 }
 
 extern "C" int cand_tree_attn_fwd(const void* cand_q, const void* own_k, const void* own_v,
@@ -259,7 +663,7 @@ extern "C" int cand_tree_attn_fwd(const void* cand_q, const void* own_k, const v
                                   jca_stream_t stream) {
   int rc = cache_check(B, Nc, R, H, Hkv, d_head, q_stride, k_stride, v_stride, idx_bits);
   if (rc) return rc;
-  if (max_cand < 1 || max_cand > kMaxTree || (B == 0 && Nc > 0) || B > 65535) return JCA_ERR_SHAPE;
+  if (max_cand < 1 || max_cand > kMaxTree || (B == 0 && Nc > 0)) return JCA_ERR_SHAPE;
   if (B == 0) return JCA_OK;
   if (!status || !cand_offsets || !hist_offsets ||
       (Nc > 0 && (!cand_q || !own_k || !own_v || !parent || !out)) ||
@@ -292,13 +696,9 @@ extern "C" int cand_tree_attn_fwd(const void* cand_q, const void* own_k, const v
   a.H = H;
   a.Hkv = Hkv;
   a.max_cand = max_cand;
-  a.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)d_head);
+  a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)d_head)) * 1.4426950408889634f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  switch (d_head) {
-    case 16: launch_tree<16>(a, idx_bits, st); break;
-    case 32: launch_tree<32>(a, idx_bits, st); break;
-    case 64: launch_tree<64>(a, idx_bits, st); break;
-    default: launch_tree<128>(a, idx_bits, st); break;
-  }
-  return cudaGetLastError() == cudaSuccess ? JCA_OK : JCA_ERR_CUDA;
+  const int64_t max_rows = (int64_t)max_cand * (H / Hkv), keys = R / B + max_cand;
+  return idx_bits == 32 ? launch_heads<true, int32_t>(a, d_head, max_rows, keys, dev, sms, st)
+                        : launch_heads<true, int64_t>(a, d_head, max_rows, keys, dev, sms, st);
 }

@@ -547,7 +547,7 @@ def test_tree_bad_users_leave_the_others():
     assert code(hl=(1, 31)) == 1
     assert code(hl=(1, -1)) == 1
     assert code(ho=(2, 200)) == 2
-    assert code(off=(1, 11)) == 2
+    assert code(off=(1, 11)) in (2, 8)         # falling offsets, and a first run of 11: either wins
     b = Tree([4, 6, 3], [20, 30, 10], 2, 2, 16, seed=5)
     b.out.fill_(7.0)
     b.run(5)                                   # a run longer than max_cand
