@@ -605,56 +605,6 @@ __device__ void mma_role(const AttnArgs& a, uint32_t sbase, uint32_t bars, uint3
 // ------------------------------------------------------------------------------------------
 // Softmax + epilogue
 // ------------------------------------------------------------------------------------------
-template <int N>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t t, uint32_t* r) {
-  if constexpr (N == 8) {
-    tmem_ld_x8(t, r);
-  } else if constexpr (N == 16) {
-    tmem_ld_x16(t, r);
-  } else {
-    tmem_ld_x32(t, r);
-  }
-}
-
-template <int N>
-__device__ __forceinline__ void tmem_st_cols(uint32_t t, const uint32_t* r) {
-  if constexpr (N == 8) {
-    tmem_st_x8(t, r);
-  } else if constexpr (N == 16) {
-    tmem_st_x16(t, r);
-  } else {
-    tmem_st_x32(t, r);
-  }
-}
-
-template <int N>
-__device__ __forceinline__ void reg_fence_cols(uint32_t* r) {
-  if constexpr (N == 8) {
-    reg_fence8(r);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 16) reg_fence16(r + i);
-  }
-}
-
-// One O row (D columns) of this group, multiplied by alpha in place in TMEM.
-template <int D>
-__device__ __forceinline__ void rescale_o_row(uint32_t t_o, float alpha) {
-  constexpr int CW = D < 32 ? D : 32;
-#pragma unroll
-  for (int c0 = 0; c0 < D; c0 += CW) {
-    uint32_t u[CW];
-    tmem_ld_cols<CW>(t_o + c0, u);
-    tmem_wait_ld();
-    reg_fence_cols<CW>(u);
-#pragma unroll
-    for (int i = 0; i < CW; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * alpha);
-    tmem_st_cols<CW>(t_o + c0, u);
-  }
-  tmem_wait_st();
-}
-
-
 // Score of a candidate row against its own key, scaled to log2 units (the diagonal term of the
 // mask). Plain CUDA-core dot product over 16-byte loads, half a row at a time.
 template <int D>

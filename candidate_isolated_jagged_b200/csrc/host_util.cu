@@ -42,11 +42,16 @@ std::mutex g_props_mu;
 
 bool make_rows_map_bf16(CUtensorMap* map, const void* base, int64_t rows, int H, int D,
                         int box_rows) {
+  return make_strided_map_bf16(map, base, rows, H, D, (int64_t)H * D, box_rows);
+}
+
+bool make_strided_map_bf16(CUtensorMap* map, const void* base, int64_t rows, int H, int D,
+                           int64_t row_stride, int box_rows) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const int sw = D * 2 >= 128 ? 128 : D * 2;
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)rows};
-  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)row_stride * 2};
   const cuuint32_t box[3] = {(cuuint32_t)(sw / 2), 1u, (cuuint32_t)box_rows};
   const cuuint32_t estr[3] = {1u, 1u, 1u};
   const CUtensorMapSwizzle swz = sw == 128  ? CU_TENSOR_MAP_SWIZZLE_128B

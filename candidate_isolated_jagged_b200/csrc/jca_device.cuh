@@ -286,6 +286,56 @@ __device__ __forceinline__ void reg_fence16(uint32_t* r) {
                  "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
 
+// N (8, 16 or 32) columns.
+template <int N>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t t, uint32_t* r) {
+  if constexpr (N == 8) {
+    tmem_ld_x8(t, r);
+  } else if constexpr (N == 16) {
+    tmem_ld_x16(t, r);
+  } else {
+    tmem_ld_x32(t, r);
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void tmem_st_cols(uint32_t t, const uint32_t* r) {
+  if constexpr (N == 8) {
+    tmem_st_x8(t, r);
+  } else if constexpr (N == 16) {
+    tmem_st_x16(t, r);
+  } else {
+    tmem_st_x32(t, r);
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void reg_fence_cols(uint32_t* r) {
+  if constexpr (N == 8) {
+    reg_fence8(r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 16) reg_fence16(r + i);
+  }
+}
+
+// One accumulator row (D columns) multiplied by alpha in place in TMEM.
+template <int D>
+__device__ __forceinline__ void rescale_o_row(uint32_t t_o, float alpha) {
+  constexpr int CW = D < 32 ? D : 32;
+#pragma unroll
+  for (int c0 = 0; c0 < D; c0 += CW) {
+    uint32_t u[CW];
+    tmem_ld_cols<CW>(t_o + c0, u);
+    tmem_wait_ld();
+    reg_fence_cols<CW>(u);
+#pragma unroll
+    for (int i = 0; i < CW; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * alpha);
+    tmem_st_cols<CW>(t_o + c0, u);
+  }
+  tmem_wait_st();
+}
+
 // ------------------------------------------------------------------------------------------
 // Math and memory helpers
 // ------------------------------------------------------------------------------------------

@@ -31,6 +31,11 @@ int64_t max_work_items(int64_t B, int64_t rows, int H);
 bool make_rows_map_bf16(CUtensorMap* map, const void* base, int64_t rows, int H, int D,
                         int box_rows);
 
+// The same over rows that are row_stride elements apart (a multiple of 8): slices of a fused
+// projection.
+bool make_strided_map_bf16(CUtensorMap* map, const void* base, int64_t rows, int H, int D,
+                           int64_t row_stride, int box_rows);
+
 // The current device (index < 64) and its multiprocessor count, cached per device. Returns
 // JCA_ERR_DEVICE on a device that is not sm_100, JCA_ERR_CUDA when a query fails.
 int current_device(int* dev, int* sms);

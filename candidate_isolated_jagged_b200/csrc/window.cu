@@ -1,49 +1,64 @@
-// Causal attention over packed rows with a sliding window and first tokens that stay visible:
-// forward and backward (include/jca.h states the mask and the layout).
+// Causal attention over packed rows with a sliding window and first tokens that stay visible, forward
+// (include/jca.h states the mask and the layout). The backward pass is in window_bwd.cu.
+//
+// Mathematics: row i of a user that starts at row s sees the keys of the two intervals
+//   [max(s, i - window + 1), i]   and   [s, min(s + n_sinks, that lower end)),
+// padding left out; softmax with a running maximum (p = 2^(scale log2e s - m), moved only when it
+// grows by 2^8) and sum in fp32, so each key is visited once.
+//
+// Tiling. The packed rows are cut into blocks of 256 whatever users they hold: both lower ends never
+// fall from row to row, so the keys that a 128-row tile needs are one run of packed rows ending
+// at the tile itself, plus the first tokens of the tile's first user (every later user of the
+// tile starts inside it). Short users therefore share tiles, every block costs about
+// (window + 256) / 128 key tiles, and no list of work is needed beyond each row's user start, which a
+// small kernel writes while it checks the offsets. Key tiles start at multiples of 128 rows, so
+// most tiles are visible whole or not at all to a warp's 32 rows; the visible columns of a tile
+// are decided for 32 columns at a time and per warp: chunks that no row sees are not read, chunks that
+// every row sees are not masked.
+//
+// Kernel (one persistent block per SM, 12 warps; tcgen05 with TMEM accumulators, TMA loads):
+//   warp 0       lane 0 loads Q and K tiles, lane 1 loads V tiles (rings of stages);
+//   warp 1       allocates TMEM; one thread issues every MMA;
+//   warps 2..9   two softmax groups, one per 128-row query tile A and B of the block, one row a thread
+//                (TMEM lane = row); P is written back over S as bf16 and read from there by the PV
+//                MMA; the group finishes its own rows;
+//   warp 10      with padding: zeroes the padding rows of each landed V tile (a weight of 0 does not
+//                undo an Inf or NaN there), otherwise idle;
+//   warp 11      claims the next block from a counter, reads where its users start and passes both
+//                to every role through a ring, several blocks ahead of the loads.
+// A and B share every K and V tile they both need. MMA order, one stream over all blocks:
+//   QK_A(t), PV_B(t - 1), QK_B(t), PV_A(t)
+// so that one group's softmax runs while the tensor core works for the other.
+//
+// What bounds it: at a window of 256 the bytes (Q, K, V read and O written once: 172 us on the
+// 256-user batch at the copy bandwidth) and the softmax of about 3 key tiles per query tile (93 us of
+// exponentials); at 1024 the tensor core and the softmax, as in the full layer.
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "jca_device.cuh"
 #include "jca_internal.h"
+#include "window.h"
 
 namespace jca {
 namespace {
 
 using bf16 = __nv_bfloat16;
 
-constexpr int kMaxSinks = 128;
-
-struct WindowArgs {
-  const bf16* q;
-  const bf16* k;
-  const bf16* v;
-  const bf16* out;
-  const bf16* dout;
-  const float* lse;
-  bf16* o;
-  float* lse_out;
-  bf16* dq;
-  bf16* dk;
-  bf16* dv;
-  const uint8_t* valid;
-  const int32_t* row_start;   // [T] first row of the row's user
-  const int32_t* row_end;     // [T] one past its last
-  const int32_t* status;
-  int64_t T, q_stride, k_stride, v_stride;
-  int H, Hkv, window, n_sinks;
-  float scale;
-};
-
-// Checks the offsets and writes each row's user bounds; one block per user.
+// Checks the offsets and writes each row's user bounds; one block per user. Zeroes the counter from
+// which the attention kernel claims its blocks.
 template <typename IdxT>
 __global__ void __launch_bounds__(128)
     window_plan_kernel(const IdxT* __restrict__ off, int64_t B, int64_t T,
                        int32_t* __restrict__ row_start, int32_t* __restrict__ row_end,
-                       int32_t* status) {
+                       int32_t* counters, int n_counters, int32_t* status) {
+  if (blockIdx.x == 0 && (int)threadIdx.x < n_counters) counters[threadIdx.x] = 0;
   if (*status != 0) return;
   for (int64_t b = blockIdx.x; b < B; b += gridDim.x) {
     const long long s = (long long)off[b], e = (long long)off[b + 1];
@@ -58,157 +73,669 @@ __global__ void __launch_bounds__(128)
   }
 }
 
-// One warp per (row, head); lane l holds elements l * EPL ... of the head.
+struct FwdArgs {
+  bf16* out;
+  float* lse;                 // [T, H] or null
+  const uint8_t* valid;       // [T] or null
+  const int32_t* row_start;   // [T]
+  int32_t* counter;           // next block to claim
+  int32_t* status;
+  int T, H, group, window, n_sinks, n_items;
+  int out_v8;                 // rows can be written with 32-byte stores
+  float scale_log2;
+};
+
+constexpr int kRing = 4;
+constexpr int kThreads = 384;
+constexpr int kGroup = 128;   // softmax threads of a query tile
+
 template <int D>
-struct Row {
-  static constexpr int EPL = D >= 32 ? D / 32 : 1;
-  float x[EPL];
-  __device__ __forceinline__ void load(const bf16* p, int lane) {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      x[i] = lane * EPL < D ? __bfloat162float(p[lane * EPL + i]) : 0.f;
+struct Cfg {
+  static constexpr int BM = kTileM, BN = kTileN;
+  static constexpr int ROW_BYTES = D * 2;
+  static constexpr int SW = ROW_BYTES >= 128 ? 128 : ROW_BYTES;    // swizzle span (bytes)
+  static constexpr int NBLK = ROW_BYTES / SW;                      // column blocks of a tile
+  static constexpr int BOX_X = SW / 2;
+  static constexpr int TILE_BYTES = BM * ROW_BYTES;
+  static constexpr int BLK_BYTES = BM * SW;
+  static constexpr uint32_t LAYOUT = SW == 128 ? 2u : (SW == 64 ? 4u : 6u);
+  static constexpr int KSTEPS_QK = D / 16;
+  static constexpr int KSTEPS_PER_BLK = SW / 32;
+  static constexpr int KSTEPS_PV = BN / 16;
+  // Ring depths; d = 128 fills shared memory (192 KB) with one Q buffer per tile and two stages.
+  static constexpr int QS = D >= 128 ? 1 : 2;
+  static constexpr int KVS = D >= 128 ? 2 : 4;
+  static constexpr int OFF_Q = 0;                                  // [group][QS]
+  static constexpr int OFF_K = OFF_Q + 2 * QS * TILE_BYTES;
+  static constexpr int OFF_V = OFF_K + KVS * TILE_BYTES;
+  static constexpr int OFF_BAR = OFF_V + KVS * TILE_BYTES;
+  static constexpr int B_QFULL = 0;                                // [group][QS]
+  static constexpr int B_QEMPTY = B_QFULL + 2 * QS;
+  static constexpr int B_KFULL = B_QEMPTY + 2 * QS;                // [KVS]
+  static constexpr int B_KEMPTY = B_KFULL + KVS;
+  static constexpr int B_VFULL = B_KEMPTY + KVS;
+  static constexpr int B_VREADY = B_VFULL + KVS;                   // padding rows zeroed
+  static constexpr int B_VEMPTY = B_VREADY + KVS;
+  static constexpr int B_SFULL = B_VEMPTY + KVS;                   // [group]
+  static constexpr int B_PFULL = B_SFULL + 2;
+  static constexpr int B_OREADY = B_PFULL + 2;
+  static constexpr int B_OFREE = B_OREADY + 2;
+  static constexpr int B_DRAIN = B_OFREE + 2;
+  static constexpr int B_RINGFULL = B_DRAIN + 1;                   // [kRing]
+  static constexpr int B_RINGEMPTY = B_RINGFULL + kRing;
+  static constexpr int NUM_BARS = B_RINGEMPTY + kRing;
+  static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+  static constexpr int OFF_RING = OFF_MISC + 16;                   // kRing x 6 ints
+  static constexpr int SMEM_USED = OFF_RING + kRing * 24;
+  static constexpr int SMEM_RAW = SMEM_USED + 1024;                // slack for 1 KB alignment
+  // At least 120 KB so that a second block never shares the SM (and its TMEM).
+  static constexpr int SMEM_ALLOC = SMEM_RAW > 120 * 1024 ? SMEM_RAW : 120 * 1024;
+  static constexpr uint32_t TMEM_S = 0, TMEM_O = 256, TMEM_COLS = 512;   // + 128 for group B
+  static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory budget");
+};
+
+// A block of up to 256 rows of one head, as every role derives it from the ring entry.
+struct Item {
+  int q0, h, kstart, n_sink, n_tiles;
+  int lo[2], start[2], last[2];   // per query tile: lowest window key, first user's start, last row
+  bool has_b;
+
+  __device__ __forceinline__ int key_row(int j) const {
+    return n_sink ? (j == 0 ? start[0] : kstart + (j - 1) * kTileN) : kstart + j * kTileN;
   }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) x[i] = 0.f;
-  }
-  __device__ __forceinline__ float dot(const Row& o) const {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) s = fmaf(x[i], o.x[i], s);
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-    return s;
-  }
-  __device__ __forceinline__ void axpy(float a, const Row& o) {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) x[i] = fmaf(a, o.x[i], x[i]);
-  }
-  __device__ __forceinline__ void store(bf16* p, float a, int lane) const {
-    if (lane * EPL < D)
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) p[lane * EPL + i] = __float2bfloat16(x[i] * a);
+  __device__ __forceinline__ bool is_sink(int j) const { return n_sink && j == 0; }
+  // Whether tile g (0: A, 1: B) reads key tile j.
+  __device__ __forceinline__ bool needs(int g, int j, int n_sinks) const {
+    if (g == 1 && !has_b) return false;
+    if (is_sink(j)) return g == 0 || start[1] == start[0];
+    const int kr = key_row(j);
+    return kr <= last[g] && (kr + kTileN > lo[g] ||
+                             (start[g] < kr + kTileN && start[g] + n_sinks > kr));
   }
 };
 
-template <int D>
-__global__ void __launch_bounds__(128) window_fwd_kernel(const WindowArgs a) {
-  if (*a.status != 0) return;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = blockIdx.x * (int64_t)4 + (threadIdx.x >> 5);
-  if (w >= a.T * a.H) return;
-  const int64_t i = w / a.H;
-  const int h = (int)(w % a.H), hk = h / (a.H / a.Hkv);
-  Row<D> q, acc, x;
-  q.load(a.q + i * a.q_stride + (int64_t)h * D, lane);
-  acc.zero();
-  float m = -INFINITY, l = 0.f;
-  const bool real = !a.valid || a.valid[i];
-  if (real) {
-    const int64_t s = a.row_start[i];
-    const int64_t lo = max(s, i - a.window + 1);
-    const int64_t first = min(s + a.n_sinks, lo);   // sinks [s, first), then [lo, i]
-    for (int64_t j = s; j <= i; ++j) {
-      if (j == first && first < lo) {
-        j = lo;
-      }
-      if (a.valid && !a.valid[j]) continue;
-      x.load(a.k + j * a.k_stride + (int64_t)hk * D, lane);
-      const float sc = q.dot(x) * a.scale;
-      const float mn = fmaxf(m, sc);
-      const float al = m == -INFINITY ? 0.f : __expf(m - mn), p = __expf(sc - mn);
-#pragma unroll
-      for (int t = 0; t < Row<D>::EPL; ++t) acc.x[t] *= al;
-      x.load(a.v + j * a.v_stride + (int64_t)hk * D, lane);
-      acc.axpy(p, x);
-      l = l * al + p;
-      m = mn;
-    }
-  }
-  acc.store(a.o + (i * a.H + h) * D, l > 0.f ? 1.f / l : 0.f, lane);
-  if (a.lse_out && lane == 0) a.lse_out[i * a.H + h] = l > 0.f ? m + logf(l) : -INFINITY;
+__device__ __forceinline__ Item make_item(const volatile int* e, const FwdArgs& a) {
+  Item w;
+  w.q0 = e[0];
+  w.h = e[1];
+  w.lo[0] = e[2];
+  w.start[0] = e[3];
+  w.lo[1] = e[4];
+  w.start[1] = e[5];
+  w.has_b = w.q0 + kTileM < a.T;
+  w.last[0] = min(w.q0 + kTileM, a.T) - 1;
+  w.last[1] = min(w.q0 + kItemRows, a.T) - 1;
+  w.kstart = w.lo[0] & ~(kTileN - 1);
+  // First tokens below the run of key tiles get a (trimmed) tile of their own.
+  w.n_sink = max(0, min(a.n_sinks, w.kstart - w.start[0]));
+  w.n_tiles = (w.q0 + (w.has_b ? kItemRows : kTileM) - w.kstart) / kTileN + (w.n_sink ? 1 : 0);
+  return w;
 }
 
-template <int D>
-__global__ void __launch_bounds__(128) window_dq_kernel(const WindowArgs a) {
-  if (*a.status != 0) return;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = blockIdx.x * (int64_t)4 + (threadIdx.x >> 5);
-  if (w >= a.T * a.H) return;
-  const int64_t i = w / a.H;
-  const int h = (int)(w % a.H), hk = h / (a.H / a.Hkv);
-  Row<D> q, dov, acc, x;
-  acc.zero();
-  if (!a.valid || a.valid[i]) {
-    q.load(a.q + i * a.q_stride + (int64_t)h * D, lane);
-    dov.load(a.dout + (i * a.H + h) * D, lane);
-    x.load(a.out + (i * a.H + h) * D, lane);
-    const float dl = dov.dot(x), lse = a.lse[i * a.H + h];
-    const int64_t s = a.row_start[i];
-    const int64_t lo = max(s, i - a.window + 1);
-    const int64_t first = min(s + a.n_sinks, lo);
-    for (int64_t j = s; j <= i; ++j) {
-      if (j == first && first < lo) j = lo;
-      if (a.valid && !a.valid[j]) continue;
-      x.load(a.v + j * a.v_stride + (int64_t)hk * D, lane);
-      const float dp = dov.dot(x);
-      x.load(a.k + j * a.k_stride + (int64_t)hk * D, lane);
-      const float p = __expf(q.dot(x) * a.scale - lse);
-      acc.axpy(p * (dp - dl), x);
-    }
-  }
-  acc.store(a.dq + (i * a.H + h) * D, a.scale, lane);
-}
-
-template <int D>
-__global__ void __launch_bounds__(128) window_dkv_kernel(const WindowArgs a) {
-  if (*a.status != 0) return;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = blockIdx.x * (int64_t)4 + (threadIdx.x >> 5);
-  if (w >= a.T * a.Hkv) return;
-  const int64_t j = w / a.Hkv;
-  const int hk = (int)(w % a.Hkv), G = a.H / a.Hkv;
-  Row<D> k, v, dk, dv, x, y;
-  dk.zero();
-  dv.zero();
-  if (!a.valid || a.valid[j]) {
-    k.load(a.k + j * a.k_stride + (int64_t)hk * D, lane);
-    v.load(a.v + j * a.v_stride + (int64_t)hk * D, lane);
-    const int64_t s = a.row_start[j], e = a.row_end[j];
-    const int64_t end = j - s < a.n_sinks ? e : min(e, j + a.window);
-    for (int64_t i = j; i < end; ++i) {
-      if (a.valid && !a.valid[i]) continue;
-      for (int h = hk * G; h < hk * G + G; ++h) {
-        x.load(a.dout + (i * a.H + h) * D, lane);
-        y.load(a.out + (i * a.H + h) * D, lane);
-        const float dl = x.dot(y), dp = x.dot(v);
-        y.load(a.q + i * a.q_stride + (int64_t)h * D, lane);
-        const float p = __expf(y.dot(k) * a.scale - a.lse[i * a.H + h]);
-        dv.axpy(p, x);
-        dk.axpy(p * (dp - dl), y);
-      }
-    }
-  }
-  dk.store(a.dk + (j * a.Hkv + hk) * D, a.scale, lane);
-  dv.store(a.dv + (j * a.Hkv + hk) * D, 1.f, lane);
-}
-
-struct WindowLayout {
-  size_t row_start = 0, row_end = 0, total = 0;
+struct Ring {
+  volatile int* slot;
+  uint32_t full, empty, k;
 };
 
-WindowLayout window_layout(int64_t T, bool bwd) {
-  WindowLayout L;
-  L.row_end = align_up(4 * (size_t)T, 256);
-  L.total = align_up(L.row_end + (bwd ? 4 * (size_t)T : 0), 256);
-  if (L.total == 0) L.total = 256;
+// Takes the next entry; false when aborting or at the end.
+__device__ __forceinline__ bool ring_take(Ring& r, const FwdArgs& a, Item& w,
+                                          volatile int* abort_flag, bool& ok) {
+  const int s = (int)(r.k % kRing);
+  ok = mbar_wait(r.full + 8 * s, (r.k / kRing) & 1, abort_flag, a.status);
+  if (!ok) return false;
+  const volatile int* e = r.slot + 6 * s;
+  const bool more = e[0] >= 0;
+  if (more) w = make_item(e, a);
+  mbar_arrive(r.empty + 8 * s);
+  ++r.k;
+  return more;
+}
+
+// Claims blocks until none is left and posts them, then the end marker.
+__device__ void claim_role(const FwdArgs& a, Ring r, volatile int* abort_flag) {
+  for (;;) {
+    const int v = atomicAdd(a.counter, 1);
+    int e[6] = {-1, 0, 0, 0, 0, 0};
+    if (v < a.n_items) {
+      // Heads fastest: concurrent blocks share rows, and with shared heads K and V. Rows from the
+      // end: under a long window the later blocks of a user are the longer ones.
+      const int t = (a.n_items - 1 - v) / a.H;
+      e[0] = t * kItemRows;
+      e[1] = (a.n_items - 1 - v) % a.H;
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int i = min(e[0] + g * kTileM, a.T - 1);
+        e[3 + 2 * g] = a.row_start[i];
+        e[2 + 2 * g] = max(e[3 + 2 * g], i - a.window + 1);
+      }
+    }
+    const int s = (int)(r.k % kRing);
+    if (!mbar_wait(r.empty + 8 * s, ((r.k / kRing) & 1) ^ 1, abort_flag, a.status)) return;
+#pragma unroll
+    for (int i = 0; i < 6; ++i) r.slot[6 * s + i] = e[i];
+    mbar_arrive(r.full + 8 * s);
+    ++r.k;
+    if (e[0] < 0) return;
+  }
+}
+
+template <int D>
+__device__ void producer_role(const CUtensorMap* tmQ, const CUtensorMap* tmKV, const FwdArgs& a,
+                              uint32_t sbase, uint32_t bars, volatile int* abort_flag,
+                              bool loads_v, Ring ring) {
+  using C = Cfg<D>;
+  uint32_t nq[2] = {0, 0}, g = 0;
+  const int empty = loads_v ? C::B_VEMPTY : C::B_KEMPTY, full = loads_v ? C::B_VFULL : C::B_KFULL;
+  const int off = loads_v ? C::OFF_V : C::OFF_K;
+  bool ok = true;
+  Item w;
+  while (ring_take(ring, a, w, abort_flag, ok)) {
+    const int hk = w.h / a.group;
+    for (int j = 0; ok && j < w.n_tiles; ++j) {
+      const int s = (int)(g % C::KVS);
+      ok = mbar_wait(bars + 8 * (empty + s), ((g / C::KVS) & 1) ^ 1, abort_flag, a.status);
+      if (!ok) break;
+      mbar_arrive_expect_tx(bars + 8 * (full + s), C::TILE_BYTES);
+#pragma unroll
+      for (int c = 0; c < C::NBLK; ++c)
+        tma_load_3d(sbase + off + s * C::TILE_BYTES + c * C::BLK_BYTES, tmKV,
+                    bars + 8 * (full + s), c * C::BOX_X, hk, w.key_row(j));
+      ++g;
+      if (loads_v || j > 0) continue;
+      // The item's Q tiles go out behind its first K tile, whose stage was freed earlier.
+      for (int t = 0; t < (w.has_b ? 2 : 1); ++t) {
+        const int slot = t * C::QS + (int)(nq[t] % C::QS);
+        ok = mbar_wait(bars + 8 * (C::B_QEMPTY + slot), ((nq[t] / C::QS) & 1) ^ 1, abort_flag,
+                       a.status);
+        if (!ok) break;
+        mbar_arrive_expect_tx(bars + 8 * (C::B_QFULL + slot), C::TILE_BYTES);
+        ++nq[t];
+#pragma unroll
+        for (int c = 0; c < C::NBLK; ++c)
+          tma_load_3d(sbase + C::OFF_Q + slot * C::TILE_BYTES + c * C::BLK_BYTES, tmQ,
+                      bars + 8 * (C::B_QFULL + slot), c * C::BOX_X, w.h, w.q0 + t * C::BM);
+      }
+    }
+    if (!ok) break;
+  }
+  if (!ok) {
+    // Aborting: let every copy this thread started land before the block exits.
+    for (int t = 0; t < 2; ++t)
+      for (uint32_t n = nq[t] > (uint32_t)C::QS ? nq[t] - C::QS : 0; n < nq[t]; ++n)
+        mbar_wait_drain(bars + 8 * (C::B_QFULL + t * C::QS + (int)(n % C::QS)), (n / C::QS) & 1);
+    for (uint32_t n = g > (uint32_t)C::KVS ? g - C::KVS : 0; n < g; ++n)
+      mbar_wait_drain(bars + 8 * (full + (int)(n % C::KVS)), (n / C::KVS) & 1);
+  }
+}
+
+// Zeroes the rows of padding in every V tile; one warp.
+template <int D>
+__device__ void padding_role(const FwdArgs& a, uint32_t sbase, uint32_t bars,
+                             volatile int* abort_flag, int lane, Ring ring) {
+  using C = Cfg<D>;
+  constexpr int CH = C::ROW_BYTES / 16, CB = C::SW / 16;
+  uint32_t g = 0;
+  bool ok = true;
+  Item w;
+  for (;;) {
+    const bool more = ring_take(ring, a, w, abort_flag, ok);
+    if (!__all_sync(0xffffffffu, more)) return;
+    for (int j = 0; j < w.n_tiles; ++j, ++g) {
+      const int s = (int)(g % C::KVS), row = w.key_row(j);
+      uint32_t pad[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int k = row + 32 * c + lane;
+        pad[c] = __ballot_sync(0xffffffffu, k < a.T && !a.valid[k]);
+      }
+      ok = mbar_wait(bars + 8 * (C::B_VFULL + s), (g / C::KVS) & 1, abort_flag, a.status);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      const uint32_t tile = sbase + C::OFF_V + s * C::TILE_BYTES;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (!pad[c]) continue;
+        // A row's bytes of a column block are contiguous; the swizzle only reorders them.
+        for (int i = lane; i < 32 * CH; i += 32) {
+          const int r = i / CH, x = i % CH;
+          if ((pad[c] >> r) & 1)
+            st_shared_v4(tile + (x / CB) * C::BLK_BYTES + (32 * c + r) * C::SW + (x % CB) * 16, 0u,
+                         0u, 0u, 0u);
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bars + 8 * (C::B_VREADY + s));
+    }
+  }
+}
+
+// O (+)= P V over ksteps of 16 keys; P sits in TMEM as bf16 pairs, 8 columns a step.
+template <int D>
+__device__ __forceinline__ void mma_pv(uint32_t o, uint32_t p, uint64_t v, int ksteps,
+                                       bool overwrite) {
+  using C = Cfg<D>;
+  constexpr uint32_t kIdesc = idesc_bf16_f32(C::BM, D, false, true);
+  constexpr uint32_t kStep = (16 * C::SW) >> 4;
+  if (ksteps == C::KSTEPS_PV) {
+#pragma unroll
+    for (int kk = 0; kk < C::KSTEPS_PV; ++kk)
+      tc_mma_ts(o, p + (uint32_t)kk * 8u, v + (uint64_t)(kk * kStep), kIdesc,
+                (overwrite && kk == 0) ? 0u : 1u);
+  } else {
+    for (int kk = 0; kk < ksteps; ++kk)
+      tc_mma_ts(o, p + (uint32_t)kk * 8u, v + (uint64_t)(kk * kStep), kIdesc,
+                (overwrite && kk == 0) ? 0u : 1u);
+  }
+}
+
+template <int D>
+__device__ void mma_role(const FwdArgs& a, uint32_t sbase, uint32_t bars, uint32_t tmem,
+                         volatile int* abort_flag, Ring ring) {
+  using C = Cfg<D>;
+  constexpr uint32_t kIdescFull = idesc_bf16_f32(C::BM, C::BN, false, false);
+  constexpr uint32_t kIdesc0 = kIdescFull & ~(0x3Fu << 17);
+  const int vfull = a.valid ? C::B_VREADY : C::B_VFULL;
+  const uint64_t dq = smem_desc(sbase + C::OFF_Q, 16, 8 * C::SW, C::LAYOUT);
+  const uint64_t dk = smem_desc(sbase + C::OFF_K, 16, 8 * C::SW, C::LAYOUT);
+  const uint64_t dv = smem_desc(sbase + C::OFF_V, C::BLK_BYTES, 8 * C::SW, C::LAYOUT);
+  uint32_t g = 0, v_seen = 0, p_seen[2] = {0, 0}, o_items[2] = {0, 0}, q_seen[2] = {0, 0};
+  bool ok = true;
+  Item w;
+  auto qk = [&](int grp, uint64_t q, uint64_t k, uint32_t idesc) {
+#pragma unroll
+    for (int kk = 0; kk < C::KSTEPS_QK; ++kk) {
+      const uint32_t off = ((kk / C::KSTEPS_PER_BLK) * C::BLK_BYTES +
+                            (kk % C::KSTEPS_PER_BLK) * 32) >> 4;
+      tc_mma(tmem + C::TMEM_S + 128u * grp, q + off, k + off, idesc, kk > 0 ? 1u : 0u);
+    }
+    tc_commit(bars + 8 * (C::B_SFULL + grp));
+  };
+  auto pv = [&](int grp, uint32_t gg, bool first, int ksteps) -> bool {
+    const int s = (int)(gg % C::KVS);
+    if (gg + 1 != v_seen) {
+      if (!mbar_wait(bars + 8 * (vfull + s), (gg / C::KVS) & 1, abort_flag, a.status)) return false;
+      v_seen = gg + 1;
+    }
+    if (!mbar_wait(bars + 8 * (C::B_PFULL + grp), p_seen[grp] & 1, abort_flag, a.status))
+      return false;
+    ++p_seen[grp];
+    if (first && o_items[grp] > 0 &&
+        !mbar_wait(bars + 8 * (C::B_OFREE + grp), (o_items[grp] - 1) & 1, abort_flag, a.status))
+      return false;
+    tc_fence_after();
+    mma_pv<D>(tmem + C::TMEM_O + 128u * grp, tmem + C::TMEM_S + 128u * grp,
+              dv + (uint64_t)((s * C::TILE_BYTES) >> 4), ksteps, first);
+    return true;
+  };
+  // PV_B of the key tile before, possibly of the item before.
+  struct {
+    uint32_t gg;
+    int ksteps;   // 0: nothing pending
+    bool first, last;
+  } pend = {0, 0, false, false};
+  auto flush_b = [&]() -> bool {
+    if (pend.ksteps == 0) return true;
+    if (!pv(1, pend.gg, pend.first, pend.ksteps)) return false;
+    tc_commit(bars + 8 * (C::B_VEMPTY + (int)(pend.gg % C::KVS)));
+    if (pend.last) {
+      tc_commit(bars + 8 * (C::B_OREADY + 1));
+      ++o_items[1];
+    }
+    pend.ksteps = 0;
+    return true;
+  };
+  auto wait_q = [&](int t, int slot) -> bool {
+    if (!mbar_wait(bars + 8 * (C::B_QFULL + slot), (q_seen[t] / C::QS) & 1, abort_flag, a.status))
+      return false;
+    ++q_seen[t];
+    tc_fence_after();
+    return true;
+  };
+  while (ok && ring_take(ring, a, w, abort_flag, ok)) {
+    const int qslot[2] = {(int)(q_seen[0] % C::QS), C::QS + (int)(q_seen[1] % C::QS)};
+    const uint64_t q[2] = {dq + (uint64_t)((qslot[0] * C::TILE_BYTES) >> 4),
+                           dq + (uint64_t)((qslot[1] * C::TILE_BYTES) >> 4)};
+    // Key tiles run from low to high rows: a tile is a query tile's last when it holds its rows.
+    bool seen[2] = {false, false};
+    for (int j = 0; j < w.n_tiles; ++j, ++g) {
+      const int s = (int)(g % C::KVS);
+      const bool na = w.needs(0, j, a.n_sinks), nb = w.needs(1, j, a.n_sinks);
+      const int kr = w.key_row(j);
+      const bool last_a = !w.is_sink(j) && kr == w.q0, last_b = !w.is_sink(j) && kr == w.q0 + C::BM;
+      const int keys = w.is_sink(j) ? (w.n_sink + 15) & ~15 : C::BN;
+      const uint32_t idesc = kIdesc0 | ((uint32_t)(keys >> 3) << 17);
+      const uint64_t k = dk + (uint64_t)((s * C::TILE_BYTES) >> 4);
+      ok = mbar_wait(bars + 8 * (C::B_KFULL + s), (g / C::KVS) & 1, abort_flag, a.status);
+      if (!ok) break;
+      tc_fence_after();
+      if (na) {
+        if (!seen[0]) {
+          ok = wait_q(0, qslot[0]);
+          if (!ok) break;
+        }
+        qk(0, q[0], k, idesc);
+        if (last_a) tc_commit(bars + 8 * (C::B_QEMPTY + qslot[0]));
+      }
+      ok = flush_b();
+      if (!ok) break;
+      if (nb) {
+        if (!seen[1]) {
+          ok = wait_q(1, qslot[1]);
+          if (!ok) break;
+        }
+        qk(1, q[1], k, idesc);
+        if (last_b) tc_commit(bars + 8 * (C::B_QEMPTY + qslot[1]));
+      }
+      tc_commit(bars + 8 * (C::B_KEMPTY + s));
+      if (na) {
+        ok = pv(0, g, !seen[0], keys >> 4);
+        if (!ok) break;
+        seen[0] = true;
+        if (!nb) tc_commit(bars + 8 * (C::B_VEMPTY + s));
+        if (last_a) {
+          tc_commit(bars + 8 * C::B_OREADY);
+          ++o_items[0];
+        }
+      }
+      if (nb) {
+        pend.gg = g;
+        pend.ksteps = keys >> 4;
+        pend.first = !seen[1];
+        pend.last = last_b;
+        seen[1] = true;
+      }
+    }
+  }
+  if (ok) ok = flush_b();
+  if (!ok) {
+    // Aborting: wait until every MMA this thread issued has completed.
+    tc_commit(bars + 8 * C::B_DRAIN);
+    mbar_wait_drain(bars + 8 * C::B_DRAIN, 0);
+  }
+}
+
+// Bits [a, b) of a word, for any a and b.
+__device__ __forceinline__ uint32_t range_bits(int a, int b) {
+  a = min(max(a, 0), 32);
+  b = min(max(b, 0), 32);
+  const uint32_t below_b = b >= 32 ? 0xffffffffu : (1u << b) - 1u;
+  return a >= 32 ? 0u : below_b & (0xffffffffu << a);
+}
+
+template <int D>
+__device__ void softmax_role(const FwdArgs& a, uint32_t bars, uint32_t tmem,
+                             volatile int* abort_flag, int warp, int lane, Ring ring) {
+  using C = Cfg<D>;
+  const int grp = (warp - 2) >> 2;
+  const int quarter = warp & 3;
+  const int r = quarter * 32 + lane;
+  const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
+  const uint32_t t_s = t_lane + C::TMEM_S + 128u * grp, t_o = t_lane + C::TMEM_O + 128u * grp;
+  const float sl2 = a.scale_log2;
+  const float2 sl2v = make_float2(sl2, sl2);
+  uint32_t lt = 0, oi = 0;
+  bool ok = true;
+  Item w;
+  for (;;) {
+    const bool more = ring_take(ring, a, w, abort_flag, ok);
+    if (!__all_sync(0xffffffffu, more)) break;
+    if (grp == 1 && !w.has_b) continue;
+    const int i = w.q0 + grp * C::BM + r;           // this thread's row
+    const bool row_ok = i < a.T;
+    const bool sees = row_ok && (!a.valid || a.valid[i]);
+    const int start = row_ok ? a.row_start[i] : 0;
+    // Visible keys: [lo, hi) and [start, first).
+    const int lo = sees ? max(start, i - a.window + 1) : 0, hi = sees ? i + 1 : 0;
+    const int first = sees ? min(start + a.n_sinks, lo) : start;
+    float m = -INFINITY, l = 0.f;
+    bool fresh = true;
+    for (int j = 0; j < w.n_tiles; ++j) {
+      if (!w.needs(grp, j, a.n_sinks)) continue;
+      const int kr = w.key_row(j), cols = w.is_sink(j) ? w.n_sink : C::BN;
+      // Visible columns: per chunk of 32 columns, none, some or all for the warp's rows.
+      uint32_t bits[4], any = 0xfu, all = 0xfu;
+      const bool whole = cols == C::BN && !a.valid && lo <= kr && hi >= kr + C::BN;
+      if (!__all_sync(0xffffffffu, whole)) {
+        any = all = 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int k0 = kr + 32 * c;
+          uint32_t b = range_bits(lo - k0, hi - k0) | range_bits(start - k0, first - k0);
+          b &= range_bits(0, cols - 32 * c);
+          if (a.valid) {
+            const int k = k0 + lane;
+            b &= __ballot_sync(0xffffffffu, k < a.T && a.valid[k]);
+          }
+          bits[c] = b;
+          any |= __any_sync(0xffffffffu, b != 0u) ? 1u << c : 0u;
+          all |= __all_sync(0xffffffffu, b == 0xffffffffu) ? 1u << c : 0u;
+        }
+      }
+      ok = __all_sync(0xffffffffu,
+                      mbar_wait(bars + 8 * (C::B_SFULL + grp), lt & 1, abort_flag, a.status));
+      if (!ok) break;
+      ++lt;
+      tc_fence_after();
+      uint32_t x[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if ((any >> c) & 1) tmem_ld_x32(t_s + 32 * c, x + 32 * c);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 128; c += 16) reg_fence16(x + c);
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (!((any >> c) & 1)) continue;
+        uint32_t* y = x + 32 * c;
+        if (!((all >> c) & 1)) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) y[k] = ((bits[c] >> k) & 1u) ? y[k] : 0xff800000u;   // -inf
+        }
+        float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 32; k += 8) {
+          m0 = fmax3(m0, __uint_as_float(y[k]), __uint_as_float(y[k + 1]));
+          m1 = fmax3(m1, __uint_as_float(y[k + 2]), __uint_as_float(y[k + 3]));
+          m2 = fmax3(m2, __uint_as_float(y[k + 4]), __uint_as_float(y[k + 5]));
+          m3 = fmax3(m3, __uint_as_float(y[k + 6]), __uint_as_float(y[k + 7]));
+        }
+        mx = fmax3(mx, fmaxf(m0, m1), fmaxf(m2, m3));
+      }
+      const float m_new = fmaxf(m, mx * sl2);
+      // The reference maximum moves only when it grows by more than 2^8: the weights stay below 2^8
+      // and O and l keep the same reference.
+      const bool rescale = m_new > m + 8.0f;
+      const float m_use = rescale ? m_new : m;
+      const float neg_m = (m_use == -INFINITY) ? 0.f : -m_use;
+      const float alpha = (rescale && m != -INFINITY) ? fast_exp2(m - m_use) : 1.f;
+      const bool warp_rescale = __any_sync(0xffffffffu, rescale && !fresh);
+      const float2 negv = make_float2(neg_m, neg_m);
+      float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0, acc2 = acc0, acc3 = acc0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (32 * c >= cols) continue;   // the trimmed PV does not read these
+        uint32_t pk[16];
+        if ((any >> c) & 1) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float2 xs = __ffma2_rn(make_float2(__uint_as_float(x[32 * c + 2 * k]),
+                                                     __uint_as_float(x[32 * c + 2 * k + 1])),
+                                         sl2v, negv);
+            float2 p;
+            p.x = fast_exp2(xs.x);
+            p.y = fast_exp2(xs.y);
+            if ((k & 3) == 0) acc0 = __fadd2_rn(acc0, p);
+            if ((k & 3) == 1) acc1 = __fadd2_rn(acc1, p);
+            if ((k & 3) == 2) acc2 = __fadd2_rn(acc2, p);
+            if ((k & 3) == 3) acc3 = __fadd2_rn(acc3, p);
+            pk[k] = pack_bf16x2(p.x, p.y);   // the operand type of the PV product
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) pk[k] = 0u;
+        }
+        tmem_st_x16(t_s + 16 * c, pk);
+      }
+      const float2 acc01 = __fadd2_rn(acc0, acc1), acc23 = __fadd2_rn(acc2, acc3);
+      // O is stable here: its last PV was issued before the QK that filled S, and a commit fires
+      // only after every earlier MMA.
+      if (warp_rescale) rescale_o_row<D>(t_o, alpha);
+      l = l * alpha + ((acc01.x + acc01.y) + (acc23.x + acc23.y));
+      m = m_use;
+      fresh = false;
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bars + 8 * (C::B_PFULL + grp));
+    }
+    if (!ok) break;
+    ok = __all_sync(0xffffffffu,
+                    mbar_wait(bars + 8 * (C::B_OREADY + grp), oi & 1, abort_flag, a.status));
+    if (!ok) break;
+    ++oi;
+    tc_fence_after();
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const size_t row = (size_t)i * a.H + w.h;
+    constexpr int CW = D < 32 ? D : 32, PER = D / CW >= 2 ? 2 : 1;
+#pragma unroll
+    for (int c0 = 0; c0 < D; c0 += CW * PER) {
+      uint32_t u[CW * PER];
+#pragma unroll
+      for (int p = 0; p < PER; ++p) tmem_ld_cols<CW>(t_o + c0 + p * CW, u + p * CW);
+      tmem_wait_ld();
+#pragma unroll
+      for (int p = 0; p < PER; ++p) reg_fence_cols<CW>(u + p * CW);
+      if (c0 + CW * PER >= D) {
+        tc_fence_before();
+        mbar_arrive(bars + 8 * (C::B_OFREE + grp));
+      }
+      if (!row_ok) continue;
+#pragma unroll
+      for (int c = 0; c < CW * PER; c += 16) {
+        uint32_t p[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          p[k] = pack_bf16x2(__uint_as_float(u[c + 2 * k]) * inv,
+                             __uint_as_float(u[c + 2 * k + 1]) * inv);
+        bf16* dst = a.out + row * D + c0 + c;
+        if (a.out_v8) {
+          st_global_v8(dst, p);
+        } else {
+          reinterpret_cast<uint4*>(dst)[0] = make_uint4(p[0], p[1], p[2], p[3]);
+          reinterpret_cast<uint4*>(dst)[1] = make_uint4(p[4], p[5], p[6], p[7]);
+        }
+      }
+    }
+    if (a.lse && row_ok)
+      a.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_fwd_kernel(const __grid_constant__ CUtensorMap tmQ,
+                      const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const FwdArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw);
+  const uint32_t bars = sbase + C::OFF_BAR;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  volatile int* skip = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    *skip = *a.status != 0;   // an error recorded earlier makes the launch a no-op
+    for (int i = 0; i < C::NUM_BARS; ++i) {
+      uint32_t n = 1;
+      if (i >= C::B_PFULL && i < C::B_PFULL + 2) n = kGroup;
+      if (i >= C::B_OFREE && i < C::B_OFREE + 2) n = kGroup;
+      if (i >= C::B_VREADY && i < C::B_VREADY + C::KVS) n = 32;
+      // Readers of the ring: two producer threads, the MMA thread, both groups, the padding warp.
+      if (i >= C::B_RINGEMPTY) n = 3 + 2 * kGroup + (a.valid ? 32 : 0);
+      mbar_init(bars + 8 * i, n);
+    }
+    *abort_flag = 0;
+    mbar_fence_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_map(&tmQ);
+    tma_prefetch_map(&tmK);
+    tma_prefetch_map(&tmV);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Ring ring{reinterpret_cast<volatile int*>(smem + C::OFF_RING), bars + 8 * C::B_RINGFULL,
+            bars + 8 * C::B_RINGEMPTY, 0u};
+  if (!*skip) {
+    if (warp == 0) {
+      if (lane < 2)
+        producer_role<D>(&tmQ, lane == 1 ? &tmV : &tmK, a, sbase, bars, abort_flag, lane == 1,
+                         ring);
+    } else if (warp == 1) {
+      if (lane == 0) mma_role<D>(a, sbase, bars, tmem, abort_flag, ring);
+    } else if (warp < 10) {
+      softmax_role<D>(a, bars, tmem, abort_flag, warp, lane, ring);
+    } else if (warp == 10) {
+      if (a.valid) padding_role<D>(a, sbase, bars, abort_flag, lane, ring);
+    } else if (lane == 0) {
+      claim_role(a, ring, abort_flag);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+template <int D>
+int launch_fwd(FwdArgs a, const void* q, const void* k, const void* v, int Hkv, int64_t qs,
+               int64_t ks, int64_t vs, int dev, int sms, cudaStream_t st) {
+  using C = Cfg<D>;
+  static std::atomic<bool> set[64];
+  if (!set[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(window_fwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::SMEM_ALLOC) != cudaSuccess)
+      return JCA_ERR_CUDA;
+    set[dev].store(true, std::memory_order_release);
+  }
+  CUtensorMap tmQ, tmK, tmV;
+  if (!make_strided_map_bf16(&tmQ, q, a.T, a.H, D, qs, C::BM) ||
+      !make_strided_map_bf16(&tmK, k, a.T, Hkv, D, ks, C::BN) ||
+      !make_strided_map_bf16(&tmV, v, a.T, Hkv, D, vs, C::BN))
+    return JCA_ERR_CUDA;
+  const int grid = a.n_items < sms ? a.n_items : sms;
+  window_fwd_kernel<D><<<grid, kThreads, C::SMEM_ALLOC, st>>>(tmQ, tmK, tmV, a);
+  return cudaGetLastError() == cudaSuccess ? JCA_OK : JCA_ERR_CUDA;
+}
+
+struct FwdLayout {
+  size_t row_start = 0, counter = 0, total = 0;
+};
+
+FwdLayout fwd_layout(int64_t T) {
+  FwdLayout L;
+  L.counter = align_up(4 * (size_t)T, 256);
+  L.total = L.counter + 256;
   return L;
 }
 
+}  // namespace
+
 bool window_sizes_ok(int64_t B, int64_t T, int H, int Hkv, int n_sinks) {
   return B >= 0 && T >= 0 && T < (int64_t)INT_MAX - kItemRows && B < (int64_t)INT_MAX && H >= 1 &&
-         H < 65536 && Hkv >= 1 && H % Hkv == 0 && n_sinks >= 0 && n_sinks <= kMaxSinks &&
-         (B > 0 || T == 0);
+         H < 65536 && Hkv >= 1 && H % Hkv == 0 && n_sinks >= 0 && n_sinks <= kWindowMaxSinks &&
+         (B > 0 || T == 0) && (T / kTileM + 1) * H < (int64_t)INT_MAX;
 }
 
 int window_check(int64_t B, int64_t T, int H, int Hkv, int d, int64_t window, int n_sinks,
@@ -216,24 +743,29 @@ int window_check(int64_t B, int64_t T, int H, int Hkv, int d, int64_t window, in
   if (idx_bits != 32 && idx_bits != 64) return JCA_ERR_IDX_BITS;
   if (!head_dim_ok(d)) return JCA_ERR_HEAD_DIM;
   if (!window_sizes_ok(B, T, H, Hkv, n_sinks) || window < 1) return JCA_ERR_SHAPE;
-  if (qs < (int64_t)H * d || ks < (int64_t)Hkv * d || vs < (int64_t)Hkv * d) return JCA_ERR_SHAPE;
+  const int64_t far = (int64_t)1 << 38;   // row strides of a tensor map stay below 2^40 bytes
+  if (qs < (int64_t)H * d || ks < (int64_t)Hkv * d || vs < (int64_t)Hkv * d || qs >= far ||
+      ks >= far || vs >= far)
+    return JCA_ERR_SHAPE;
   if (qs % 8 || ks % 8 || vs % 8) return JCA_ERR_ALIGN;
   return JCA_OK;
 }
 
 int window_plan(const void* offsets, int64_t B, int64_t T, int idx_bits, int32_t* row_start,
-                int32_t* row_end, int32_t* status, cudaStream_t st) {
+                int32_t* row_end, int32_t* counters, int n_counters, int32_t* status,
+                cudaStream_t st) {
   const unsigned grid = (unsigned)(B < (1 << 20) ? B : (1 << 20));
   if (idx_bits == 32)
     window_plan_kernel<int32_t><<<grid, 128, 0, st>>>(static_cast<const int32_t*>(offsets), B, T,
-                                                      row_start, row_end, status);
+                                                      row_start, row_end, counters, n_counters,
+                                                      status);
   else
     window_plan_kernel<int64_t><<<grid, 128, 0, st>>>(static_cast<const int64_t*>(offsets), B, T,
-                                                      row_start, row_end, status);
+                                                      row_start, row_end, counters, n_counters,
+                                                      status);
   return cudaGetLastError() == cudaSuccess ? JCA_OK : JCA_ERR_CUDA;
 }
 
-}  // namespace
 }  // namespace jca
 
 using namespace jca;
@@ -241,13 +773,7 @@ using namespace jca;
 extern "C" size_t jca_window_workspace_bytes(int64_t B, int64_t T, int H, int Hkv, int d_head,
                                              int n_sinks) {
   if (!window_sizes_ok(B, T, H, Hkv, n_sinks) || !head_dim_ok(d_head)) return 0;
-  return window_layout(T, false).total;
-}
-
-extern "C" size_t jca_window_bwd_workspace_bytes(int64_t B, int64_t T, int H, int Hkv, int d_head,
-                                                 int n_sinks) {
-  if (!window_sizes_ok(B, T, H, Hkv, n_sinks) || !head_dim_ok(d_head)) return 0;
-  return window_layout(T, true).total;
+  return fwd_layout(T).total;
 }
 
 extern "C" int jagged_window_attn_fwd(const void* q, const void* k, const void* v, void* out,
@@ -265,7 +791,7 @@ extern "C" int jagged_window_attn_fwd(const void* q, const void* k, const void* 
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
       !aligned(lse, 4) || !aligned(workspace, 256))
     return JCA_ERR_ALIGN;
-  const WindowLayout L = window_layout(T, false);
+  const FwdLayout L = fwd_layout(T);
   if (workspace_bytes < L.total) return JCA_ERR_WORKSPACE;
   if (B == 0) return JCA_OK;
   int dev = 0, sms = 0;
@@ -273,104 +799,28 @@ extern "C" int jagged_window_attn_fwd(const void* q, const void* k, const void* 
   if (rc) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
-  WindowArgs a = {};
-  a.q = static_cast<const bf16*>(q);
-  a.k = static_cast<const bf16*>(k);
-  a.v = static_cast<const bf16*>(v);
-  a.o = static_cast<bf16*>(out);
-  a.lse_out = lse;
-  a.valid = valid;
-  a.row_start = reinterpret_cast<int32_t*>(ws + L.row_start);
-  a.status = status;
-  a.T = T;
-  a.q_stride = q_stride;
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
-  a.H = H;
-  a.Hkv = Hkv;
-  a.window = (int)(window < T ? window : (T > 0 ? T : 1));
-  a.n_sinks = n_sinks;
-  a.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)d_head);
-  rc = window_plan(offsets, B, T, idx_bits, reinterpret_cast<int32_t*>(ws + L.row_start), nullptr,
-                   status, st);
-  if (rc || T == 0) return rc;
-  const int64_t blocks = (T * H + 3) / 4;
-  if (blocks >= (int64_t)INT_MAX) return JCA_ERR_SHAPE;
-  switch (d_head) {
-    case 16: window_fwd_kernel<16><<<(unsigned)blocks, 128, 0, st>>>(a); break;
-    case 32: window_fwd_kernel<32><<<(unsigned)blocks, 128, 0, st>>>(a); break;
-    case 64: window_fwd_kernel<64><<<(unsigned)blocks, 128, 0, st>>>(a); break;
-    default: window_fwd_kernel<128><<<(unsigned)blocks, 128, 0, st>>>(a); break;
-  }
-  return cudaGetLastError() == cudaSuccess ? JCA_OK : JCA_ERR_CUDA;
-}
-
-namespace jca {
-namespace {
-template <int D>
-void launch_window_bwd(const WindowArgs& a, cudaStream_t st) {
-  window_dq_kernel<D><<<(unsigned)((a.T * a.H + 3) / 4), 128, 0, st>>>(a);
-  window_dkv_kernel<D><<<(unsigned)((a.T * a.Hkv + 3) / 4), 128, 0, st>>>(a);
-}
-}  // namespace
-}  // namespace jca
-
-extern "C" int jagged_window_attn_bwd(const void* q, const void* k, const void* v, const void* out,
-                                      const void* dout, const float* lse, void* dq, void* dk,
-                                      void* dv, const void* offsets, const uint8_t* valid,
-                                      int64_t B, int64_t T, int H, int Hkv, int d_head,
-                                      int64_t window, int n_sinks, int64_t q_stride,
-                                      int64_t k_stride, int64_t v_stride, float scale,
-                                      int idx_bits, void* workspace, size_t workspace_bytes,
-                                      int32_t* status, jca_stream_t stream) {
-  int rc = window_check(B, T, H, Hkv, d_head, window, n_sinks, q_stride, k_stride, v_stride,
-                        idx_bits);
-  if (rc) return rc;
-  if (!status || !offsets || !workspace) return JCA_ERR_NULL;
-  if (T > 0 && (!q || !k || !v || !out || !dout || !lse || !dq || !dk || !dv)) return JCA_ERR_NULL;
-  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
-      !aligned(dout, 16) || !aligned(lse, 4) || !aligned(dq, 16) || !aligned(dk, 16) ||
-      !aligned(dv, 16) || !aligned(workspace, 256))
-    return JCA_ERR_ALIGN;
-  const WindowLayout L = window_layout(T, true);
-  if (workspace_bytes < L.total) return JCA_ERR_WORKSPACE;
-  if (B == 0) return JCA_OK;
-  int dev = 0, sms = 0;
-  rc = current_device(&dev, &sms);
-  if (rc) return rc;
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  char* ws = static_cast<char*>(workspace);
-  WindowArgs a = {};
-  a.q = static_cast<const bf16*>(q);
-  a.k = static_cast<const bf16*>(k);
-  a.v = static_cast<const bf16*>(v);
-  a.out = static_cast<const bf16*>(out);
-  a.dout = static_cast<const bf16*>(dout);
+  FwdArgs a = {};
+  a.out = static_cast<bf16*>(out);
   a.lse = lse;
-  a.dq = static_cast<bf16*>(dq);
-  a.dk = static_cast<bf16*>(dk);
-  a.dv = static_cast<bf16*>(dv);
   a.valid = valid;
   a.row_start = reinterpret_cast<int32_t*>(ws + L.row_start);
-  a.row_end = reinterpret_cast<int32_t*>(ws + L.row_end);
+  a.counter = reinterpret_cast<int32_t*>(ws + L.counter);
   a.status = status;
-  a.T = T;
-  a.q_stride = q_stride;
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
+  a.T = (int)T;
   a.H = H;
-  a.Hkv = Hkv;
+  a.group = H / Hkv;
   a.window = (int)(window < T ? window : (T > 0 ? T : 1));
   a.n_sinks = n_sinks;
-  a.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)d_head);
-  rc = window_plan(offsets, B, T, idx_bits, reinterpret_cast<int32_t*>(ws + L.row_start),
-                   reinterpret_cast<int32_t*>(ws + L.row_end), status, st);
+  a.n_items = (int)((T + kItemRows - 1) / kItemRows) * H;
+  a.out_v8 = aligned(out, 32) ? 1 : 0;
+  a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)d_head)) * 1.4426950408889634f;
+  rc = window_plan(offsets, B, T, idx_bits, reinterpret_cast<int32_t*>(ws + L.row_start), nullptr,
+                   a.counter, 1, status, st);
   if (rc || T == 0) return rc;
   switch (d_head) {
-    case 16: launch_window_bwd<16>(a, st); break;
-    case 32: launch_window_bwd<32>(a, st); break;
-    case 64: launch_window_bwd<64>(a, st); break;
-    default: launch_window_bwd<128>(a, st); break;
+    case 16: return launch_fwd<16>(a, q, k, v, Hkv, q_stride, k_stride, v_stride, dev, sms, st);
+    case 32: return launch_fwd<32>(a, q, k, v, Hkv, q_stride, k_stride, v_stride, dev, sms, st);
+    case 64: return launch_fwd<64>(a, q, k, v, Hkv, q_stride, k_stride, v_stride, dev, sms, st);
+    default: return launch_fwd<128>(a, q, k, v, Hkv, q_stride, k_stride, v_stride, dev, sms, st);
   }
-  return cudaGetLastError() == cudaSuccess ? JCA_OK : JCA_ERR_CUDA;
 }
