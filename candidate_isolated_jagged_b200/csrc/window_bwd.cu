@@ -1,9 +1,38 @@
-// Causal attention over packed rows with a sliding window and first tokens that stay visible:
-// forward and backward (include/jca.h states the mask and the layout).
+// Backward pass of the causal attention with a sliding window and visible first tokens (window.cu;
+// include/jca.h states the mask and the layout).
+//
+// Mathematics, with P rebuilt tile by tile from the forward's log-sum-exp:
+//   dV = P^T dO,   dS = P * (dO V^T - D),  D = rowsum(dO * O),   dQ = scale dS K,   dK = scale dS^T Q,
+// dK and dV of a key head summed over its query heads. Three disjoint parts, no atomics:
+//   * dQ: a 128-row query tile of one head walks the key tiles that the forward walks;
+//   * dKV: a 128-row key tile of one key head walks the query tiles that see it through the window
+//     (rows j <= i < min(j + window, end)) for each of its query heads;
+//   * first tokens are also seen from behind their window, by every later row of the user: a unit
+//     takes a user's first tokens as its key tile and walks up to kChunk of those rows, leaving an
+//     fp32 partial sum that the dKV unit of those keys adds in chunk order. Without this
+//     split one key tile would walk a whole long history for its few first tokens.
+// Row tiles are cut from the packed rows whatever users they hold, as in the forward.
+//
+// Kernel (one persistent block per SM, 12 warps; tcgen05 with TMEM accumulators, TMA loads). O1/O2 are
+// the unit's outer tiles, I1/I2 the inner tiles streamed through a ring:
+//   S = O1 I1^T,  dP = O2 I2^T  (SS MMAs)   ->   dS (and P) as bf16 in TMEM   ->   TS MMAs
+//   dQ  (O1 = Q, O2 = dO, I1 = K, I2 = V):   acc0 += dS I1
+//   dKV (O1 = K, O2 = V, I1 = Q, I2 = dO):   acc0 (dV) += P^T I2,  acc1 (dK) += dS^T I1
+// An inner tile is taken as two half steps of 64 rows, so that S and dP fit twice in TMEM and the
+// tensor core works on step t + 1 while the compute warps do step t. Columns a warp's rows do not
+// see are decided per 32 columns: none (zeros are written), all (no masking) or some.
+//   warp 0      TMA loads;  warp 1  MMA issue (one thread);  warps 2..9  compute, a row a thread,
+//   two warps per 32 rows (32 of the 64 columns each);  warp 10  with padding: zeroes the padding
+//   rows of the inner tiles;  warp 11  claims units and posts them to a ring.
+//
+// What bounds it: seven products per pair instead of five (S and dP are formed in both passes) on
+// the tensor core, whose 64-column steps cost the issuing thread about what 128-column ones would.
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -16,134 +45,848 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-struct WindowArgs {
-  const bf16* q;
-  const bf16* k;
-  const bf16* v;
-  const bf16* out;
-  const bf16* dout;
-  const float* lse;
-  bf16* o;
-  float* lse_out;
+constexpr int kDQ = 0, kDKV = 1, kSink = 2;   // kSink: dKV of first tokens from behind the window
+constexpr int kThreads = 384;
+constexpr int kCompute = 256;
+constexpr int kStages = 2;
+constexpr int kHalf = 64;        // inner rows of a half step
+constexpr int kChunk = 1024;     // query rows of a kSink unit
+constexpr int kRing = 4;
+constexpr int kEntry = 6;        // ints of a ring entry
+
+struct BwdArgs {
   bf16* dq;
   bf16* dk;
   bf16* dv;
-  const uint8_t* valid;
-  const int32_t* row_start;   // [T] first row of the row's user
-  const int32_t* row_end;     // [T] one past its last
-  const int32_t* status;
-  int64_t T, q_stride, k_stride, v_stride;
-  int H, Hkv, window, n_sinks;
-  float scale;
-};
-
-// One warp per (row, head); lane l holds elements l * EPL ... of the head.
-template <int D>
-struct Row {
-  static constexpr int EPL = D >= 32 ? D / 32 : 1;
-  float x[EPL];
-  __device__ __forceinline__ void load(const bf16* p, int lane) {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i)
-      x[i] = lane * EPL < D ? __bfloat162float(p[lane * EPL + i]) : 0.f;
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) x[i] = 0.f;
-  }
-  __device__ __forceinline__ float dot(const Row& o) const {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) s = fmaf(x[i], o.x[i], s);
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-    return s;
-  }
-  __device__ __forceinline__ void axpy(float a, const Row& o) {
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) x[i] = fmaf(a, o.x[i], x[i]);
-  }
-  __device__ __forceinline__ void store(bf16* p, float a, int lane) const {
-    if (lane * EPL < D)
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) p[lane * EPL + i] = __float2bfloat16(x[i] * a);
-  }
+  const uint8_t* valid;       // [T] or null
+  const int32_t* row_start;   // [T]
+  const int32_t* row_end;     // [T]
+  const int32_t* row_user;    // [T], with first tokens
+  const float* lse2;          // [H][T] log2 units; +inf: the row sees no key
+  const float* dsum;          // [H][T] D
+  float* part;                // kSink partials [slot][Hkv][n_sinks][2][D]: dV, dK / scale
+  const int4* sinks;          // kSink units {first row, end, chunk, slot}
+  const int32_t* n_sink_units;
+  int32_t* counter;
+  int32_t* status;
+  int T, H, Hkv, group, window, n_sinks, n_units;
+  float scale, scale_log2;
 };
 
 template <int D>
-__global__ void __launch_bounds__(128) window_dq_kernel(const WindowArgs a) {
-  if (*a.status != 0) return;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = blockIdx.x * (int64_t)4 + (threadIdx.x >> 5);
-  if (w >= a.T * a.H) return;
-  const int64_t i = w / a.H;
-  const int h = (int)(w % a.H), hk = h / (a.H / a.Hkv);
-  Row<D> q, dov, acc, x;
-  acc.zero();
-  if (!a.valid || a.valid[i]) {
-    q.load(a.q + i * a.q_stride + (int64_t)h * D, lane);
-    dov.load(a.dout + (i * a.H + h) * D, lane);
-    x.load(a.out + (i * a.H + h) * D, lane);
-    const float dl = dov.dot(x), lse = a.lse[i * a.H + h];
-    const int64_t s = a.row_start[i];
-    const int64_t lo = max(s, i - a.window + 1);
-    const int64_t first = min(s + a.n_sinks, lo);
-    for (int64_t j = s; j <= i; ++j) {
-      if (j == first && first < lo) j = lo;
-      if (a.valid && !a.valid[j]) continue;
-      x.load(a.v + j * a.v_stride + (int64_t)hk * D, lane);
-      const float dp = dov.dot(x);
-      x.load(a.k + j * a.k_stride + (int64_t)hk * D, lane);
-      const float p = __expf(q.dot(x) * a.scale - lse);
-      acc.axpy(p * (dp - dl), x);
-    }
+struct Cfg {
+  static constexpr int BM = kTileM;
+  static constexpr int ROW_BYTES = D * 2;
+  static constexpr int SW = ROW_BYTES >= 128 ? 128 : ROW_BYTES;
+  static constexpr int NBLK = ROW_BYTES / SW;
+  static constexpr int BOX_X = SW / 2;
+  static constexpr int TILE_BYTES = BM * ROW_BYTES;
+  static constexpr int BLK_BYTES = BM * SW;
+  static constexpr uint32_t LAYOUT = SW == 128 ? 2u : (SW == 64 ? 4u : 6u);
+  static constexpr int KSTEPS_QK = D / 16;
+  static constexpr int KSTEPS_PER_BLK = SW / 32;
+  static constexpr int OFF_OUT = 0;                                   // 2 tiles
+  static constexpr int OFF_IN = 2 * TILE_BYTES;                       // kStages x 2 tiles
+  static constexpr int OFF_BAR = OFF_IN + kStages * 2 * TILE_BYTES;
+  static constexpr int B_OUTFULL = 0;
+  static constexpr int B_OUTEMPTY = 1;
+  static constexpr int B_INFULL = 2;                                  // [kStages]
+  static constexpr int B_INREADY = B_INFULL + kStages;                // padding rows zeroed
+  static constexpr int B_INEMPTY = B_INREADY + kStages;
+  static constexpr int B_SPFULL = B_INEMPTY + kStages;                // [2] S and dP written
+  static constexpr int B_DSFULL = B_SPFULL + 2;                       // [2] dS (and P) written
+  static constexpr int B_ACCFULL = B_DSFULL + 2;
+  static constexpr int B_ACCFREE = B_ACCFULL + 1;
+  static constexpr int B_COLS = B_ACCFREE + 1;                        // [2] column statistics
+  static constexpr int B_DRAIN = B_COLS + 2;
+  static constexpr int B_RINGFULL = B_DRAIN + 1;
+  static constexpr int B_RINGEMPTY = B_RINGFULL + kRing;
+  static constexpr int NUM_BARS = B_RINGEMPTY + kRing;
+  static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+  static constexpr int OFF_RING = OFF_MISC + 16;
+  static constexpr int OFF_COLS = (OFF_RING + kRing * kEntry * 4 + 15) / 16 * 16;   // [2][2][128]
+  static constexpr int SMEM_USED = OFF_COLS + 2 * 2 * BM * 4;
+  static constexpr int SMEM_RAW = SMEM_USED + 1024;
+  // At least 120 KB so that a second block never shares the SM (and its TMEM).
+  static constexpr int SMEM_ALLOC = SMEM_RAW > 120 * 1024 ? SMEM_RAW : 120 * 1024;
+  static constexpr uint32_t TMEM_S = 0, TMEM_P = 64, TMEM_BUF = 128, TMEM_A0 = 256,
+                            TMEM_A1 = 384, TMEM_COLS = 512;
+  static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory budget");
+};
+
+// A unit as every role derives it from a ring entry. Inner tile i is rows [in_row(i), + in_valid(i))
+// of head in_head(i).
+struct Unit {
+  int orow0, oh;                // outer rows and head (dQ: query head, else key head)
+  int n_in;
+  int base, n_run;              // inner tiles: n_run of 128 rows from base on, per head
+  int end;                      // dKV, kSink: inner rows stop here
+  int sink0, n_sink;            // dQ: rows of the first tokens' tile, which comes first
+  int slot, uend;               // kSink: partial sum's slot, end of the user
+};
+
+template <int MODE>
+__device__ __forceinline__ Unit make_unit(const volatile int* e, const BwdArgs& a) {
+  Unit u;
+  u.orow0 = e[0];
+  u.oh = e[1];
+  u.sink0 = u.n_sink = u.slot = u.uend = 0;
+  if (MODE == kDQ) {
+    const int lo = e[2], start = e[3];
+    u.base = lo & ~(kTileN - 1);
+    u.sink0 = start;
+    u.n_sink = max(0, min(a.n_sinks, u.base - start));
+    u.n_run = (u.orow0 + kTileM - u.base) / kTileN;
+    u.end = a.T;
+    u.n_in = u.n_run + (u.n_sink ? 1 : 0);
+  } else {
+    u.base = e[2];
+    u.end = e[3];
+    u.n_run = (u.end - u.base + kTileN - 1) / kTileN;
+    u.n_in = u.n_run * a.group;
+    u.slot = e[4];
+    u.uend = e[5];
   }
-  acc.store(a.dq + (i * a.H + h) * D, a.scale, lane);
+  return u;
 }
 
-template <int D>
-__global__ void __launch_bounds__(128) window_dkv_kernel(const WindowArgs a) {
-  if (*a.status != 0) return;
-  const int lane = threadIdx.x & 31;
-  const int64_t w = blockIdx.x * (int64_t)4 + (threadIdx.x >> 5);
-  if (w >= a.T * a.Hkv) return;
-  const int64_t j = w / a.Hkv;
-  const int hk = (int)(w % a.Hkv), G = a.H / a.Hkv;
-  Row<D> k, v, dk, dv, x, y;
-  dk.zero();
-  dv.zero();
-  if (!a.valid || a.valid[j]) {
-    k.load(a.k + j * a.k_stride + (int64_t)hk * D, lane);
-    v.load(a.v + j * a.v_stride + (int64_t)hk * D, lane);
-    const int64_t s = a.row_start[j], e = a.row_end[j];
-    const int64_t end = j - s < a.n_sinks ? e : min(e, j + a.window);
-    for (int64_t i = j; i < end; ++i) {
-      if (a.valid && !a.valid[i]) continue;
-      for (int h = hk * G; h < hk * G + G; ++h) {
-        x.load(a.dout + (i * a.H + h) * D, lane);
-        y.load(a.out + (i * a.H + h) * D, lane);
-        const float dl = x.dot(y), dp = x.dot(v);
-        y.load(a.q + i * a.q_stride + (int64_t)h * D, lane);
-        const float p = __expf(y.dot(k) * a.scale - a.lse[i * a.H + h]);
-        dv.axpy(p, x);
-        dk.axpy(p * (dp - dl), y);
+template <int MODE>
+__device__ __forceinline__ int in_row(const Unit& u, int i) {
+  if (MODE == kDQ) {
+    if (!u.n_sink) return u.base + i * kTileN;
+    return i == 0 ? u.sink0 : u.base + (i - 1) * kTileN;
+  }
+  return u.base + (i % u.n_run) * kTileN;
+}
+template <int MODE>
+__device__ __forceinline__ int in_head(const Unit& u, int i, const BwdArgs& a) {
+  return MODE == kDQ ? u.oh / a.group : u.oh * a.group + i / u.n_run;
+}
+template <int MODE>
+__device__ __forceinline__ int in_valid(const Unit& u, int i) {
+  if (MODE == kDQ && u.n_sink && i == 0) return u.n_sink;
+  return min(kTileN, u.end - in_row<MODE>(u, i));
+}
+
+struct Ring {
+  volatile int* slot;
+  uint32_t full, empty, k;
+};
+
+template <int MODE>
+__device__ __forceinline__ bool ring_take(Ring& r, const BwdArgs& a, Unit& u,
+                                          volatile int* abort_flag, bool& ok) {
+  const int s = (int)(r.k % kRing);
+  ok = mbar_wait(r.full + 8 * s, (r.k / kRing) & 1, abort_flag, a.status);
+  if (!ok) return false;
+  const volatile int* e = r.slot + kEntry * s;
+  const bool more = e[0] >= 0;
+  if (more) u = make_unit<MODE>(e, a);
+  mbar_arrive(r.empty + 8 * s);
+  ++r.k;
+  return more;
+}
+
+template <int MODE>
+__device__ void claim_role(const BwdArgs& a, Ring r, volatile int* abort_flag) {
+  const int heads = MODE == kDQ ? a.H : a.Hkv;
+  const int n = MODE == kSink ? *a.n_sink_units * heads : a.n_units;
+  for (;;) {
+    const int v = atomicAdd(a.counter, 1);
+    int e[kEntry] = {-1, 0, 0, 0, 0, 0};
+    if (v < n) {
+      e[1] = v % heads;
+      if (MODE == kSink) {
+        const int4 x = a.sinks[v / heads];   // {first row, end, chunk, slot}
+        e[0] = x.x;
+        e[2] = max(x.x + a.window, x.z * kChunk) & ~(kTileN - 1);
+        e[3] = (int)min((long long)x.y, (long long)(x.z + 1) * kChunk);
+        e[4] = x.w;
+        e[5] = x.y;
+      } else {
+        // Under a long window the later query tiles and the earlier key tiles are the longer units.
+        const int t = MODE == kDQ ? (n - 1 - v) / heads : v / heads;
+        e[0] = t * kTileM;
+        if (MODE == kDQ) {
+          e[3] = a.row_start[e[0]];
+          e[2] = max(e[3], e[0] - a.window + 1);
+        } else {
+          const int last = min(e[0] + kTileM, a.T) - 1;
+          e[2] = e[0];
+          e[3] = (int)min((long long)a.row_end[last], (long long)last + a.window);
+        }
+      }
+    }
+    const int s = (int)(r.k % kRing);
+    if (!mbar_wait(r.empty + 8 * s, ((r.k / kRing) & 1) ^ 1, abort_flag, a.status)) return;
+#pragma unroll
+    for (int i = 0; i < kEntry; ++i) r.slot[kEntry * s + i] = e[i];
+    mbar_arrive(r.full + 8 * s);
+    ++r.k;
+    if (e[0] < 0) return;
+  }
+}
+
+template <int D, int MODE>
+__device__ void producer_role(const CUtensorMap* tmO1, const CUtensorMap* tmO2,
+                              const CUtensorMap* tmI1, const CUtensorMap* tmI2, const BwdArgs& a,
+                              uint32_t sbase, uint32_t bars, volatile int* abort_flag, Ring ring) {
+  using C = Cfg<D>;
+  uint32_t units = 0, g = 0;
+  bool ok = true;
+  Unit u;
+  while (ok && ring_take<MODE>(ring, a, u, abort_flag, ok)) {
+    for (int i = 0; i < u.n_in; ++i) {
+      const int s = (int)(g % kStages);
+      ok = mbar_wait(bars + 8 * (C::B_INEMPTY + s), ((g / kStages) & 1) ^ 1, abort_flag, a.status);
+      if (!ok) break;
+      mbar_arrive_expect_tx(bars + 8 * (C::B_INFULL + s), 2 * C::TILE_BYTES);
+      const uint32_t dst = sbase + C::OFF_IN + s * 2 * C::TILE_BYTES;
+      const int row = in_row<MODE>(u, i), h = in_head<MODE>(u, i, a);
+#pragma unroll
+      for (int c = 0; c < C::NBLK; ++c) {
+        tma_load_3d(dst + c * C::BLK_BYTES, tmI1, bars + 8 * (C::B_INFULL + s), c * C::BOX_X, h,
+                    row);
+        tma_load_3d(dst + C::TILE_BYTES + c * C::BLK_BYTES, tmI2, bars + 8 * (C::B_INFULL + s),
+                    c * C::BOX_X, h, row);
+      }
+      ++g;
+      if (i > 0) continue;
+      // The outer tiles go out behind the unit's first inner tiles, whose stage was freed earlier.
+      ok = mbar_wait(bars + 8 * C::B_OUTEMPTY, (units & 1) ^ 1, abort_flag, a.status);
+      if (!ok) break;
+      mbar_arrive_expect_tx(bars + 8 * C::B_OUTFULL, 2 * C::TILE_BYTES);
+      ++units;
+#pragma unroll
+      for (int c = 0; c < C::NBLK; ++c) {
+        tma_load_3d(sbase + C::OFF_OUT + c * C::BLK_BYTES, tmO1, bars + 8 * C::B_OUTFULL,
+                    c * C::BOX_X, u.oh, u.orow0);
+        tma_load_3d(sbase + C::OFF_OUT + C::TILE_BYTES + c * C::BLK_BYTES, tmO2,
+                    bars + 8 * C::B_OUTFULL, c * C::BOX_X, u.oh, u.orow0);
       }
     }
   }
-  dk.store(a.dk + (j * a.Hkv + hk) * D, a.scale, lane);
-  dv.store(a.dv + (j * a.Hkv + hk) * D, 1.f, lane);
+  if (!ok) {
+    // Aborting: let the copies this thread started land before the block exits.
+    if (units > 0) mbar_wait_drain(bars + 8 * C::B_OUTFULL, (units - 1) & 1);
+    for (uint32_t n = g > (uint32_t)kStages ? g - kStages : 0; n < g; ++n)
+      mbar_wait_drain(bars + 8 * (C::B_INFULL + (int)(n % kStages)), (n / kStages) & 1);
+  }
+}
+
+// Zeroes the rows of padding in both inner tiles; one warp.
+template <int D, int MODE>
+__device__ void padding_role(const BwdArgs& a, uint32_t sbase, uint32_t bars,
+                             volatile int* abort_flag, int lane, Ring ring) {
+  using C = Cfg<D>;
+  constexpr int CH = C::ROW_BYTES / 16, CB = C::SW / 16;
+  uint32_t g = 0;
+  bool ok = true;
+  Unit u;
+  for (;;) {
+    const bool more = ring_take<MODE>(ring, a, u, abort_flag, ok);
+    if (!__all_sync(0xffffffffu, more)) return;
+    for (int i = 0; i < u.n_in; ++i, ++g) {
+      const int s = (int)(g % kStages), row = in_row<MODE>(u, i);
+      uint32_t pad[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int k = row + 32 * c + lane;
+        pad[c] = __ballot_sync(0xffffffffu, k < a.T && !a.valid[k]);
+      }
+      ok = mbar_wait(bars + 8 * (C::B_INFULL + s), (g / kStages) & 1, abort_flag, a.status);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      const uint32_t tile = sbase + C::OFF_IN + s * 2 * C::TILE_BYTES;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (!pad[c]) continue;
+        // A row's bytes of a column block are contiguous; the swizzle only reorders them.
+        for (int y = lane; y < 32 * CH; y += 32) {
+          const int r = y / CH, x = y % CH;
+          if (!((pad[c] >> r) & 1)) continue;
+          const uint32_t at =
+              tile + (x / CB) * C::BLK_BYTES + (32 * c + r) * C::SW + (x % CB) * 16;
+          st_shared_v4(at, 0u, 0u, 0u, 0u);
+          st_shared_v4(at + C::TILE_BYTES, 0u, 0u, 0u, 0u);
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bars + 8 * (C::B_INREADY + s));
+    }
+  }
+}
+
+// Half steps of a unit; the second half of an inner tile exists when it has more than 64 rows.
+struct HalfStep {
+  int i, hh, valid;
+};
+
+template <int MODE>
+__device__ __forceinline__ bool next_half(const Unit& u, HalfStep& h) {
+  if (h.hh == 0 && in_valid<MODE>(u, h.i) > kHalf) {
+    h.hh = 1;
+  } else {
+    if (h.i + 1 >= u.n_in) return false;
+    ++h.i;
+    h.hh = 0;
+  }
+  h.valid = min(kHalf, in_valid<MODE>(u, h.i) - h.hh * kHalf);
+  return true;
+}
+
+template <int D, int MODE>
+__device__ void mma_role(const BwdArgs& a, uint32_t sbase, uint32_t bars, uint32_t tmem,
+                         volatile int* abort_flag, Ring ring) {
+  using C = Cfg<D>;
+  constexpr uint32_t kIdescSS = idesc_bf16_f32(C::BM, kHalf, false, false);
+  constexpr uint32_t kIdesc0 = kIdescSS & ~(0x3Fu << 17);
+  constexpr uint32_t kIdescTS = idesc_bf16_f32(C::BM, D, false, true);
+  constexpr uint32_t kHalfRows = (kHalf * C::SW) >> 4;
+  constexpr uint32_t kStep = (16 * C::SW) >> 4;
+  const int infull = a.valid ? C::B_INREADY : C::B_INFULL;
+  const uint64_t o1 = smem_desc(sbase + C::OFF_OUT, 16, 8 * C::SW, C::LAYOUT);
+  const uint64_t o2 = o1 + (uint64_t)(C::TILE_BYTES >> 4);
+  const uint64_t in_k = smem_desc(sbase + C::OFF_IN, 16, 8 * C::SW, C::LAYOUT);
+  const uint64_t in_mn = smem_desc(sbase + C::OFF_IN, C::BLK_BYTES, 8 * C::SW, C::LAYOUT);
+  uint32_t units = 0, g = 0, steps = 0, ts_steps = 0, acc_units = 0;
+  bool ok = true;
+  Unit u;
+  auto ss = [&](uint32_t d_tmem, uint64_t x, uint64_t y, uint32_t idesc) {
+#pragma unroll
+    for (int kk = 0; kk < C::KSTEPS_QK; ++kk) {
+      const uint32_t off = ((kk / C::KSTEPS_PER_BLK) * C::BLK_BYTES +
+                            (kk % C::KSTEPS_PER_BLK) * 32) >> 4;
+      tc_mma(d_tmem, x + off, y + off, idesc, kk > 0 ? 1u : 0u);
+    }
+  };
+  // The pairs of a half step sit in two 16-column runs, one per compute warp of a lane quarter.
+  auto ts = [&](uint32_t acc, uint32_t p, uint64_t y, int ksteps, bool overwrite) {
+    for (int kk = 0; kk < ksteps; ++kk)
+      tc_mma_ts(acc, p + (uint32_t)(kk >> 1) * 32u + (uint32_t)(kk & 1) * 8u,
+                y + (uint64_t)(kk * kStep), kIdescTS, (overwrite && kk == 0) ? 0u : 1u);
+  };
+  auto issue_ss = [&](const HalfStep& h, uint32_t stage) {
+    const uint32_t idesc = kIdesc0 | ((uint32_t)(((h.valid + 15) & ~15) >> 3) << 17);
+    const uint64_t i1 = in_k + (uint64_t)((stage * 2 * C::TILE_BYTES) >> 4) +
+                        (uint64_t)(h.hh * kHalfRows);
+    const uint32_t buf = (steps & 1) * C::TMEM_BUF;
+    ss(tmem + buf + C::TMEM_S, o1, i1, idesc);
+    ss(tmem + buf + C::TMEM_P, o2, i1 + (uint64_t)(C::TILE_BYTES >> 4), idesc);
+    tc_commit(bars + 8 * (C::B_SPFULL + (int)(steps & 1)));
+    ++steps;
+  };
+  auto issue_ts = [&](const HalfStep& h, uint32_t stage, bool first, bool closes) -> bool {
+    if (!mbar_wait(bars + 8 * (C::B_DSFULL + (int)(ts_steps & 1)), (ts_steps >> 1) & 1, abort_flag,
+                   a.status))
+      return false;
+    const uint32_t buf = (ts_steps & 1) * C::TMEM_BUF;
+    ++ts_steps;
+    if (first && acc_units > 0 &&
+        !mbar_wait(bars + 8 * C::B_ACCFREE, (acc_units - 1) & 1, abort_flag, a.status))
+      return false;
+    tc_fence_after();
+    const int ksteps = (h.valid + 15) >> 4;
+    const uint64_t m1 = in_mn + (uint64_t)((stage * 2 * C::TILE_BYTES) >> 4) +
+                        (uint64_t)(h.hh * kHalfRows);
+    if (MODE == kDQ) {
+      ts(tmem + C::TMEM_A0, tmem + buf + C::TMEM_P, m1, ksteps, first);
+    } else {
+      ts(tmem + C::TMEM_A0, tmem + buf + C::TMEM_S, m1 + (uint64_t)(C::TILE_BYTES >> 4), ksteps,
+         first);
+      ts(tmem + C::TMEM_A1, tmem + buf + C::TMEM_P, m1, ksteps, first);
+    }
+    if (closes) tc_commit(bars + 8 * (C::B_INEMPTY + (int)stage));
+    return true;
+  };
+  auto wait_in = [&](uint32_t stage) -> bool {
+    if (!mbar_wait(bars + 8 * (infull + (int)stage), (g / kStages) & 1, abort_flag, a.status))
+      return false;
+    tc_fence_after();
+    return true;
+  };
+  while (ok && ring_take<MODE>(ring, a, u, abort_flag, ok)) {
+    // One half step of lookahead: S/dP of step t + 1 are issued before the TS MMAs of step t.
+    HalfStep cur{0, 0, min(kHalf, in_valid<MODE>(u, 0))};
+    uint32_t stage = g % kStages;
+    ok = wait_in(stage);
+    if (!ok) break;
+    ok = mbar_wait(bars + 8 * C::B_OUTFULL, units & 1, abort_flag, a.status);
+    if (!ok) break;
+    ++units;
+    tc_fence_after();
+    issue_ss(cur, stage);
+    bool first = true;
+    for (;;) {
+      HalfStep nxt = cur;
+      const bool more = next_half<MODE>(u, nxt);
+      uint32_t nstage = stage;
+      if (more && nxt.hh == 0) {
+        ++g;
+        nstage = g % kStages;
+        ok = wait_in(nstage);
+        if (!ok) break;
+      }
+      if (more) issue_ss(nxt, nstage);
+      ok = issue_ts(cur, stage, first, !(more && nxt.hh == 1));
+      if (!ok) break;
+      first = false;
+      if (!more) break;
+      cur = nxt;
+      stage = nstage;
+    }
+    if (!ok) break;
+    ++g;
+    tc_commit(bars + 8 * C::B_OUTEMPTY);
+    tc_commit(bars + 8 * C::B_ACCFULL);
+    ++acc_units;
+  }
+  if (!ok) {
+    tc_commit(bars + 8 * C::B_DRAIN);
+    mbar_wait_drain(bars + 8 * C::B_DRAIN, 0);
+  }
+}
+
+// Bits [a, b) of a word, for any a and b.
+__device__ __forceinline__ uint32_t range_bits(int a, int b) {
+  a = min(max(a, 0), 32);
+  b = min(max(b, 0), 32);
+  const uint32_t below_b = b >= 32 ? 0xffffffffu : (1u << b) - 1u;
+  return a >= 32 ? 0u : below_b & (0xffffffffu << a);
+}
+
+__device__ __forceinline__ void store_bf16x8(bf16* p, const float* o) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
+                                            pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+}
+
+template <int D, int MODE>
+__device__ void compute_role(const BwdArgs& a, uint32_t bars, uint32_t tmem, float* cols,
+                             volatile int* abort_flag, int warp, int lane, Ring ring) {
+  using C = Cfg<D>;
+  const int quarter = warp & 3;
+  const int ch = (warp - 2) >> 2;               // 32-column half of every half step
+  const int r = quarter * 32 + lane;            // outer row of this thread inside its tile
+  const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
+  const uint32_t t_s = t_lane + C::TMEM_S + 32 * ch, t_p = t_lane + C::TMEM_P + 32 * ch;
+  constexpr int HD = D / 2;                     // accumulator columns of this warp
+  constexpr int CW = HD < 32 ? HD : 32;
+  const uint32_t t_a0 = t_lane + C::TMEM_A0 + ch * HD, t_a1 = t_lane + C::TMEM_A1 + ch * HD;
+  const float2 sl2v = make_float2(a.scale_log2, a.scale_log2);
+  const size_t T = (size_t)a.T;
+  uint32_t sp_seen = 0, acc_seen = 0, cols_n = 0;
+  bool ok = true;
+  Unit u;
+  for (;;) {
+    const bool more = ring_take<MODE>(ring, a, u, abort_flag, ok);
+    if (!__all_sync(0xffffffffu, more)) break;
+    const int row = u.orow0 + r;                // this thread's row
+    const bool row_ok = row < a.T;
+    const bool real = row_ok && (!a.valid || a.valid[row]);
+    const int start = row_ok ? a.row_start[row] : 0;
+    // Inner rows the outer row pairs with: [lo, hi), and for dQ the first tokens [start, first).
+    int lo = 0, hi = 0, first = start;
+    if (real) {
+      if (MODE == kDQ) {
+        lo = max(start, row - a.window + 1);
+        hi = row + 1;
+        first = min(start + a.n_sinks, lo);
+      } else if (MODE == kDKV) {
+        lo = row;
+        hi = (int)min((long long)a.row_end[row], (long long)row + a.window);
+      } else if (row < min(u.orow0 + a.n_sinks, u.uend)) {
+        hi = u.uend;
+        lo = (int)min((long long)hi, (long long)row + a.window);
+      }
+    }
+    // dQ: this row's statistics.
+    const size_t stat = (size_t)u.oh * T + (size_t)row;
+    const float lse2 = (MODE == kDQ && row_ok) ? a.lse2[stat] : INFINITY;
+    const float dsum = (MODE == kDQ && row_ok) ? a.dsum[stat] : 0.f;
+    const float2 nlv = make_float2(-lse2, -lse2), ndv = make_float2(-dsum, -dsum);
+    // dKV: column statistics of the query tiles, negated in shared memory (warps of column half 0
+    // fill -lse2, half 1 -D); the next tile's are fetched while this one is computed.
+    auto col_stat = [&](int i) -> float {
+      const int q = in_row<MODE>(u, i) + r;
+      if (q >= a.T) return ch == 0 ? -INFINITY : 0.f;
+      const size_t at = (size_t)in_head<MODE>(u, i, a) * T + (size_t)q;
+      return ch == 0 ? -a.lse2[at] : -a.dsum[at];
+    };
+    float next_stat = MODE != kDQ ? col_stat(0) : 0.f;
+    for (int i = 0; i < u.n_in; ++i) {
+      const int valid = in_valid<MODE>(u, i), irow = in_row<MODE>(u, i);
+      float* cl = cols + (cols_n & 1) * 2 * kTileN;
+      if (MODE != kDQ) {
+        cl[ch * kTileN + r] = next_stat;
+        mbar_arrive(bars + 8 * (C::B_COLS + (cols_n & 1)));
+        if (i + 1 < u.n_in) next_stat = col_stat(i + 1);
+        ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (C::B_COLS + (cols_n & 1)),
+                                               (cols_n >> 1) & 1, abort_flag, a.status));
+        ++cols_n;
+        if (!ok) break;
+      }
+      for (int hh = 0; hh < 2; ++hh) {
+        const int cvalid = min(kHalf, valid - hh * kHalf) - 32 * ch;   // of this warp's columns
+        if (valid - hh * kHalf <= 0) break;
+        const int b = (int)(sp_seen & 1);
+        // Which of the warp's 32 columns each row pairs with.
+        const int c0 = irow + hh * kHalf + 32 * ch;
+        uint32_t bits = range_bits(lo - c0, hi - c0);
+        if (MODE == kDQ) bits |= range_bits(start - c0, first - c0);
+        if (cvalid < 32) bits &= range_bits(0, cvalid);
+        if (a.valid) {
+          const int k = c0 + lane;
+          bits &= __ballot_sync(0xffffffffu, k < a.T && a.valid[k]);
+        }
+        const bool any = __any_sync(0xffffffffu, bits != 0u);
+        const bool all = __all_sync(0xffffffffu, bits == 0xffffffffu);
+        ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (C::B_SPFULL + b), (sp_seen >> 1) & 1,
+                                               abort_flag, a.status));
+        if (!ok) break;
+        ++sp_seen;
+        tc_fence_after();
+        const uint32_t buf = b * C::TMEM_BUF;
+        // The bf16 pairs go to the first 16 columns of the warp's own chunk of S (P) and dP (dS).
+        uint32_t pk_ds[16], pk_p[16];
+        if (any) {
+          uint32_t sv[32], dp[32];
+          tmem_ld_x32(t_s + buf, sv);
+          tmem_ld_x32(t_p + buf, dp);
+          tmem_wait_ld();
+          reg_fence16(sv);
+          reg_fence16(sv + 16);
+          reg_fence16(dp);
+          reg_fence16(dp + 16);
+          if (!all) {
+            // Off the mask P = 0, and dP (from padding it may not be finite) counts as 0.
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              sv[j] = ((bits >> j) & 1u) ? sv[j] : 0xff800000u;
+              dp[j] = ((bits >> j) & 1u) ? dp[j] : 0u;
+            }
+          }
+          const float* cln = cl + hh * kHalf + 32 * ch;
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            float2 nl = nlv, nd = ndv;
+            if (MODE != kDQ) {
+              nl = *reinterpret_cast<const float2*>(cln + j);
+              nd = *reinterpret_cast<const float2*>(cln + kTileN + j);
+            }
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[j]),
+                                                    __uint_as_float(sv[j + 1])), sl2v, nl);
+            const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            const float2 dd = __fadd2_rn(make_float2(__uint_as_float(dp[j]),
+                                                     __uint_as_float(dp[j + 1])), nd);
+            const float2 ds = __fmul2_rn(pp, dd);
+            // bf16: the operand type of the gradient products.
+            pk_ds[j / 2] = pack_bf16x2(ds.x, ds.y);
+            if (MODE != kDQ) pk_p[j / 2] = pack_bf16x2(pp.x, pp.y);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) pk_ds[j] = pk_p[j] = 0u;
+        }
+        tmem_st_x16(t_p + buf, pk_ds);
+        if (MODE != kDQ) tmem_st_x16(t_s + buf, pk_p);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bars + 8 * (C::B_DSFULL + b));
+      }
+      if (!ok) break;
+    }
+    if (!ok) break;
+    ok = __all_sync(0xffffffffu,
+                    mbar_wait(bars + 8 * C::B_ACCFULL, acc_seen & 1, abort_flag, a.status));
+    if (!ok) break;
+    ++acc_seen;
+    tc_fence_after();
+    // Epilogue: this warp's half of the accumulator columns.
+    const size_t base = ((size_t)row * (MODE == kDQ ? a.H : a.Hkv) + u.oh) * D + ch * HD;
+    if (MODE == kDQ) {
+#pragma unroll
+      for (int c0 = 0; c0 < HD; c0 += CW) {
+        uint32_t acc[CW];
+        tmem_ld_cols<CW>(t_a0 + c0, acc);
+        tmem_wait_ld();
+        reg_fence_cols<CW>(acc);
+        if (c0 + CW >= HD) {
+          tc_fence_before();
+          mbar_arrive(bars + 8 * C::B_ACCFREE);
+        }
+        if (!row_ok) continue;
+#pragma unroll
+        for (int x = 0; x < CW; x += 8) {
+          float o[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = a.scale * __uint_as_float(acc[x + e]);
+          store_bf16x8(a.dq + base + c0 + x, o);
+        }
+      }
+      continue;
+    }
+    // The chunks of partial sums that rows behind the window left for a first token.
+    int slot = 0, n_part = 0;
+    const size_t pstep = (size_t)a.Hkv * a.n_sinks * 2 * D;
+    const float* part = nullptr;
+    if (MODE == kDKV && a.part && real && row - start < a.n_sinks) {
+      const int end = a.row_end[row];
+      if (end - start > a.window) {
+        const int k0 = (start + a.window) / kChunk, k1 = (end - 1) / kChunk;
+        slot = k0 + a.row_user[row];
+        n_part = k1 - k0 + 1;
+        part = a.part + ((size_t)slot * a.Hkv + u.oh) * a.n_sinks * 2 * D +
+               (size_t)(row - start) * 2 * D + ch * HD;
+      }
+    }
+    float* mine = MODE == kSink
+                      ? a.part + (((size_t)u.slot * a.Hkv + u.oh) * a.n_sinks + r) * 2 * D + ch * HD
+                      : nullptr;
+    const bool writes = MODE == kSink ? r < a.n_sinks : row_ok;
+#pragma unroll
+    for (int c0 = 0; c0 < HD; c0 += CW) {
+      uint32_t dvv[CW], dkk[CW];
+      tmem_ld_cols<CW>(t_a0 + c0, dvv);
+      tmem_ld_cols<CW>(t_a1 + c0, dkk);
+      tmem_wait_ld();
+      reg_fence_cols<CW>(dvv);
+      reg_fence_cols<CW>(dkk);
+      if (c0 + CW >= HD) {
+        tc_fence_before();
+        mbar_arrive(bars + 8 * C::B_ACCFREE);
+      }
+      if (!writes) continue;
+#pragma unroll
+      for (int x = 0; x < CW; x += 8) {
+        float v[8], k[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[e] = __uint_as_float(dvv[x + e]);
+          k[e] = __uint_as_float(dkk[x + e]);
+        }
+        if (MODE == kSink) {
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            *reinterpret_cast<float4*>(mine + c0 + x + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+            *reinterpret_cast<float4*>(mine + D + c0 + x + e) = make_float4(k[e], k[e + 1], k[e + 2], k[e + 3]);
+          }
+        } else {
+          for (int p = 0; p < n_part; ++p) {
+            const float* y = part + (size_t)p * pstep + c0 + x;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              v[e] += y[e];
+              k[e] += y[D + e];
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) k[e] *= a.scale;
+          store_bf16x8(a.dv + base + c0 + x, v);
+          store_bf16x8(a.dk + base + c0 + x, k);
+        }
+      }
+    }
+  }
+}
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_bwd_kernel(const __grid_constant__ CUtensorMap tmO1,
+                      const __grid_constant__ CUtensorMap tmO2,
+                      const __grid_constant__ CUtensorMap tmI1,
+                      const __grid_constant__ CUtensorMap tmI2, const BwdArgs a) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw);
+  const uint32_t bars = sbase + C::OFF_BAR;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  volatile int* skip = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    *skip = *a.status != 0;   // an error recorded earlier makes the launch a no-op
+    for (int i = 0; i < C::NUM_BARS; ++i) {
+      uint32_t n = 1;
+      if (i == C::B_DSFULL || i == C::B_DSFULL + 1 || i == C::B_ACCFREE || i == C::B_COLS ||
+          i == C::B_COLS + 1)
+        n = kCompute;
+      if (i >= C::B_INREADY && i < C::B_INREADY + kStages) n = 32;
+      // Readers of the ring: the producer and MMA threads, the compute warps, the padding warp.
+      if (i >= C::B_RINGEMPTY) n = 2 + kCompute + (a.valid ? 32 : 0);
+      mbar_init(bars + 8 * i, n);
+    }
+    *abort_flag = 0;
+    mbar_fence_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_map(&tmO1);
+    tma_prefetch_map(&tmO2);
+    tma_prefetch_map(&tmI1);
+    tma_prefetch_map(&tmI2);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Ring ring{reinterpret_cast<volatile int*>(smem + C::OFF_RING), bars + 8 * C::B_RINGFULL,
+            bars + 8 * C::B_RINGEMPTY, 0u};
+  if (!*skip) {
+    if (warp == 0) {
+      if (lane == 0)
+        producer_role<D, MODE>(&tmO1, &tmO2, &tmI1, &tmI2, a, sbase, bars, abort_flag, ring);
+    } else if (warp == 1) {
+      if (lane == 0) mma_role<D, MODE>(a, sbase, bars, tmem, abort_flag, ring);
+    } else if (warp < 10) {
+      compute_role<D, MODE>(a, bars, tmem, reinterpret_cast<float*>(smem + C::OFF_COLS),
+                            abort_flag, warp, lane, ring);
+    } else if (warp == 10) {
+      if (a.valid) padding_role<D, MODE>(a, sbase, bars, abort_flag, lane, ring);
+    } else if (lane == 0) {
+      claim_role<MODE>(a, ring, abort_flag);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Statistics of every row and head, [H][T]: the log-sum-exp in log2 units (+inf for a row that sees no
+// key) and D = rowsum(dO * O); D / 8 lanes per row and head. Also the list of kSink units, one thread per
+// user.
+template <int D, typename IdxT>
+__global__ void __launch_bounds__(256)
+    window_prep_kernel(const bf16* __restrict__ out, const bf16* __restrict__ dout,
+                       const float* __restrict__ lse, const uint8_t* __restrict__ valid, int T,
+                       int H, float* __restrict__ lse2, float* __restrict__ dsum,
+                       const IdxT* __restrict__ off, int64_t B, int window, int4* sinks,
+                       int32_t* n_sink_units, const int32_t* status) {
+  if (*status != 0) return;
+  constexpr int L = D / 8;
+  const int64_t n = (int64_t)T * H;
+  const int64_t step = (int64_t)gridDim.x * (256 / L);
+  const int sub = threadIdx.x % L;
+  // Every lane of a warp takes the same number of turns: the reduction needs them all.
+  for (int64_t x0 = (int64_t)blockIdx.x * (256 / L); x0 < n; x0 += step) {
+    const int64_t x = x0 + threadIdx.x / L;
+    const bool in = x < n;
+    const int64_t row = in ? x / H : 0;
+    const int h = in ? (int)(x - row * H) : 0;
+    const bool real = in && (!valid || valid[row]);
+    float acc = 0.f;
+    if (real) {
+      const uint4 o = ld_global_nc_v4(out + x * D + sub * 8), g = ld_global_nc_v4(dout + x * D + sub * 8);
+      const uint32_t ow[4] = {o.x, o.y, o.z, o.w}, gw[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc = fmaf(bf16_lo(ow[i]), bf16_lo(gw[i]), fmaf(bf16_hi(ow[i]), bf16_hi(gw[i]), acc));
+    }
+#pragma unroll
+    for (int m = L / 2; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
+    if (in && sub == 0) {
+      const float l = real ? lse[x] : -INFINITY;
+      lse2[(size_t)h * T + row] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
+      dsum[(size_t)h * T + row] = real ? acc : 0.f;
+    }
+  }
+  if (!sinks) return;
+  for (int64_t b = blockIdx.x * (int64_t)256 + threadIdx.x; b < B;
+       b += (int64_t)gridDim.x * 256) {
+    const int s = (int)off[b], e = (int)off[b + 1];
+    if (e - s <= window) continue;
+    for (int c = (s + window) / kChunk; c <= (e - 1) / kChunk; ++c)
+      sinks[atomicAdd(n_sink_units, 1)] = make_int4(s, e, c, c + (int)b);
+  }
 }
 
 struct BwdLayout {
-  size_t row_start = 0, row_end = 0, counters = 0, total = 0;
+  size_t row_start = 0, row_end = 0, row_user = 0, lse2 = 0, dsum = 0, sinks = 0, part = 0,
+         counters = 0, total = 0;
 };
 
-BwdLayout bwd_layout(int64_t T) {
+// Slots of partial sums: chunk index + user index is unique to a (user, chunk) pair, since both never
+// fall from pair to pair and one of them rises.
+BwdLayout bwd_layout(int64_t B, int64_t T, int H, int Hkv, int d, int n_sinks) {
   BwdLayout L;
-  L.row_end = align_up(4 * (size_t)T, 256);
-  L.counters = align_up(L.row_end + 4 * (size_t)T, 256);
+  const size_t t4 = align_up(4 * (size_t)T, 256);
+  const size_t slots = n_sinks > 0 ? (size_t)(T / kChunk + 1 + B) : 0;
+  L.row_end = t4;
+  L.row_user = 2 * t4;
+  L.lse2 = 3 * t4;
+  L.dsum = L.lse2 + align_up(4 * (size_t)T * H, 256);
+  L.sinks = L.dsum + align_up(4 * (size_t)T * H, 256);
+  L.part = L.sinks + align_up(16 * slots, 256);
+  L.counters = L.part + align_up(8 * slots * Hkv * n_sinks * d, 256);
   L.total = L.counters + 256;
   return L;
+}
+
+struct Maps {
+  CUtensorMap q, k, v, dout;
+};
+
+template <int D, int MODE>
+int launch_pass(BwdArgs a, const Maps& m, int counter, int units, int dev, int sms,
+                cudaStream_t st) {
+  using C = Cfg<D>;
+  static std::atomic<bool> set[64];
+  if (!set[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(window_bwd_kernel<D, MODE>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::SMEM_ALLOC) != cudaSuccess)
+      return JCA_ERR_CUDA;
+    set[dev].store(true, std::memory_order_release);
+  }
+  a.counter += counter;
+  a.n_units = units;
+  const int grid = units < sms ? units : sms;
+  if (MODE == kDQ)
+    window_bwd_kernel<D, MODE><<<grid, kThreads, C::SMEM_ALLOC, st>>>(m.q, m.dout, m.k, m.v, a);
+  else
+    window_bwd_kernel<D, MODE><<<grid, kThreads, C::SMEM_ALLOC, st>>>(m.k, m.v, m.q, m.dout, a);
+  return cudaGetLastError() == cudaSuccess ? JCA_OK : JCA_ERR_CUDA;
+}
+
+template <int D>
+int launch_bwd(const BwdArgs& a, const void* q, const void* k, const void* v, const void* out,
+               const void* dout, const float* lse, const void* offsets, int64_t B, int64_t qs,
+               int64_t ks, int64_t vs, int idx_bits, float* lse2, float* dsum, int4* sinks,
+               int32_t* n_sink_units, int64_t slots, int dev, int sms, cudaStream_t st) {
+  Maps m;
+  if (!make_strided_map_bf16(&m.q, q, a.T, a.H, D, qs, kTileM) ||
+      !make_strided_map_bf16(&m.k, k, a.T, a.Hkv, D, ks, kTileM) ||
+      !make_strided_map_bf16(&m.v, v, a.T, a.Hkv, D, vs, kTileM) ||
+      !make_rows_map_bf16(&m.dout, dout, a.T, a.H, D, kTileM))
+    return JCA_ERR_CUDA;
+  const int64_t want = ((int64_t)a.T * a.H * (D / 8) + 255) / 256;
+  const int grid = (int)(want < (int64_t)sms * 16 ? want : (int64_t)sms * 16);
+  const bf16 *o = static_cast<const bf16*>(out), *g = static_cast<const bf16*>(dout);
+  if (idx_bits == 32)
+    window_prep_kernel<D, int32_t><<<grid, 256, 0, st>>>(
+        o, g, lse, a.valid, a.T, a.H, lse2, dsum, static_cast<const int32_t*>(offsets), B, a.window,
+        sinks, n_sink_units, a.status);
+  else
+    window_prep_kernel<D, int64_t><<<grid, 256, 0, st>>>(
+        o, g, lse, a.valid, a.T, a.H, lse2, dsum, static_cast<const int64_t*>(offsets), B, a.window,
+        sinks, n_sink_units, a.status);
+  if (cudaGetLastError() != cudaSuccess) return JCA_ERR_CUDA;
+  const int tiles = (a.T + kTileM - 1) / kTileM;
+  int rc = launch_pass<D, kDQ>(a, m, 0, tiles * a.H, dev, sms, st);
+  if (rc) return rc;
+  if (sinks) {
+    const int64_t most = slots * a.Hkv;   // the list's length is known on the device only
+    rc = launch_pass<D, kSink>(a, m, 1, (int)(most < sms ? most : sms), dev, sms, st);
+    if (rc) return rc;
+  }
+  return launch_pass<D, kDKV>(a, m, 2, tiles * a.Hkv, dev, sms, st);
 }
 
 }  // namespace
@@ -154,18 +897,8 @@ using namespace jca;
 extern "C" size_t jca_window_bwd_workspace_bytes(int64_t B, int64_t T, int H, int Hkv, int d_head,
                                                  int n_sinks) {
   if (!window_sizes_ok(B, T, H, Hkv, n_sinks) || !head_dim_ok(d_head)) return 0;
-  return bwd_layout(T).total;
+  return bwd_layout(B, T, H, Hkv, d_head, n_sinks).total;
 }
-
-namespace jca {
-namespace {
-template <int D>
-void launch_window_bwd(const WindowArgs& a, cudaStream_t st) {
-  window_dq_kernel<D><<<(unsigned)((a.T * a.H + 3) / 4), 128, 0, st>>>(a);
-  window_dkv_kernel<D><<<(unsigned)((a.T * a.Hkv + 3) / 4), 128, 0, st>>>(a);
-}
-}  // namespace
-}  // namespace jca
 
 extern "C" int jagged_window_attn_bwd(const void* q, const void* k, const void* v, const void* out,
                                       const void* dout, const float* lse, void* dq, void* dk,
@@ -184,7 +917,7 @@ extern "C" int jagged_window_attn_bwd(const void* q, const void* k, const void* 
       !aligned(dout, 16) || !aligned(lse, 4) || !aligned(dq, 16) || !aligned(dk, 16) ||
       !aligned(dv, 16) || !aligned(workspace, 256))
     return JCA_ERR_ALIGN;
-  const BwdLayout L = bwd_layout(T);
+  const BwdLayout L = bwd_layout(B, T, H, Hkv, d_head, n_sinks);
   if (workspace_bytes < L.total) return JCA_ERR_WORKSPACE;
   if (B == 0) return JCA_OK;
   int dev = 0, sms = 0;
@@ -192,38 +925,48 @@ extern "C" int jagged_window_attn_bwd(const void* q, const void* k, const void* 
   if (rc) return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
-  WindowArgs a = {};
-  a.q = static_cast<const bf16*>(q);
-  a.k = static_cast<const bf16*>(k);
-  a.v = static_cast<const bf16*>(v);
-  a.out = static_cast<const bf16*>(out);
-  a.dout = static_cast<const bf16*>(dout);
-  a.lse = lse;
+  // A window as long as the batch leaves no row behind it.
+  const bool sinks = n_sinks > 0 && window < T;
+  BwdArgs a = {};
   a.dq = static_cast<bf16*>(dq);
   a.dk = static_cast<bf16*>(dk);
   a.dv = static_cast<bf16*>(dv);
   a.valid = valid;
   a.row_start = reinterpret_cast<int32_t*>(ws + L.row_start);
   a.row_end = reinterpret_cast<int32_t*>(ws + L.row_end);
+  a.row_user = reinterpret_cast<int32_t*>(ws + L.row_user);
+  a.lse2 = reinterpret_cast<float*>(ws + L.lse2);
+  a.dsum = reinterpret_cast<float*>(ws + L.dsum);
+  a.part = sinks ? reinterpret_cast<float*>(ws + L.part) : nullptr;
+  a.sinks = reinterpret_cast<int4*>(ws + L.sinks);
+  a.counter = reinterpret_cast<int32_t*>(ws + L.counters);   // [3] claims, [1] kSink units
+  a.n_sink_units = a.counter + 3;
   a.status = status;
-  a.T = T;
-  a.q_stride = q_stride;
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
+  a.T = (int)T;
   a.H = H;
   a.Hkv = Hkv;
+  a.group = H / Hkv;
   a.window = (int)(window < T ? window : (T > 0 ? T : 1));
   a.n_sinks = n_sinks;
   a.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)d_head);
+  a.scale_log2 = a.scale * 1.4426950408889634f;
   rc = window_plan(offsets, B, T, idx_bits, reinterpret_cast<int32_t*>(ws + L.row_start),
                    reinterpret_cast<int32_t*>(ws + L.row_end),
-                   reinterpret_cast<int32_t*>(ws + L.counters), 1, status, st);
+                   sinks ? reinterpret_cast<int32_t*>(ws + L.row_user) : nullptr, a.counter, 4,
+                   status, st);
   if (rc || T == 0) return rc;
+  float* lse2 = reinterpret_cast<float*>(ws + L.lse2);
+  float* dsum = reinterpret_cast<float*>(ws + L.dsum);
+  int4* list = sinks ? reinterpret_cast<int4*>(ws + L.sinks) : nullptr;
+  const int64_t slots = T / kChunk + 1 + B;
+  auto run = [&](auto fn) {
+    return fn(a, q, k, v, out, dout, lse, offsets, B, q_stride, k_stride, v_stride, idx_bits, lse2,
+              dsum, list, a.counter + 3, slots, dev, sms, st);
+  };
   switch (d_head) {
-    case 16: launch_window_bwd<16>(a, st); break;
-    case 32: launch_window_bwd<32>(a, st); break;
-    case 64: launch_window_bwd<64>(a, st); break;
-    default: launch_window_bwd<128>(a, st); break;
+    case 16: return run(launch_bwd<16>);
+    case 32: return run(launch_bwd<32>);
+    case 64: return run(launch_bwd<64>);
+    default: return run(launch_bwd<128>);
   }
-  return cudaGetLastError() == cudaSuccess ? JCA_OK : JCA_ERR_CUDA;
 }
