@@ -336,6 +336,16 @@ __device__ __forceinline__ void rescale_o_row(uint32_t t_o, float alpha) {
   tmem_wait_st();
 }
 
+// Moves this warpgroup's register allowance to N a thread (four consecutive warps, all of them).
+template <int N>
+__device__ __forceinline__ void set_max_regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_max_regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // ------------------------------------------------------------------------------------------
 // Math and memory helpers
 // ------------------------------------------------------------------------------------------

@@ -4,20 +4,23 @@
 //   (a, b) -> (a cos x - b sin x, a sin x + b cos x),  x = position[token, axis(j)] * theta_j.
 // The gradient of a rotation is the rotation by -x.
 //
-// What bounds it: memory. q and k are read and written once, so a token of H + Hkv heads moves
-// 2 (H + Hkv) d elements; the cosines and sines depend on the token and the pair alone. A block
-// takes a tile of tokens, forms the tile's (cos, sin) once into shared memory (512 entries, two per
-// thread) and then turns every head of q and k of those tokens with 16-byte accesses, so the
-// trigonometry is paid once per token and not once per head, and one launch serves q and k.
+// What bounds it: memory (256 users, 16 heads of 128: 202 us, 0.85 of the copy bandwidth; fp32 gradient
+// of 64 users 47 us, 0.90). q and k are read and written once; the cosines and sines depend on the
+// token and the pair alone. A warp takes a few tokens at a time, starts its first loads, forms the
+// tokens' (cos, sin) once into its part of shared memory while they are under way (frequencies in
+// registers, positions fetched a step ahead) and turns every head of q and k of them with 16-byte
+// accesses: the trigonometry is paid once per token, one launch serves q and k, and no warp waits
+// for another. With one barrier per block and tile instead it took 254 us, with half the entries
+// per step 249 us, with more warps that each spill 208 to 260 us.
 //
-// Angles: the turn count position * theta / 2 pi is formed in fp64, with theta / 2 pi as a sum of two
-// numbers and the product's rounding recovered by an FMA, and its whole part removed there: with one
-// fp64 factor a position of 2^31 (seconds since an epoch) would already cost 2^-22 of a radian, as
-// much as fp32 elements can show. The nearest quarter turn is
-// split off there too, and only the remainder in [-1/8, 1/8] turns goes to the fp32 sine and cosine:
-// its rounding is then at most pi 2^-27, where that of a whole half turn would be pi 2^-25, more
-// than the sine's own error. theta / 2 pi comes from the host as a kernel argument. The
-// rotation is fp32, rounded once to the element type; pairs past the sections keep their bits.
+// Angles are counted in turns, in 64-bit fixed point: theta / 2 pi is an integer multiple of 2^-64 (the
+// host rounds it from extended precision), and the position times that integer, wrapped to 64 bits,
+// is the fraction of the turn, whatever the position: one integer product in place of a chain of fp64
+// operations and their reduction (a third of the time on the 256-user batch), off by at most 2^-65
+// of a turn per unit of position, 2^-34 at a position of 2^31 (seconds since an epoch), where an
+// fp64 product would be off by 2^-22 of a radian. The nearest quarter turn is split off and the
+// remainder in [-1/8, 1/8] turns goes to fp32 series for sine and cosine: its rounding there is at
+// most 2^-24, where that of a whole half turn would be four times as much. The rotation is fp32, rounded once to the element type; pairs past the sections keep their bits.
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -32,7 +35,8 @@ namespace jca {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeEntries = 512;   // (cos, sin) pairs of a tile
+constexpr int kRopeEntries = 128;   // (cos, sin) pairs of a warp's tile
+constexpr int kRopeBlocks = 2;      // blocks per SM
 constexpr int kMaxHalf = 64;
 constexpr int kMaxAxes = 4;
 
@@ -46,8 +50,7 @@ struct RopeAxesArgs {
   int H, Hkv, n_axes;
   int n_turned;                     // pairs [0, n_turned) turn, the rest stay as they are
   float sign;                       // -1 turns backwards (the gradient)
-  double turns[kMaxHalf];           // theta_j / 2 pi, and what its rounding to fp64 left out
-  double turns_lo[kMaxHalf];
+  uint64_t turns[kMaxHalf];         // theta_j / 2 pi in units of 2^-64
   uint8_t axis[kMaxHalf];
 };
 
@@ -112,6 +115,16 @@ struct Vec<float> {
   }
 };
 
+// Sine and cosine of |x| <= pi / 4 by their Taylor series, to x^9 and x^10: the next terms are below
+// 2^-29. A dozen multiply-adds where the library's function also reduces any argument.
+__device__ __forceinline__ void sin_cos_eighth(float x, float& s, float& c) {
+  const float y = x * x;
+  s = fmaf(y, fmaf(y, fmaf(y, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f);
+  s = fmaf(s * y, x, x);
+  c = fmaf(y, fmaf(y, fmaf(y, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f);
+  c = fmaf(y, fmaf(y, c, -0.5f), 1.f);
+}
+
 // The first n elements of `a`, the others of `b`.
 template <typename E>
 __device__ __forceinline__ uint4 keep_tail(uint4 a, uint4 b, int n) {
@@ -127,75 +140,124 @@ __device__ __forceinline__ uint4 keep_tail(uint4 a, uint4 b, int n) {
 }
 
 template <typename E, typename IdxT, int D>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks)
     rope_axes_kernel(const __grid_constant__ RopeAxesArgs a) {
   constexpr int HALF = D / 2;
   constexpr int ROWS = kRopeEntries / HALF;      // tokens of a tile
   constexpr int N = Vec<E>::N;
   constexpr int CH = HALF / N;                   // 16-byte chunks of half a head
-  __shared__ __align__(16) float2 cs[kRopeEntries];
-  const int64_t t0 = (int64_t)blockIdx.x * ROWS;
-  const int rows = (int)min((int64_t)ROWS, a.T - t0);
+  constexpr int U = 4;                           // units a lane has in flight
+  constexpr int EPL = kRopeEntries / 32;         // entries a lane forms
+  __shared__ __align__(16) float2 table[kRopeThreads / 32][kRopeEntries];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float2* cs = table[warp];
   const IdxT* pos = static_cast<const IdxT*>(a.pos);
+  // The lane's pairs: their frequencies, and where their entries lie. Entries of a token: the first
+  // two pairs of every chunk, then the next two of every chunk, ..., so that the lanes that read a
+  // chunk each read consecutive 16 bytes.
+  uint64_t turns[EPL];
+  int axis[EPL], at[EPL], row[EPL];
 #pragma unroll
-  for (int e = threadIdx.x; e < kRopeEntries; e += kRopeThreads) {
-    const int r = e / HALF, j = e % HALF;
-    if (r < rows) {
-      const double p = (double)pos[(t0 + r) * a.n_axes + a.axis[j]];
-      double n = p * a.turns[j];
-      const double left = fma(p, a.turns[j], -n) + p * a.turns_lo[j];
-      n = 4.0 * ((n - rint(n)) + left);
-      const double k = rint(n);
-      float s, c;
-      sincospif((float)(0.5 * (n - k)), &s, &c);
-      const int quarter = (int)k;   // -2..2: a quarter turn swaps the two and flips one
-      const float s1 = (quarter & 1) ? c : s, c1 = (quarter & 1) ? -s : c;
-      cs[e] = make_float2((quarter & 2) ? -c1 : c1, a.sign * ((quarter & 2) ? -s1 : s1));
-    }
+  for (int i = 0; i < EPL; ++i) {
+    const int e = lane + 32 * i, j = e % HALF;
+    turns[i] = a.turns[j];
+    axis[i] = a.axis[j];
+    row[i] = e / HALF;
+    at[i] = row[i] * HALF + (j % N / 2 * CH + j / N) * 2 + (j & 1);
   }
-  __syncthreads();
-  // Units of the tile: (token, head, chunk of half a head), the chunk fastest.
+  // Units of a tile: (token, head, chunk of half a head), the chunk fastest.
   const uint32_t per_row = (uint32_t)(a.H + a.Hkv) * CH;
-  const uint32_t units = per_row * (uint32_t)rows;
-  for (uint32_t u = threadIdx.x; u < units; u += kRopeThreads) {
-    const uint32_t r = u / per_row, x = u - r * per_row;
-    const int head = (int)(x / CH), j0 = (int)(x % CH) * N;
-    const bool is_q = head < a.H;
-    const E* src = is_q ? static_cast<const E*>(a.q) + (t0 + r) * a.q_stride + (int64_t)head * D
-                        : static_cast<const E*>(a.k) + (t0 + r) * a.k_stride +
-                              (int64_t)(head - a.H) * D;
-    E* dst = is_q ? static_cast<E*>(a.q_out) + (t0 + r) * a.qo_stride + (int64_t)head * D
-                  : static_cast<E*>(a.k_out) + (t0 + r) * a.ko_stride +
-                        (int64_t)(head - a.H) * D;
-    float lo[N], hi[N];
-    const uint4 wlo = *reinterpret_cast<const uint4*>(src + j0);
-    const uint4 whi = *reinterpret_cast<const uint4*>(src + HALF + j0);
-    Vec<E>::load(wlo, lo);
-    Vec<E>::load(whi, hi);
-    const float4* t4 = reinterpret_cast<const float4*>(cs + r * HALF + j0);
+  const int64_t tiles = (a.T + ROWS - 1) / ROWS;
+  const int64_t first = blockIdx.x * (int64_t)(kRopeThreads / 32) + warp;
+  const int64_t stride = gridDim.x * (int64_t)(kRopeThreads / 32);
+  // Positions are loaded a tile ahead: behind the tile's own loads they would hold up its angles.
+  IdxT next[EPL] = {};
+  auto fetch = [&](int64_t tile) {
 #pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const float4 t = t4[i / 2];
-      const float a0 = lo[i], b0 = hi[i], a1 = lo[i + 1], b1 = hi[i + 1];
-      lo[i] = fmaf(a0, t.x, -(b0 * t.y));
-      hi[i] = fmaf(a0, t.y, b0 * t.x);
-      lo[i + 1] = fmaf(a1, t.z, -(b1 * t.w));
-      hi[i + 1] = fmaf(a1, t.w, b1 * t.z);
+    for (int i = 0; i < EPL; ++i) {
+      const int64_t r = tile * ROWS + row[i];
+      if (r < a.T) next[i] = pos[r * a.n_axes + axis[i]];
     }
-    uint4 olo = Vec<E>::store(lo), ohi = Vec<E>::store(hi);
-    if (j0 + N > a.n_turned) {
-      olo = keep_tail<E>(olo, wlo, a.n_turned - j0);
-      ohi = keep_tail<E>(ohi, whi, a.n_turned - j0);
+  };
+  fetch(first);
+  for (int64_t tile = first; tile < tiles; tile += stride) {
+    const int64_t t0 = tile * ROWS;
+    const int rows = (int)min((int64_t)ROWS, a.T - t0);
+    const uint32_t units = per_row * (uint32_t)rows;
+    for (uint32_t u0 = 0; u0 < units; u0 += 32 * U) {
+      uint4 lo[U], hi[U];
+      uint32_t r[U], x[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const uint32_t u = u0 + 32 * i + lane;
+        r[i] = ROWS == 1 ? 0u : u / per_row;
+        x[i] = u - r[i] * per_row;
+        if (u < units) {
+          const int head = (int)(x[i] / CH);
+          const bool is_q = head < a.H;
+          const E* s = static_cast<const E*>(is_q ? a.q : a.k) +
+                       (t0 + r[i]) * (is_q ? a.q_stride : a.k_stride) +
+                       (is_q ? head : head - a.H) * (int64_t)D + x[i] % CH * N;
+          lo[i] = *reinterpret_cast<const uint4*>(s);
+          hi[i] = *reinterpret_cast<const uint4*>(s + HALF);
+        }
+      }
+      if (u0 == 0) {
+        // The tile's cosines and sines, formed while the first loads are under way.
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          const uint64_t f = (uint64_t)(int64_t)next[i] * turns[i];   // of a turn, in 2^-64
+          const uint32_t quarter = (uint32_t)((f + (1ull << 61)) >> 62);
+          const int32_t rest = (int32_t)((f - ((uint64_t)quarter << 62)) >> 32);
+          float s, c;
+          sin_cos_eighth((float)rest * 1.4629180792671596e-9f, s, c);   // 2 pi 2^-32
+          // A quarter turn swaps the two and flips one.
+          const float s1 = (quarter & 1) ? c : s, c1 = (quarter & 1) ? -s : c;
+          cs[at[i]] = make_float2((quarter & 2) ? -c1 : c1, a.sign * ((quarter & 2) ? -s1 : s1));
+        }
+        fetch(tile + stride);
+        __syncwarp();
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (u0 + 32 * i + lane >= units) continue;
+        const int c = (int)(x[i] % CH), head = (int)(x[i] / CH);
+        float u[N], v[N];
+        Vec<E>::load(lo[i], u);
+        Vec<E>::load(hi[i], v);
+        const float4* t4 = reinterpret_cast<const float4*>(cs + r[i] * HALF) + c;
+#pragma unroll
+        for (int k = 0; k < N; k += 2) {
+          const float4 t = t4[k / 2 * CH];
+          const float a0 = u[k], b0 = v[k], a1 = u[k + 1], b1 = v[k + 1];
+          u[k] = fmaf(a0, t.x, -(b0 * t.y));
+          v[k] = fmaf(a0, t.y, b0 * t.x);
+          u[k + 1] = fmaf(a1, t.z, -(b1 * t.w));
+          v[k + 1] = fmaf(a1, t.w, b1 * t.z);
+        }
+        uint4 olo = Vec<E>::store(u), ohi = Vec<E>::store(v);
+        const int turned = a.n_turned - c * N;   // of the chunk's pairs
+        if (turned < N) {
+          olo = keep_tail<E>(olo, lo[i], turned);
+          ohi = keep_tail<E>(ohi, hi[i], turned);
+        }
+        const bool is_q = head < a.H;
+        E* d = static_cast<E*>(is_q ? a.q_out : a.k_out) +
+               (t0 + r[i]) * (is_q ? a.qo_stride : a.ko_stride) +
+               (is_q ? head : head - a.H) * (int64_t)D + c * N;
+        *reinterpret_cast<uint4*>(d) = olo;
+        *reinterpret_cast<uint4*>(d + HALF) = ohi;
+      }
     }
-    *reinterpret_cast<uint4*>(dst + j0) = olo;
-    *reinterpret_cast<uint4*>(dst + HALF + j0) = ohi;
   }
 }
 
 template <typename E, typename IdxT>
-void launch_rope_axes(const RopeAxesArgs& a, int d, cudaStream_t st) {
-  const int rows = kRopeEntries / (d / 2);
-  const unsigned grid = (unsigned)((a.T + rows - 1) / rows);
+void launch_rope_axes(const RopeAxesArgs& a, int d, int sms, cudaStream_t st) {
+  const int rows = kRopeEntries / (d / 2) * (kRopeThreads / 32);   // tokens of a block's warps
+  const int64_t want = (a.T + rows - 1) / rows;
+  const unsigned grid = (unsigned)(want < (int64_t)sms * kRopeBlocks ? want : sms * kRopeBlocks);
   switch (d) {
     case 16: rope_axes_kernel<E, IdxT, 16><<<grid, kRopeThreads, 0, st>>>(a); break;
     case 32: rope_axes_kernel<E, IdxT, 32><<<grid, kRopeThreads, 0, st>>>(a); break;
@@ -256,21 +318,19 @@ int rope_axes(const void* q, const void* k, void* q_out, void* k_out, const void
   for (int ax = 0; ax < n_axes; ++ax)
     for (int i = 0; i < sections[ax]; ++i, ++j) {
       const long double e = per_axis ? (long double)i / sections[ax] : (long double)j / half;
-      const long double t = exp2l(-e * log2_base) * inv_2pi;
-      a.turns[j] = (double)t;
-      a.turns_lo[j] = (double)(t - (long double)a.turns[j]);
+      a.turns[j] = (uint64_t)roundl(ldexpl(exp2l(-e * log2_base) * inv_2pi, 64));
       a.axis[j] = (uint8_t)ax;
     }
   a.n_turned = j;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (idx_bits == 32) {
-    if (dtype == JCA_BF16) launch_rope_axes<__nv_bfloat16, int32_t>(a, d, st);
-    else if (dtype == JCA_FP16) launch_rope_axes<__half, int32_t>(a, d, st);
-    else launch_rope_axes<float, int32_t>(a, d, st);
+    if (dtype == JCA_BF16) launch_rope_axes<__nv_bfloat16, int32_t>(a, d, sms, st);
+    else if (dtype == JCA_FP16) launch_rope_axes<__half, int32_t>(a, d, sms, st);
+    else launch_rope_axes<float, int32_t>(a, d, sms, st);
   } else {
-    if (dtype == JCA_BF16) launch_rope_axes<__nv_bfloat16, int64_t>(a, d, st);
-    else if (dtype == JCA_FP16) launch_rope_axes<__half, int64_t>(a, d, st);
-    else launch_rope_axes<float, int64_t>(a, d, st);
+    if (dtype == JCA_BF16) launch_rope_axes<__nv_bfloat16, int64_t>(a, d, sms, st);
+    else if (dtype == JCA_FP16) launch_rope_axes<__half, int64_t>(a, d, sms, st);
+    else launch_rope_axes<float, int64_t>(a, d, sms, st);
   }
   return cudaGetLastError() == cudaSuccess ? JCA_OK : JCA_ERR_CUDA;
 }

@@ -16,23 +16,29 @@
 // are decided for 32 columns at a time and per warp: chunks that no row sees are not read, chunks that
 // every row sees are not masked.
 //
-// Kernel (one persistent block per SM, 12 warps; tcgen05 with TMEM accumulators, TMA loads):
+// Kernel (one persistent block per SM, 16 warps; tcgen05 with TMEM accumulators, TMA loads):
 //   warp 0       lane 0 loads Q and K tiles, lane 1 loads V tiles (rings of stages);
-//   warp 1       allocates TMEM; one thread issues every MMA;
-//   warps 2..9   two softmax groups, one per 128-row query tile A and B of the block, one row a thread
-//                (TMEM lane = row); P is written back over S as bf16 and read from there by the PV
-//                MMA; the group finishes its own rows;
-//   warp 10      with padding: zeroes the padding rows of each landed V tile (a weight of 0 does not
+//   warps 1, 2   one thread each issues the MMAs of query tile A (rows 0..127 of the block) and B: the
+//                two tiles share every K and V tile they both need, but neither waits for the
+//                other's softmax (warp 1 also allocates TMEM);
+//   warp 3       with padding: zeroes the padding rows of each landed V tile (a weight of 0 does not
 //                undo an Inf or NaN there), otherwise idle;
-//   warp 11      claims the next block from a counter, reads where its users start and passes both
-//                to every role through a ring, several blocks ahead of the loads.
-// A and B share every K and V tile they both need. MMA order, one stream over all blocks:
-//   QK_A(t), PV_B(t - 1), QK_B(t), PV_A(t)
-// so that one group's softmax runs while the tensor core works for the other.
+//   warps 4..11  two softmax groups, one per query tile, one row a thread (TMEM lane = row); P goes
+//                back to TMEM as bf16 and is read from there by the PV MMA; the group finishes its
+//                own rows. They take over registers of the other warps, so that a row's 128 scores
+//                stay in registers;
+//   warp 12      claims the next block from a counter, reads where its rows' users start and passes
+//                both to every role through a ring, several blocks ahead of the loads.
+// The roles' code is kept small: instruction fetch of a larger kernel cost more than the steps
+// themselves (256 users: 663 us with the softmax specialised by the number of visible chunks, which
+// is 350 us here).
 //
-// What bounds it: at a window of 256 the bytes (Q, K, V read and O written once: 172 us on the
-// 256-user batch at the copy bandwidth) and the softmax of about 3 key tiles per query tile (93 us of
-// exponentials); at 1024 the tensor core and the softmax, as in the full layer.
+// What bounds it (256 users, window 256, d = 128: 350 us, 0.49 of the copy bandwidth; 12 long users,
+// window 1024, d = 64: 510 us): the chain QK -> softmax -> PV of each query tile. A tile's softmax takes
+// about 1700 cycles alone, of which 1024 are its 16,384 exponentials, and TMEM holds the scores of
+// two tiles. Eight warps on one tile at a time (64 columns a thread) measured 350 and 657 us,
+// one thread issuing both tiles' MMAs 350 and 562 us. Without padding the kernel reads and writes
+// each tensor about once; exponentials and tensor core are each busy less than half of the time.
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -88,8 +94,12 @@ struct FwdArgs {
 };
 
 constexpr int kRing = 4;
-constexpr int kThreads = 384;
+constexpr int kEntry = 8 + kItemRows;   // first row, head, then each row's user start from 8 on
+constexpr int kThreads = 512;
 constexpr int kGroup = 128;   // softmax threads of a query tile
+// Registers a thread: 512 x 128 at launch, of which the softmax warps take what the others give up
+// (72 + 40 + 2 x 200 = 4 x 128).
+constexpr int kRegsRoles = 72, kRegsClaim = 40, kRegsSoftmax = 200;
 
 template <int D>
 struct Cfg {
@@ -122,55 +132,68 @@ struct Cfg {
   static constexpr int B_PFULL = B_SFULL + 2;
   static constexpr int B_OREADY = B_PFULL + 2;
   static constexpr int B_OFREE = B_OREADY + 2;
-  static constexpr int B_DRAIN = B_OFREE + 2;
-  static constexpr int B_RINGFULL = B_DRAIN + 1;                   // [kRing]
+  static constexpr int B_SREAD = B_OFREE + 2;                      // SEP_P: S_w is in registers
+  static constexpr int B_PVDONE = B_SREAD + 2;                     // SEP_P: P_w was read
+  static constexpr int B_DRAIN = B_PVDONE + 2;                     // [group]
+  static constexpr int B_RINGFULL = B_DRAIN + 2;                   // [kRing]
   static constexpr int B_RINGEMPTY = B_RINGFULL + kRing;
   static constexpr int NUM_BARS = B_RINGEMPTY + kRing;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
-  static constexpr int OFF_RING = OFF_MISC + 16;                   // kRing x 6 ints
-  static constexpr int SMEM_USED = OFF_RING + kRing * 24;
+  static constexpr int OFF_RING = OFF_MISC + 16;                   // [kRing][kEntry] ints
+  static constexpr int SMEM_USED = OFF_RING + kRing * kEntry * 4;
   static constexpr int SMEM_RAW = SMEM_USED + 1024;                // slack for 1 KB alignment
   // At least 120 KB so that a second block never shares the SM (and its TMEM).
   static constexpr int SMEM_ALLOC = SMEM_RAW > 120 * 1024 ? SMEM_RAW : 120 * 1024;
-  static constexpr uint32_t TMEM_S = 0, TMEM_O = 256, TMEM_COLS = 512;   // + 128 for group B
+  // TMEM columns: S_A | S_B (128 each), then O_A | O_B. Heads of up to 64 leave room for the weights
+  // beside the scores: the next QK of a query tile is then issued as soon as its scores are in
+  // registers, and the softmax never waits for a PV and a QK in a row. At d = 128 the weights lie
+  // over the scores.
+  static constexpr bool SEP_P = D <= 64;
+  static constexpr uint32_t TMEM_COLS = 512;
+  static __device__ __forceinline__ uint32_t s_col(int grp) { return 128u * grp; }
+  static __device__ __forceinline__ uint32_t o_col(int grp) { return 256u + (SEP_P ? 64u : 128u) * grp; }
+  static __device__ __forceinline__ uint32_t p_col(int grp) { return SEP_P ? 384u + 64u * grp : 128u * grp; }
   static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory budget");
 };
 
-// A block of up to 256 rows of one head, as every role derives it from the ring entry.
+// A block of up to 256 rows of one head, as every role derives it from the ring entry. Its key tiles
+// are, in order, the first tokens of A's first user (when they lie below the others; trimmed to
+// n_sink keys) and the 128-row tiles from kstart to the block's own rows.
 struct Item {
-  int q0, h, kstart, n_sink, n_tiles;
-  int lo[2], start[2], last[2];   // per query tile: lowest window key, first user's start, last row
+  int q0, h, kstart, n_sink, sink0, n_tiles;
+  int last_a;                 // A reads tiles [0, last_a]; the last holds its own rows
+  int b0, sb0, sb1;           // B reads tiles [b0, n_tiles) and, for first tokens, [sb0, sb1)
   bool has_b;
 
-  __device__ __forceinline__ int key_row(int j) const {
-    return n_sink ? (j == 0 ? start[0] : kstart + (j - 1) * kTileN) : kstart + j * kTileN;
-  }
   __device__ __forceinline__ bool is_sink(int j) const { return n_sink && j == 0; }
-  // Whether tile g (0: A, 1: B) reads key tile j.
-  __device__ __forceinline__ bool needs(int g, int j, int n_sinks) const {
-    if (g == 1 && !has_b) return false;
-    if (is_sink(j)) return g == 0 || start[1] == start[0];
-    const int kr = key_row(j);
-    return kr <= last[g] && (kr + kTileN > lo[g] ||
-                             (start[g] < kr + kTileN && start[g] + n_sinks > kr));
+  __device__ __forceinline__ int key_row(int j) const {
+    return is_sink(j) ? sink0 : kstart + (j - (n_sink ? 1 : 0)) * kTileN;
   }
+  __device__ __forceinline__ bool a_reads(int j) const { return j <= last_a; }
+  __device__ __forceinline__ bool b_reads(int j) const { return j >= b0 || (j >= sb0 && j < sb1); }
 };
 
 __device__ __forceinline__ Item make_item(const volatile int* e, const FwdArgs& a) {
   Item w;
   w.q0 = e[0];
   w.h = e[1];
-  w.lo[0] = e[2];
-  w.start[0] = e[3];
-  w.lo[1] = e[4];
-  w.start[1] = e[5];
   w.has_b = w.q0 + kTileM < a.T;
-  w.last[0] = min(w.q0 + kTileM, a.T) - 1;
-  w.last[1] = min(w.q0 + kItemRows, a.T) - 1;
-  w.kstart = w.lo[0] & ~(kTileN - 1);
-  // First tokens below the run of key tiles get a (trimmed) tile of their own.
-  w.n_sink = max(0, min(a.n_sinks, w.kstart - w.start[0]));
-  w.n_tiles = (w.q0 + (w.has_b ? kItemRows : kTileM) - w.kstart) / kTileN + (w.n_sink ? 1 : 0);
+  const int start_a = e[8], start_b = e[8 + kTileM];
+  const int lo_a = max(start_a, w.q0 - a.window + 1);
+  const int lo_b = max(start_b, w.q0 + kTileM - a.window + 1);
+  w.sink0 = start_a;
+  w.kstart = lo_a & ~(kTileN - 1);
+  w.n_sink = max(0, min(a.n_sinks, w.kstart - start_a));
+  const int x = w.n_sink ? 1 : 0;
+  w.last_a = x + (w.q0 - w.kstart) / kTileN;
+  w.n_tiles = w.last_a + (w.has_b ? 2 : 1);
+  w.b0 = w.has_b ? x + max(0, lo_b - w.kstart) / kTileN : w.n_tiles;
+  // First tokens of B's first user: in A's tile of them, in the tiles from kstart on, or both.
+  const int first_b = min(start_b + a.n_sinks, lo_b);
+  w.sb0 = start_b < w.kstart ? 0 : x + (start_b - w.kstart) / kTileN;
+  w.sb1 = !w.has_b || first_b <= start_b ? 0
+          : first_b <= w.kstart          ? 1
+                                         : x + (first_b - 1 - w.kstart) / kTileN + 1;
   return w;
 }
 
@@ -179,45 +202,50 @@ struct Ring {
   uint32_t full, empty, k;
 };
 
-// Takes the next entry; false when aborting or at the end.
+// Takes the next entry, and the user start of row `r` of the block; false when aborting or at the end.
 __device__ __forceinline__ bool ring_take(Ring& r, const FwdArgs& a, Item& w,
-                                          volatile int* abort_flag, bool& ok) {
+                                          volatile int* abort_flag, bool& ok, int row = 0,
+                                          int* start = nullptr) {
   const int s = (int)(r.k % kRing);
   ok = mbar_wait(r.full + 8 * s, (r.k / kRing) & 1, abort_flag, a.status);
   if (!ok) return false;
-  const volatile int* e = r.slot + 6 * s;
+  const volatile int* e = r.slot + kEntry * s;
   const bool more = e[0] >= 0;
   if (more) w = make_item(e, a);
+  if (start) *start = e[8 + row];
   mbar_arrive(r.empty + 8 * s);
   ++r.k;
   return more;
 }
 
-// Claims blocks until none is left and posts them, then the end marker.
-__device__ void claim_role(const FwdArgs& a, Ring r, volatile int* abort_flag) {
+// Claims blocks until none is left and posts them, then the end marker; one warp.
+__device__ void claim_role(const FwdArgs& a, Ring r, volatile int* abort_flag, int lane) {
   for (;;) {
-    const int v = atomicAdd(a.counter, 1);
-    int e[6] = {-1, 0, 0, 0, 0, 0};
-    if (v < a.n_items) {
-      // Heads fastest: concurrent blocks share rows, and with shared heads K and V. Rows from the
-      // end: under a long window the later blocks of a user are the longer ones.
-      const int t = (a.n_items - 1 - v) / a.H;
-      e[0] = t * kItemRows;
-      e[1] = (a.n_items - 1 - v) % a.H;
+    int v = lane == 0 ? atomicAdd(a.counter, 1) : 0;
+    v = __shfl_sync(0xffffffffu, v, 0);
+    // Heads fastest: concurrent blocks share rows, and with shared heads K and V. Rows from the
+    // end: under a long window the later blocks of a user are the longer ones.
+    const int left = a.n_items - 1 - v;
+    const int q0 = left < 0 ? -1 : left / a.H * kItemRows;
+    int start[kItemRows / 32];
+    if (left >= 0) {
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int i = min(e[0] + g * kTileM, a.T - 1);
-        e[3 + 2 * g] = a.row_start[i];
-        e[2 + 2 * g] = max(e[3 + 2 * g], i - a.window + 1);
-      }
+      for (int i = 0; i < kItemRows / 32; ++i)
+        start[i] = a.row_start[min(q0 + 32 * i + lane, a.T - 1)];
     }
     const int s = (int)(r.k % kRing);
-    if (!mbar_wait(r.empty + 8 * s, ((r.k / kRing) & 1) ^ 1, abort_flag, a.status)) return;
+    const bool ok = mbar_wait(r.empty + 8 * s, ((r.k / kRing) & 1) ^ 1, abort_flag, a.status);
+    if (!__all_sync(0xffffffffu, ok)) return;
+    volatile int* e = r.slot + kEntry * s;
+    if (lane == 0) e[0] = q0;
+    if (left >= 0) {
+      if (lane == 0) e[1] = left % a.H;
 #pragma unroll
-    for (int i = 0; i < 6; ++i) r.slot[6 * s + i] = e[i];
+      for (int i = 0; i < kItemRows / 32; ++i) e[8 + 32 * i + lane] = start[i];
+    }
     mbar_arrive(r.full + 8 * s);
     ++r.k;
-    if (e[0] < 0) return;
+    if (left < 0) return;
   }
 }
 
@@ -297,6 +325,7 @@ __device__ void padding_role(const FwdArgs& a, uint32_t sbase, uint32_t bars,
       for (int c = 0; c < 4; ++c) {
         if (!pad[c]) continue;
         // A row's bytes of a column block are contiguous; the swizzle only reorders them.
+#pragma unroll 1
         for (int i = lane; i < 32 * CH; i += 32) {
           const int r = i / CH, x = i % CH;
           if ((pad[c] >> r) & 1)
@@ -310,148 +339,114 @@ __device__ void padding_role(const FwdArgs& a, uint32_t sbase, uint32_t bars,
   }
 }
 
-// O (+)= P V over ksteps of 16 keys; P sits in TMEM as bf16 pairs, 8 columns a step.
-template <int D>
-__device__ __forceinline__ void mma_pv(uint32_t o, uint32_t p, uint64_t v, int ksteps,
-                                       bool overwrite) {
-  using C = Cfg<D>;
-  constexpr uint32_t kIdesc = idesc_bf16_f32(C::BM, D, false, true);
-  constexpr uint32_t kStep = (16 * C::SW) >> 4;
-  if (ksteps == C::KSTEPS_PV) {
-#pragma unroll
-    for (int kk = 0; kk < C::KSTEPS_PV; ++kk)
-      tc_mma_ts(o, p + (uint32_t)kk * 8u, v + (uint64_t)(kk * kStep), kIdesc,
-                (overwrite && kk == 0) ? 0u : 1u);
-  } else {
-    for (int kk = 0; kk < ksteps; ++kk)
-      tc_mma_ts(o, p + (uint32_t)kk * 8u, v + (uint64_t)(kk * kStep), kIdesc,
-                (overwrite && kk == 0) ? 0u : 1u);
-  }
-}
-
+// One query tile's products; a thread for A and one for B, so that neither waits for the other's
+// softmax. QK(t) is followed by PV(t), or with SEP_P by PV(t - 1).
 template <int D>
 __device__ void mma_role(const FwdArgs& a, uint32_t sbase, uint32_t bars, uint32_t tmem,
-                         volatile int* abort_flag, Ring ring) {
+                         volatile int* abort_flag, int grp, Ring ring) {
   using C = Cfg<D>;
   constexpr uint32_t kIdescFull = idesc_bf16_f32(C::BM, C::BN, false, false);
   constexpr uint32_t kIdesc0 = kIdescFull & ~(0x3Fu << 17);
+  constexpr uint32_t kIdescPV = idesc_bf16_f32(C::BM, D, false, true);
+  constexpr uint32_t kVStep = (16 * C::SW) >> 4;   // 16 key rows of V
   const int vfull = a.valid ? C::B_VREADY : C::B_VFULL;
-  const uint64_t dq = smem_desc(sbase + C::OFF_Q, 16, 8 * C::SW, C::LAYOUT);
+  const uint32_t ts = tmem + C::s_col(grp), to = tmem + C::o_col(grp), tp = tmem + C::p_col(grp);
+  const uint64_t dq = smem_desc(sbase + C::OFF_Q + grp * C::QS * C::TILE_BYTES, 16, 8 * C::SW,
+                                C::LAYOUT);
   const uint64_t dk = smem_desc(sbase + C::OFF_K, 16, 8 * C::SW, C::LAYOUT);
   const uint64_t dv = smem_desc(sbase + C::OFF_V, C::BLK_BYTES, 8 * C::SW, C::LAYOUT);
-  uint32_t g = 0, v_seen = 0, p_seen[2] = {0, 0}, o_items[2] = {0, 0}, q_seen[2] = {0, 0};
+  uint32_t g = 0, steps = 0, pvs = 0, items = 0, qn = 0;
   bool ok = true;
+  // A PV whose weights are not known to be there yet (key tile, 16-key steps, first and last of the
+  // block).
+  uint32_t pv_g = 0;
+  int pv_k = 0;
+  bool pv_first = false, pv_last = false;
+  auto issue_pv = [&]() -> bool {
+    const int s = (int)(pv_g % C::KVS);
+    if (!mbar_wait(bars + 8 * (vfull + s), (pv_g / C::KVS) & 1, abort_flag, a.status)) return false;
+    if (pv_k == 0) {   // not read by this query tile
+      mbar_arrive(bars + 8 * (C::B_VEMPTY + s));
+      return true;
+    }
+    if (pv_first && items > 0 &&
+        !mbar_wait(bars + 8 * (C::B_OFREE + grp), (items - 1) & 1, abort_flag, a.status))
+      return false;
+    if (!mbar_wait(bars + 8 * (C::B_PFULL + grp), pvs & 1, abort_flag, a.status)) return false;
+    ++pvs;
+    tc_fence_after();
+    // O (+)= P V; P sits in TMEM as bf16 pairs, 8 columns per 16 keys.
+    const uint64_t v = dv + (uint64_t)((s * C::TILE_BYTES) >> 4);
+#pragma unroll 4
+    for (int kk = 0; kk < pv_k; ++kk)
+      tc_mma_ts(to, tp + (uint32_t)kk * 8u, v + (uint64_t)(kk * kVStep), kIdescPV,
+                (pv_first && kk == 0) ? 0u : 1u);
+    tc_commit(bars + 8 * (C::B_VEMPTY + s));
+    if (C::SEP_P) tc_commit(bars + 8 * (C::B_PVDONE + grp));
+    if (pv_last) {
+      tc_commit(bars + 8 * (C::B_OREADY + grp));
+      ++items;
+    }
+    return true;
+  };
+  bool pending = false;
   Item w;
-  auto qk = [&](int grp, uint64_t q, uint64_t k, uint32_t idesc) {
-#pragma unroll
-    for (int kk = 0; kk < C::KSTEPS_QK; ++kk) {
-      const uint32_t off = ((kk / C::KSTEPS_PER_BLK) * C::BLK_BYTES +
-                            (kk % C::KSTEPS_PER_BLK) * 32) >> 4;
-      tc_mma(tmem + C::TMEM_S + 128u * grp, q + off, k + off, idesc, kk > 0 ? 1u : 0u);
-    }
-    tc_commit(bars + 8 * (C::B_SFULL + grp));
-  };
-  auto pv = [&](int grp, uint32_t gg, bool first, int ksteps) -> bool {
-    const int s = (int)(gg % C::KVS);
-    if (gg + 1 != v_seen) {
-      if (!mbar_wait(bars + 8 * (vfull + s), (gg / C::KVS) & 1, abort_flag, a.status)) return false;
-      v_seen = gg + 1;
-    }
-    if (!mbar_wait(bars + 8 * (C::B_PFULL + grp), p_seen[grp] & 1, abort_flag, a.status))
-      return false;
-    ++p_seen[grp];
-    if (first && o_items[grp] > 0 &&
-        !mbar_wait(bars + 8 * (C::B_OFREE + grp), (o_items[grp] - 1) & 1, abort_flag, a.status))
-      return false;
-    tc_fence_after();
-    mma_pv<D>(tmem + C::TMEM_O + 128u * grp, tmem + C::TMEM_S + 128u * grp,
-              dv + (uint64_t)((s * C::TILE_BYTES) >> 4), ksteps, first);
-    return true;
-  };
-  // PV_B of the key tile before, possibly of the item before.
-  struct {
-    uint32_t gg;
-    int ksteps;   // 0: nothing pending
-    bool first, last;
-  } pend = {0, 0, false, false};
-  auto flush_b = [&]() -> bool {
-    if (pend.ksteps == 0) return true;
-    if (!pv(1, pend.gg, pend.first, pend.ksteps)) return false;
-    tc_commit(bars + 8 * (C::B_VEMPTY + (int)(pend.gg % C::KVS)));
-    if (pend.last) {
-      tc_commit(bars + 8 * (C::B_OREADY + 1));
-      ++o_items[1];
-    }
-    pend.ksteps = 0;
-    return true;
-  };
-  auto wait_q = [&](int t, int slot) -> bool {
-    if (!mbar_wait(bars + 8 * (C::B_QFULL + slot), (q_seen[t] / C::QS) & 1, abort_flag, a.status))
-      return false;
-    ++q_seen[t];
-    tc_fence_after();
-    return true;
-  };
   while (ok && ring_take(ring, a, w, abort_flag, ok)) {
-    const int qslot[2] = {(int)(q_seen[0] % C::QS), C::QS + (int)(q_seen[1] % C::QS)};
-    const uint64_t q[2] = {dq + (uint64_t)((qslot[0] * C::TILE_BYTES) >> 4),
-                           dq + (uint64_t)((qslot[1] * C::TILE_BYTES) >> 4)};
-    // Key tiles run from low to high rows: a tile is a query tile's last when it holds its rows.
-    bool seen[2] = {false, false};
+    bool seen = false;
+    const int last = grp ? (w.has_b ? w.n_tiles - 1 : -1) : w.last_a;
+    const int slot = grp * C::QS + (int)(qn % C::QS);
+    const uint64_t q = dq + (uint64_t)(((int)(qn % C::QS) * C::TILE_BYTES) >> 4);
+#pragma unroll 1
     for (int j = 0; j < w.n_tiles; ++j, ++g) {
       const int s = (int)(g % C::KVS);
-      const bool na = w.needs(0, j, a.n_sinks), nb = w.needs(1, j, a.n_sinks);
-      const int kr = w.key_row(j);
-      const bool last_a = !w.is_sink(j) && kr == w.q0, last_b = !w.is_sink(j) && kr == w.q0 + C::BM;
+      const bool reads = grp ? w.b_reads(j) : w.a_reads(j);
       const int keys = w.is_sink(j) ? (w.n_sink + 15) & ~15 : C::BN;
-      const uint32_t idesc = kIdesc0 | ((uint32_t)(keys >> 3) << 17);
-      const uint64_t k = dk + (uint64_t)((s * C::TILE_BYTES) >> 4);
       ok = mbar_wait(bars + 8 * (C::B_KFULL + s), (g / C::KVS) & 1, abort_flag, a.status);
       if (!ok) break;
-      tc_fence_after();
-      if (na) {
-        if (!seen[0]) {
-          ok = wait_q(0, qslot[0]);
-          if (!ok) break;
-        }
-        qk(0, q[0], k, idesc);
-        if (last_a) tc_commit(bars + 8 * (C::B_QEMPTY + qslot[0]));
-      }
-      ok = flush_b();
-      if (!ok) break;
-      if (nb) {
-        if (!seen[1]) {
-          ok = wait_q(1, qslot[1]);
-          if (!ok) break;
-        }
-        qk(1, q[1], k, idesc);
-        if (last_b) tc_commit(bars + 8 * (C::B_QEMPTY + qslot[1]));
-      }
-      tc_commit(bars + 8 * (C::B_KEMPTY + s));
-      if (na) {
-        ok = pv(0, g, !seen[0], keys >> 4);
+      if (reads) {
+        if (!seen)
+          ok = mbar_wait(bars + 8 * (C::B_QFULL + slot), (qn / C::QS) & 1, abort_flag, a.status);
+        if (C::SEP_P && ok && steps > 0)
+          ok = mbar_wait(bars + 8 * (C::B_SREAD + grp), (steps - 1) & 1, abort_flag, a.status);
         if (!ok) break;
-        seen[0] = true;
-        if (!nb) tc_commit(bars + 8 * (C::B_VEMPTY + s));
-        if (last_a) {
-          tc_commit(bars + 8 * C::B_OREADY);
-          ++o_items[0];
+        tc_fence_after();
+        const uint64_t k = dk + (uint64_t)((s * C::TILE_BYTES) >> 4);
+        const uint32_t idesc = kIdesc0 | ((uint32_t)(keys >> 3) << 17);
+#pragma unroll
+        for (int kk = 0; kk < C::KSTEPS_QK; ++kk) {
+          const uint32_t off = ((kk / C::KSTEPS_PER_BLK) * C::BLK_BYTES +
+                                (kk % C::KSTEPS_PER_BLK) * 32) >> 4;
+          tc_mma(ts, q + off, k + off, idesc, kk > 0 ? 1u : 0u);
         }
+        ++steps;
+        tc_commit(bars + 8 * (C::B_SFULL + grp));
+        tc_commit(bars + 8 * (C::B_KEMPTY + s));
+        if (j == last) tc_commit(bars + 8 * (C::B_QEMPTY + slot));
+      } else {
+        mbar_arrive(bars + 8 * (C::B_KEMPTY + s));
       }
-      if (nb) {
-        pend.gg = g;
-        pend.ksteps = keys >> 4;
-        pend.first = !seen[1];
-        pend.last = last_b;
-        seen[1] = true;
+      if (C::SEP_P && pending) {
+        ok = issue_pv();
+        if (!ok) break;
+      }
+      pv_g = g;
+      pv_k = reads ? keys >> 4 : 0;
+      pv_first = reads && !seen;
+      pv_last = j == last;
+      seen |= reads;
+      pending = C::SEP_P;
+      if (!C::SEP_P) {
+        ok = issue_pv();
+        if (!ok) break;
       }
     }
+    if (last >= 0) ++qn;
   }
-  if (ok) ok = flush_b();
+  if (ok && pending) ok = issue_pv();
   if (!ok) {
     // Aborting: wait until every MMA this thread issued has completed.
-    tc_commit(bars + 8 * C::B_DRAIN);
-    mbar_wait_drain(bars + 8 * C::B_DRAIN, 0);
+    tc_commit(bars + 8 * (C::B_DRAIN + grp));
+    mbar_wait_drain(bars + 8 * (C::B_DRAIN + grp), 0);
   }
 }
 
@@ -463,40 +458,85 @@ __device__ __forceinline__ uint32_t range_bits(int a, int b) {
   return a >= 32 ? 0u : below_b & (0xffffffffu << a);
 }
 
+// Weights p = 2^(scale_log2 s - m) of 32 scores, their sum added to (acc0, acc1), and the weights
+// rounded to bf16 pairs, the operand type of the PV product.
+__device__ __forceinline__ void weights32(const uint32_t* x, float2 sl2v, float2 negv, float2& acc0,
+                                          float2& acc1, uint32_t (&pk)[16]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float2 xs = __ffma2_rn(
+        make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), sl2v, negv);
+    float2 p;
+    p.x = fast_exp2(xs.x);
+    p.y = fast_exp2(xs.y);
+    if (k & 1) acc1 = __fadd2_rn(acc1, p);
+    else acc0 = __fadd2_rn(acc0, p);
+    pk[k] = pack_bf16x2(p.x, p.y);
+  }
+}
+
+// One row of O multiplied by alpha in place in TMEM.
+template <int D>
+__device__ __forceinline__ void rescale_row(uint32_t t_o, float alpha) {
+  constexpr int CW = D < 32 ? D : 32;
+#pragma unroll 1
+  for (int c0 = 0; c0 < D; c0 += CW) {
+    uint32_t u[CW];
+    tmem_ld_cols<CW>(t_o + c0, u);
+    tmem_wait_ld();
+    reg_fence_cols<CW>(u);
+#pragma unroll
+    for (int i = 0; i < CW; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * alpha);
+    tmem_st_cols<CW>(t_o + c0, u);
+  }
+}
+
+__device__ __forceinline__ float max32(const uint32_t* x) {
+  float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < 32; k += 8) {
+    m0 = fmax3(m0, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+    m1 = fmax3(m1, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+    m2 = fmax3(m2, __uint_as_float(x[k + 4]), __uint_as_float(x[k + 5]));
+    m3 = fmax3(m3, __uint_as_float(x[k + 6]), __uint_as_float(x[k + 7]));
+  }
+  return fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+}
+
 template <int D>
 __device__ void softmax_role(const FwdArgs& a, uint32_t bars, uint32_t tmem,
                              volatile int* abort_flag, int warp, int lane, Ring ring) {
   using C = Cfg<D>;
-  const int grp = (warp - 2) >> 2;
+  const int grp = (warp - 4) >> 2;
   const int quarter = warp & 3;
   const int r = quarter * 32 + lane;
   const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
-  const uint32_t t_s = t_lane + C::TMEM_S + 128u * grp, t_o = t_lane + C::TMEM_O + 128u * grp;
+  const uint32_t t_s = t_lane + C::s_col(grp), t_o = t_lane + C::o_col(grp);
+  const uint32_t t_p = t_lane + C::p_col(grp);
   const float sl2 = a.scale_log2;
-  const float2 sl2v = make_float2(sl2, sl2);
   uint32_t lt = 0, oi = 0;
   bool ok = true;
   Item w;
   for (;;) {
-    const bool more = ring_take(ring, a, w, abort_flag, ok);
+    int start = 0;
+    const bool more = ring_take(ring, a, w, abort_flag, ok, grp * C::BM + r, &start);
     if (!__all_sync(0xffffffffu, more)) break;
     if (grp == 1 && !w.has_b) continue;
     const int i = w.q0 + grp * C::BM + r;           // this thread's row
     const bool row_ok = i < a.T;
     const bool sees = row_ok && (!a.valid || a.valid[i]);
-    const int start = row_ok ? a.row_start[i] : 0;
     // Visible keys: [lo, hi) and [start, first).
     const int lo = sees ? max(start, i - a.window + 1) : 0, hi = sees ? i + 1 : 0;
     const int first = sees ? min(start + a.n_sinks, lo) : start;
     float m = -INFINITY, l = 0.f;
     bool fresh = true;
     for (int j = 0; j < w.n_tiles; ++j) {
-      if (!w.needs(grp, j, a.n_sinks)) continue;
+      if (!(grp ? w.b_reads(j) : w.a_reads(j))) continue;
       const int kr = w.key_row(j), cols = w.is_sink(j) ? w.n_sink : C::BN;
-      // Visible columns: per chunk of 32 columns, none, some or all for the warp's rows.
+      // Chunks of 32 columns that some row, and that every row of the warp sees.
       uint32_t bits[4], any = 0xfu, all = 0xfu;
-      const bool whole = cols == C::BN && !a.valid && lo <= kr && hi >= kr + C::BN;
-      if (!__all_sync(0xffffffffu, whole)) {
+      if (!__all_sync(0xffffffffu,
+                      cols == C::BN && !a.valid && lo <= kr && hi >= kr + C::BN)) {
         any = all = 0;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -518,71 +558,59 @@ __device__ void softmax_role(const FwdArgs& a, uint32_t bars, uint32_t tmem,
       ++lt;
       tc_fence_after();
       uint32_t x[128];
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if ((any >> c) & 1) tmem_ld_x32(t_s + 32 * c, x + 32 * c);
+      tmem_ld_x32(t_s + 0, x);
+      tmem_ld_x32(t_s + 32, x + 32);
+      tmem_ld_x32(t_s + 64, x + 64);
+      tmem_ld_x32(t_s + 96, x + 96);
       tmem_wait_ld();
 #pragma unroll
       for (int c = 0; c < 128; c += 16) reg_fence16(x + c);
+      if (C::SEP_P) {
+        tc_fence_before();
+        mbar_arrive(bars + 8 * (C::B_SREAD + grp));
+      }
       float mx = -INFINITY;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         if (!((any >> c) & 1)) continue;
-        uint32_t* y = x + 32 * c;
         if (!((all >> c) & 1)) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) y[k] = ((bits[c] >> k) & 1u) ? y[k] : 0xff800000u;   // -inf
+          for (int k = 0; k < 32; ++k)
+            x[32 * c + k] = ((bits[c] >> k) & 1u) ? x[32 * c + k] : 0xff800000u;   // -inf
         }
-        float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 32; k += 8) {
-          m0 = fmax3(m0, __uint_as_float(y[k]), __uint_as_float(y[k + 1]));
-          m1 = fmax3(m1, __uint_as_float(y[k + 2]), __uint_as_float(y[k + 3]));
-          m2 = fmax3(m2, __uint_as_float(y[k + 4]), __uint_as_float(y[k + 5]));
-          m3 = fmax3(m3, __uint_as_float(y[k + 6]), __uint_as_float(y[k + 7]));
-        }
-        mx = fmax3(mx, fmaxf(m0, m1), fmaxf(m2, m3));
+        mx = fmaxf(mx, max32(x + 32 * c));
       }
-      const float m_new = fmaxf(m, mx * sl2);
-      // The reference maximum moves only when it grows by more than 2^8: the weights stay below 2^8
+      // The reference maximum moves only when it grows by more than 2^8: the weights stay below 2^8,
       // and O and l keep the same reference.
+      const float m_new = fmaxf(m, mx * sl2);
       const bool rescale = m_new > m + 8.0f;
       const float m_use = rescale ? m_new : m;
       const float neg_m = (m_use == -INFINITY) ? 0.f : -m_use;
       const float alpha = (rescale && m != -INFINITY) ? fast_exp2(m - m_use) : 1.f;
-      const bool warp_rescale = __any_sync(0xffffffffu, rescale && !fresh);
-      const float2 negv = make_float2(neg_m, neg_m);
-      float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0, acc2 = acc0, acc3 = acc0;
+      const float2 sl2v = make_float2(sl2, sl2), negv = make_float2(neg_m, neg_m);
+      if (C::SEP_P && lt > 1) {
+        // The PV before has read the weights that these replace, and O is stable.
+        ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (C::B_PVDONE + grp), lt & 1, abort_flag,
+                                               a.status));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        if (32 * c >= cols) continue;   // the trimmed PV does not read these
         uint32_t pk[16];
         if ((any >> c) & 1) {
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float2 xs = __ffma2_rn(make_float2(__uint_as_float(x[32 * c + 2 * k]),
-                                                     __uint_as_float(x[32 * c + 2 * k + 1])),
-                                         sl2v, negv);
-            float2 p;
-            p.x = fast_exp2(xs.x);
-            p.y = fast_exp2(xs.y);
-            if ((k & 3) == 0) acc0 = __fadd2_rn(acc0, p);
-            if ((k & 3) == 1) acc1 = __fadd2_rn(acc1, p);
-            if ((k & 3) == 2) acc2 = __fadd2_rn(acc2, p);
-            if ((k & 3) == 3) acc3 = __fadd2_rn(acc3, p);
-            pk[k] = pack_bf16x2(p.x, p.y);   // the operand type of the PV product
-          }
+          weights32(x + 32 * c, sl2v, negv, acc0, acc1, pk);
         } else {
 #pragma unroll
           for (int k = 0; k < 16; ++k) pk[k] = 0u;
         }
-        tmem_st_x16(t_s + 16 * c, pk);
+        tmem_st_x16(t_p + 16 * c, pk);
       }
-      const float2 acc01 = __fadd2_rn(acc0, acc1), acc23 = __fadd2_rn(acc2, acc3);
-      // O is stable here: its last PV was issued before the QK that filled S, and a commit fires
-      // only after every earlier MMA.
-      if (warp_rescale) rescale_o_row<D>(t_o, alpha);
-      l = l * alpha + ((acc01.x + acc01.y) + (acc23.x + acc23.y));
+      // O is stable here: without SEP_P its last PV was issued before the QK that filled S, and a
+      // commit fires only after every earlier MMA of its thread.
+      if (__any_sync(0xffffffffu, rescale && !fresh)) rescale_row<D>(t_o, alpha);
+      l = l * alpha + ((acc0.x + acc0.y) + (acc1.x + acc1.y));
       m = m_use;
       fresh = false;
       tmem_wait_st();
@@ -597,22 +625,20 @@ __device__ void softmax_role(const FwdArgs& a, uint32_t bars, uint32_t tmem,
     tc_fence_after();
     const float inv = l > 0.f ? 1.f / l : 0.f;
     const size_t row = (size_t)i * a.H + w.h;
-    constexpr int CW = D < 32 ? D : 32, PER = D / CW >= 2 ? 2 : 1;
-#pragma unroll
-    for (int c0 = 0; c0 < D; c0 += CW * PER) {
-      uint32_t u[CW * PER];
-#pragma unroll
-      for (int p = 0; p < PER; ++p) tmem_ld_cols<CW>(t_o + c0 + p * CW, u + p * CW);
+    constexpr int CW = D < 32 ? D : 32;
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += CW) {
+      uint32_t u[CW];
+      tmem_ld_cols<CW>(t_o + c0, u);
       tmem_wait_ld();
-#pragma unroll
-      for (int p = 0; p < PER; ++p) reg_fence_cols<CW>(u + p * CW);
-      if (c0 + CW * PER >= D) {
+      reg_fence_cols<CW>(u);
+      if (c0 + CW >= D) {
         tc_fence_before();
         mbar_arrive(bars + 8 * (C::B_OFREE + grp));
       }
       if (!row_ok) continue;
 #pragma unroll
-      for (int c = 0; c < CW * PER; c += 16) {
+      for (int c = 0; c < CW; c += 16) {
         uint32_t p[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
@@ -651,11 +677,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     *skip = *a.status != 0;   // an error recorded earlier makes the launch a no-op
     for (int i = 0; i < C::NUM_BARS; ++i) {
       uint32_t n = 1;
+      if (i >= C::B_KEMPTY && i < C::B_KEMPTY + C::KVS) n = 2;   // both MMA threads
+      if (i >= C::B_VEMPTY && i < C::B_VEMPTY + C::KVS) n = 2;
       if (i >= C::B_PFULL && i < C::B_PFULL + 2) n = kGroup;
       if (i >= C::B_OFREE && i < C::B_OFREE + 2) n = kGroup;
+      if (i >= C::B_SREAD && i < C::B_SREAD + 2) n = kGroup;
       if (i >= C::B_VREADY && i < C::B_VREADY + C::KVS) n = 32;
-      // Readers of the ring: two producer threads, the MMA thread, both groups, the padding warp.
-      if (i >= C::B_RINGEMPTY) n = 3 + 2 * kGroup + (a.valid ? 32 : 0);
+      if (i >= C::B_RINGFULL) n = 32;
+      // Readers of the ring: the two producer and MMA threads, both groups, the padding warp.
+      if (i >= C::B_RINGEMPTY) n = 4 + 2 * kGroup + (a.valid ? 32 : 0);
       mbar_init(bars + 8 * i, n);
     }
     *abort_flag = 0;
@@ -677,20 +707,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   Ring ring{reinterpret_cast<volatile int*>(smem + C::OFF_RING), bars + 8 * C::B_RINGFULL,
             bars + 8 * C::B_RINGEMPTY, 0u};
-  if (!*skip) {
-    if (warp == 0) {
+  if (warp < 4) {
+    set_max_regs_dec<kRegsRoles>();
+    if (*skip) {
+    } else if (warp == 0) {
       if (lane < 2)
         producer_role<D>(&tmQ, lane == 1 ? &tmV : &tmK, a, sbase, bars, abort_flag, lane == 1,
                          ring);
-    } else if (warp == 1) {
-      if (lane == 0) mma_role<D>(a, sbase, bars, tmem, abort_flag, ring);
-    } else if (warp < 10) {
-      softmax_role<D>(a, bars, tmem, abort_flag, warp, lane, ring);
-    } else if (warp == 10) {
-      if (a.valid) padding_role<D>(a, sbase, bars, abort_flag, lane, ring);
-    } else if (lane == 0) {
-      claim_role(a, ring, abort_flag);
+    } else if (warp < 3) {
+      if (lane == 0) mma_role<D>(a, sbase, bars, tmem, abort_flag, warp - 1, ring);
+    } else if (a.valid) {
+      padding_role<D>(a, sbase, bars, abort_flag, lane, ring);
     }
+  } else if (warp < 12) {
+    set_max_regs_inc<kRegsSoftmax>();
+    if (!*skip) softmax_role<D>(a, bars, tmem, abort_flag, warp, lane, ring);
+  } else {
+    set_max_regs_dec<kRegsClaim>();
+    if (!*skip && warp == 12) claim_role(a, ring, abort_flag, lane);
   }
   tc_fence_before();
   __syncthreads();

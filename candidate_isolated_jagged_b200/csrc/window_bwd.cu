@@ -9,8 +9,9 @@
 //     (rows j <= i < min(j + window, end)) for each of its query heads;
 //   * first tokens are also seen from behind their window, by every later row of the user: a unit
 //     takes a user's first tokens as its key tile and walks up to kChunk of those rows, leaving an
-//     fp32 partial sum that the dKV unit of those keys adds in chunk order. Without this
-//     split one key tile would walk a whole long history for its few first tokens.
+//     fp32 partial sum. The dKV unit leaves the window's sum of such a key in fp32 too, and a last
+//     kernel adds them in order and rounds. Without this split one key tile would walk a whole
+//     long history for its few first tokens.
 // Row tiles are cut from the packed rows whatever users they hold, as in the forward.
 //
 // Kernel (one persistent block per SM, 12 warps; tcgen05 with TMEM accumulators, TMA loads). O1/O2 are
@@ -50,7 +51,9 @@ constexpr int kThreads = 384;
 constexpr int kCompute = 256;
 constexpr int kStages = 2;
 constexpr int kHalf = 64;        // inner rows of a half step
-constexpr int kChunk = 1024;     // query rows of a kSink unit
+// Query rows of a kSink unit: 256 rows keep the longest unit at 8 half steps (16 users: 14 us, with
+// 1024 rows 36 us; 256 users 153 and 164 us).
+constexpr int kChunk = 256;
 constexpr int kRing = 4;
 constexpr int kEntry = 6;        // ints of a ring entry
 
@@ -64,9 +67,12 @@ struct BwdArgs {
   const int32_t* row_user;    // [T], with first tokens
   const float* lse2;          // [H][T] log2 units; +inf: the row sees no key
   const float* dsum;          // [H][T] D
-  float* part;                // kSink partials [slot][Hkv][n_sinks][2][D]: dV, dK / scale
+  float* part;                // partials of first tokens [slot][Hkv][n_sinks][2][D]: dV, dK / scale
+  int window_slot;            // slot of the window's own sums: this + user
   const int4* sinks;          // kSink units {first row, end, chunk, slot}
+  const int4* sink_users;     // their users {first row, end, user, 0}
   const int32_t* n_sink_units;
+  const int32_t* n_sink_users;
   int32_t* counter;
   int32_t* status;
   int T, H, Hkv, group, window, n_sinks, n_units;
@@ -624,24 +630,17 @@ __device__ void compute_role(const BwdArgs& a, uint32_t bars, uint32_t tmem, flo
       }
       continue;
     }
-    // The chunks of partial sums that rows behind the window left for a first token.
-    int slot = 0, n_part = 0;
-    const size_t pstep = (size_t)a.Hkv * a.n_sinks * 2 * D;
-    const float* part = nullptr;
-    if (MODE == kDKV && a.part && real && row - start < a.n_sinks) {
-      const int end = a.row_end[row];
-      if (end - start > a.window) {
-        const int k0 = (start + a.window) / kChunk, k1 = (end - 1) / kChunk;
-        slot = k0 + a.row_user[row];
-        n_part = k1 - k0 + 1;
-        part = a.part + ((size_t)slot * a.Hkv + u.oh) * a.n_sinks * 2 * D +
-               (size_t)(row - start) * 2 * D + ch * HD;
-      }
+    // Sums of first tokens that rows behind the window see too stay in fp32 partials.
+    float* mine = nullptr;
+    bool writes = row_ok;
+    if (MODE == kSink) {
+      writes = r < a.n_sinks;
+      mine = a.part + (((size_t)u.slot * a.Hkv + u.oh) * a.n_sinks + r) * 2 * D + ch * HD;
+    } else if (a.part && row_ok && row - start < a.n_sinks &&
+               a.row_end[row] - start > a.window) {
+      const size_t slot = (size_t)a.window_slot + a.row_user[row];
+      mine = a.part + ((slot * a.Hkv + u.oh) * a.n_sinks + (row - start)) * 2 * D + ch * HD;
     }
-    float* mine = MODE == kSink
-                      ? a.part + (((size_t)u.slot * a.Hkv + u.oh) * a.n_sinks + r) * 2 * D + ch * HD
-                      : nullptr;
-    const bool writes = MODE == kSink ? r < a.n_sinks : row_ok;
 #pragma unroll
     for (int c0 = 0; c0 < HD; c0 += CW) {
       uint32_t dvv[CW], dkk[CW];
@@ -663,21 +662,13 @@ __device__ void compute_role(const BwdArgs& a, uint32_t bars, uint32_t tmem, flo
           v[e] = __uint_as_float(dvv[x + e]);
           k[e] = __uint_as_float(dkk[x + e]);
         }
-        if (MODE == kSink) {
-#pragma unroll
-          for (int e = 0; e < 8; e += 4) {
-            *reinterpret_cast<float4*>(mine + c0 + x + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
-            *reinterpret_cast<float4*>(mine + D + c0 + x + e) = make_float4(k[e], k[e + 1], k[e + 2], k[e + 3]);
-          }
-        } else {
-          for (int p = 0; p < n_part; ++p) {
-            const float* y = part + (size_t)p * pstep + c0 + x;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              v[e] += y[e];
-              k[e] += y[D + e];
-            }
-          }
+        if (mine) {
+          float4* m = reinterpret_cast<float4*>(mine + c0 + x);
+          m[0] = make_float4(v[0], v[1], v[2], v[3]);
+          m[1] = make_float4(v[4], v[5], v[6], v[7]);
+          m[D / 4] = make_float4(k[0], k[1], k[2], k[3]);
+          m[D / 4 + 1] = make_float4(k[4], k[5], k[6], k[7]);
+        } else if (MODE == kDKV) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) k[e] *= a.scale;
           store_bf16x8(a.dv + base + c0 + x, v);
@@ -760,15 +751,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Statistics of every row and head, [H][T]: the log-sum-exp in log2 units (+inf for a row that sees no
-// key) and D = rowsum(dO * O); D / 8 lanes per row and head. Also the list of kSink units, one thread per
-// user.
+// key) and D = rowsum(dO * O); D / 8 lanes per row and head. Also the lists of kSink units and their
+// users, one thread per user; their order does not touch any result.
 template <int D, typename IdxT>
 __global__ void __launch_bounds__(256)
     window_prep_kernel(const bf16* __restrict__ out, const bf16* __restrict__ dout,
                        const float* __restrict__ lse, const uint8_t* __restrict__ valid, int T,
                        int H, float* __restrict__ lse2, float* __restrict__ dsum,
                        const IdxT* __restrict__ off, int64_t B, int window, int4* sinks,
-                       int32_t* n_sink_units, const int32_t* status) {
+                       int4* sink_users, int32_t* n_sink_units, int32_t* n_sink_users,
+                       const int32_t* status) {
   if (*status != 0) return;
   constexpr int L = D / 8;
   const int64_t n = (int64_t)T * H;
@@ -802,14 +794,51 @@ __global__ void __launch_bounds__(256)
        b += (int64_t)gridDim.x * 256) {
     const int s = (int)off[b], e = (int)off[b + 1];
     if (e - s <= window) continue;
+    sink_users[atomicAdd(n_sink_users, 1)] = make_int4(s, e, (int)b, 0);
     for (int c = (s + window) / kChunk; c <= (e - 1) / kChunk; ++c)
       sinks[atomicAdd(n_sink_units, 1)] = make_int4(s, e, c, c + (int)b);
   }
 }
 
+// dK and dV of the first tokens of users longer than the window: the window's sum, then the chunks' in
+// order. One block per user and key head, four elements a thread.
+template <int D>
+__global__ void __launch_bounds__(256) window_join_kernel(const BwdArgs a) {
+  if (*a.status != 0) return;
+  const int64_t n = *a.n_sink_users;
+  for (int64_t x = blockIdx.x; x < n * a.Hkv; x += gridDim.x) {
+    const int4 user = a.sink_users[x / a.Hkv];   // {first row, end, user, -}
+    const int hk = (int)(x % a.Hkv), s = user.x, e = user.y, b = user.z;
+    const int c0 = (s + a.window) / kChunk, chunks = (e - 1) / kChunk - c0 + 1;
+    const size_t step = (size_t)a.Hkv * a.n_sinks * 2 * D / 4;
+    const size_t head = (size_t)hk * a.n_sinks * 2 * D / 4;
+    const float4* part = reinterpret_cast<const float4*>(a.part);
+    const float4* own = part + (size_t)(a.window_slot + b) * step + head;
+    part += (size_t)(c0 + b) * step + head;
+    const int keys = min(a.n_sinks, e - s);      // a user may be shorter than the first tokens
+    for (int i = threadIdx.x; i < keys * 2 * D / 4; i += 256) {
+      float4 v = own[i];
+#pragma unroll 8
+      for (int c = 0; c < chunks; ++c) {
+        const float4 y = part[c * step + i];
+        v.x += y.x;
+        v.y += y.y;
+        v.z += y.z;
+        v.w += y.w;
+      }
+      const int key = i / (D / 2), is_k = i / (D / 4) % 2, d = i % (D / 4) * 4;
+      const float f = is_k ? a.scale : 1.f;
+      bf16* dst = (is_k ? a.dk : a.dv) + ((size_t)(s + key) * a.Hkv + hk) * D + d;
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack_bf16x2(v.x * f, v.y * f), pack_bf16x2(v.z * f, v.w * f));
+    }
+  }
+}
+
 struct BwdLayout {
-  size_t row_start = 0, row_end = 0, row_user = 0, lse2 = 0, dsum = 0, sinks = 0, part = 0,
-         counters = 0, total = 0;
+  size_t row_start = 0, row_end = 0, row_user = 0, lse2 = 0, dsum = 0, sinks = 0, users = 0,
+         part = 0, counters = 0, total = 0;
+  int64_t slots = 0, sink_users = 0;   // chunk partials, users that can have any
 };
 
 // Slots of partial sums: chunk index + user index is unique to a (user, chunk) pair, since both never
@@ -817,14 +846,18 @@ struct BwdLayout {
 BwdLayout bwd_layout(int64_t B, int64_t T, int H, int Hkv, int d, int n_sinks) {
   BwdLayout L;
   const size_t t4 = align_up(4 * (size_t)T, 256);
-  const size_t slots = n_sinks > 0 ? (size_t)(T / kChunk + 1 + B) : 0;
+  if (n_sinks > 0) {
+    L.slots = T / kChunk + 1 + B;
+    L.sink_users = B;
+  }
   L.row_end = t4;
   L.row_user = 2 * t4;
   L.lse2 = 3 * t4;
   L.dsum = L.lse2 + align_up(4 * (size_t)T * H, 256);
   L.sinks = L.dsum + align_up(4 * (size_t)T * H, 256);
-  L.part = L.sinks + align_up(16 * slots, 256);
-  L.counters = L.part + align_up(8 * slots * Hkv * n_sinks * d, 256);
+  L.users = L.sinks + align_up(16 * (size_t)L.slots, 256);
+  L.part = L.users + align_up(16 * (size_t)L.sink_users, 256);
+  L.counters = L.part + align_up(8 * (size_t)(L.slots + L.sink_users) * Hkv * n_sinks * d, 256);
   L.total = L.counters + 256;
   return L;
 }
@@ -859,7 +892,8 @@ template <int D>
 int launch_bwd(const BwdArgs& a, const void* q, const void* k, const void* v, const void* out,
                const void* dout, const float* lse, const void* offsets, int64_t B, int64_t qs,
                int64_t ks, int64_t vs, int idx_bits, float* lse2, float* dsum, int4* sinks,
-               int32_t* n_sink_units, int64_t slots, int dev, int sms, cudaStream_t st) {
+               int4* sink_users, int32_t* n_sinks, int64_t slots, int dev, int sms,
+               cudaStream_t st) {
   Maps m;
   if (!make_strided_map_bf16(&m.q, q, a.T, a.H, D, qs, kTileM) ||
       !make_strided_map_bf16(&m.k, k, a.T, a.Hkv, D, ks, kTileM) ||
@@ -872,11 +906,11 @@ int launch_bwd(const BwdArgs& a, const void* q, const void* k, const void* v, co
   if (idx_bits == 32)
     window_prep_kernel<D, int32_t><<<grid, 256, 0, st>>>(
         o, g, lse, a.valid, a.T, a.H, lse2, dsum, static_cast<const int32_t*>(offsets), B, a.window,
-        sinks, n_sink_units, a.status);
+        sinks, sink_users, n_sinks, n_sinks + 1, a.status);
   else
     window_prep_kernel<D, int64_t><<<grid, 256, 0, st>>>(
         o, g, lse, a.valid, a.T, a.H, lse2, dsum, static_cast<const int64_t*>(offsets), B, a.window,
-        sinks, n_sink_units, a.status);
+        sinks, sink_users, n_sinks, n_sinks + 1, a.status);
   if (cudaGetLastError() != cudaSuccess) return JCA_ERR_CUDA;
   const int tiles = (a.T + kTileM - 1) / kTileM;
   int rc = launch_pass<D, kDQ>(a, m, 0, tiles * a.H, dev, sms, st);
@@ -886,7 +920,11 @@ int launch_bwd(const BwdArgs& a, const void* q, const void* k, const void* v, co
     rc = launch_pass<D, kSink>(a, m, 1, (int)(most < sms ? most : sms), dev, sms, st);
     if (rc) return rc;
   }
-  return launch_pass<D, kDKV>(a, m, 2, tiles * a.Hkv, dev, sms, st);
+  rc = launch_pass<D, kDKV>(a, m, 2, tiles * a.Hkv, dev, sms, st);
+  if (rc || !sinks) return rc;
+  const int64_t most = B * a.Hkv;
+  window_join_kernel<D><<<(int)(most < (int64_t)sms * 64 ? most : sms * 64), 256, 0, st>>>(a);
+  return cudaGetLastError() == cudaSuccess ? JCA_OK : JCA_ERR_CUDA;
 }
 
 }  // namespace
@@ -938,9 +976,12 @@ extern "C" int jagged_window_attn_bwd(const void* q, const void* k, const void* 
   a.lse2 = reinterpret_cast<float*>(ws + L.lse2);
   a.dsum = reinterpret_cast<float*>(ws + L.dsum);
   a.part = sinks ? reinterpret_cast<float*>(ws + L.part) : nullptr;
+  a.window_slot = (int)L.slots;
   a.sinks = reinterpret_cast<int4*>(ws + L.sinks);
-  a.counter = reinterpret_cast<int32_t*>(ws + L.counters);   // [3] claims, [1] kSink units
+  a.sink_users = reinterpret_cast<int4*>(ws + L.users);
+  a.counter = reinterpret_cast<int32_t*>(ws + L.counters);   // [3] claims, kSink units, users
   a.n_sink_units = a.counter + 3;
+  a.n_sink_users = a.counter + 4;
   a.status = status;
   a.T = (int)T;
   a.H = H;
@@ -952,16 +993,16 @@ extern "C" int jagged_window_attn_bwd(const void* q, const void* k, const void* 
   a.scale_log2 = a.scale * 1.4426950408889634f;
   rc = window_plan(offsets, B, T, idx_bits, reinterpret_cast<int32_t*>(ws + L.row_start),
                    reinterpret_cast<int32_t*>(ws + L.row_end),
-                   sinks ? reinterpret_cast<int32_t*>(ws + L.row_user) : nullptr, a.counter, 4,
+                   sinks ? reinterpret_cast<int32_t*>(ws + L.row_user) : nullptr, a.counter, 5,
                    status, st);
   if (rc || T == 0) return rc;
   float* lse2 = reinterpret_cast<float*>(ws + L.lse2);
   float* dsum = reinterpret_cast<float*>(ws + L.dsum);
   int4* list = sinks ? reinterpret_cast<int4*>(ws + L.sinks) : nullptr;
-  const int64_t slots = T / kChunk + 1 + B;
   auto run = [&](auto fn) {
     return fn(a, q, k, v, out, dout, lse, offsets, B, q_stride, k_stride, v_stride, idx_bits, lse2,
-              dsum, list, a.counter + 3, slots, dev, sms, st);
+              dsum, list, reinterpret_cast<int4*>(ws + L.users), a.counter + 3, L.slots, dev, sms,
+              st);
   };
   switch (d_head) {
     case 16: return run(launch_bwd<16>);

@@ -9,6 +9,7 @@ the library is missing, ``lib()`` raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 from typing import Optional
@@ -580,14 +581,19 @@ def jca_stack_fwd(x, x_out, weights, n_cand_only: int, offsets, candidate_start=
 _ROPE_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
-def _rows(name: str, t: torch.Tensor, rows: int, heads: int, d: int, dtype, device) -> int:
-    """Checks a [rows, heads, d] tensor with packed heads; returns its row stride in elements."""
+def _bad_rows(name: str, t: torch.Tensor, shape, dtype, device) -> None:
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if t.dim() != 3 or t.shape[0] != rows or t.shape[1] != heads or t.shape[2] != d:
-        raise ValueError(f"{name} must be [{rows}, {heads}, {d}], got {list(t.shape)}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _rows(name: str, t: torch.Tensor, rows: int, heads: int, d: int, dtype, device) -> int:
+    """Checks a [rows, heads, d] tensor with packed heads; returns its row stride in elements."""
+    if t.dtype != dtype or t.shape != (rows, heads, d) or t.device != device:
+        _bad_rows(name, t, (rows, heads, d), dtype, device)
     if rows == 0:
         return heads * d
     s0, s1, s2 = t.stride()
@@ -597,7 +603,9 @@ def _rows(name: str, t: torch.Tensor, rows: int, heads: int, d: int, dtype, devi
 
 
 def _packed(name: str, t: torch.Tensor, rows: int, heads: int, d: int, dtype, device) -> None:
-    if _rows(name, t, rows, heads, d, dtype, device) != heads * d:
+    if t.dtype != dtype or t.shape != (rows, heads, d) or t.device != device:
+        _bad_rows(name, t, (rows, heads, d), dtype, device)
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
@@ -620,17 +628,40 @@ def _heads(name: str, t: torch.Tensor):
     return t.shape
 
 
+def _status_on(status: Optional[torch.Tensor], device) -> torch.Tensor:
+    if status is None:
+        return new_status(device)
+    _vector("status", status, 1, torch.int32, device)
+    return status
+
+
+# The current stream's handle of a device; torch.cuda.current_stream(i).cuda_stream builds two Python
+# objects for the same number, 6 us where the small calls here take 4 us on the GPU.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(fn: str, device, stream, *args) -> int:
     """The C entry point `fn` with `device` current, on its current stream unless one is given."""
-    f = getattr(lib(), fn)
-    if torch.cuda.current_device() == device.index:
-        return _check(f(*args, _stream(stream)), fn)
-    with torch.cuda.device(device):
-        return _check(f(*args, _stream(stream)), fn)
+    f = getattr(_lib or lib(), fn)
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _call(fn, device, stream, *args)
+    if stream is None:
+        handle = _raw_stream(device.index)
+    else:
+        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    code = f(*args, handle)
+    return code if code >= 0 else _check(code, fn)
 
 
 def _at(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
+
+
+@functools.lru_cache(maxsize=64)
+def _sections(sections):
+    return (c_i32 * len(sections))(*sections)
 
 
 def _rope_axes(fn, q, k, q_out, k_out, positions, sections, base, per_axis, stream) -> int:
@@ -648,12 +679,12 @@ def _rope_axes(fn, q, k, q_out, k_out, positions, sections, base, per_axis, stre
     n_axes = len(sections)
     if positions.dim() == 1:
         positions = positions[:, None]
-    if list(positions.shape) != [T, n_axes] or not positions.is_contiguous():
+    if positions.shape != (T, n_axes) or not positions.is_contiguous():
         raise ValueError(f"positions must be contiguous [{T}, {n_axes}], got "
                          f"{list(positions.shape)}")
     if positions.device != dev:
         raise ValueError(f"positions is on {positions.device}, not on {dev}")
-    sec = (c_i32 * n_axes)(*[int(x) for x in sections])
+    sec = _sections(tuple(sections))
     return _call(fn, dev, stream, _at(q), _at(k), _at(q_out), _at(k_out), _at(positions), sec,
                  n_axes, int(bool(per_axis)), T, H, Hkv, d, qs, ks, qo, ko, float(base),
                  _ROPE_TYPES[dtype], _idx_bits(positions))
@@ -690,11 +721,7 @@ def _window_scratch(workspace, status, nbytes, dev):
         workspace = torch.empty(nbytes(), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {dev}")
-    if status is None:
-        status = new_status(dev)
-    else:
-        _vector("status", status, 1, torch.int32, dev)
-    return workspace, status
+    return workspace, _status_on(status, dev)
 
 
 def jagged_window_attn_fwd(q, k, v, out, offsets, window: int, n_sinks: int = 0, valid=None,
@@ -763,10 +790,7 @@ def jagged_window_decode_fwd(q, k_new, v_new, k_cache, v_cache, out, cache_offse
     _packed("out", out, B, H, d, t16, dev)
     _vector("cache_offsets", cache_offsets, B + 1, cache_offsets.dtype, dev)
     _vector("cache_len", cache_len, B, cache_offsets.dtype, dev)
-    if status is None:
-        status = new_status(dev)
-    else:
-        _vector("status", status, 1, torch.int32, dev)
+    status = _status_on(status, dev)
     return _call("jagged_window_decode_fwd", dev, stream, _at(q), _at(k_new), _at(v_new),
                  _at(k_cache), _at(v_cache), _at(out), _at(cache_offsets), _at(cache_len), B, R, H,
                  Hkv, d, int(window), int(n_sinks), qs, ks, vs, float(scale),
@@ -793,10 +817,7 @@ def cand_tree_attn_fwd(cand_q, own_k, own_v, cand_offsets, parent, hist_k, hist_
     _vector("hist_offsets", hist_offsets, B + 1, cand_offsets.dtype, dev)
     _vector("hist_len", hist_len, B, cand_offsets.dtype, dev)
     _vector("parent", parent, N, torch.int32, dev)
-    if status is None:
-        status = new_status(dev)
-    else:
-        _vector("status", status, 1, torch.int32, dev)
+    status = _status_on(status, dev)
     return _call("cand_tree_attn_fwd", dev, stream, _at(cand_q), _at(own_k), _at(own_v),
                  _at(cand_offsets), _at(parent), _at(hist_k), _at(hist_v), _at(hist_offsets),
                  _at(hist_len), _at(out), B, N, R, H, Hkv, d, int(max_cand), qs, ks, vs,
