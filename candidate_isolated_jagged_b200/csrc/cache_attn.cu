@@ -7,11 +7,14 @@
 //
 // What bounds it: reading the cache. A user's n tokens times the G = H / Hkv query heads of a key
 // head are the rows of one product against that head's keys, so a key's 4 d bytes (K and V) serve
-// n G rows. Up to 64 rows the product stays far below what the warp-level tensor instruction
-// (m16n8k16, fp32 accumulators in registers) does in the time the bytes take: 64 rows cost about 16
-// of the 22 cycles that a key of d = 128 takes an SM at the copy bandwidth. A 128-row tcgen05 tile
-// would leave half or more of its rows empty here and would have to mask the ends of the cache in
-// shared memory; with registers the copies zero-fill what lies behind the last key.
+// n G rows. With few rows (256 users, one token each, 4 heads to a key head: 68 us, 0.90 of the copy
+// bandwidth) nothing else counts. With 64 rows (256 users with trees of 64 tokens: 222 us, 0.41) a
+// key of d = 128 takes an SM 22 cycles to read at the copy bandwidth, 16 of the warp-level tensor
+// instruction (m16n8k16, 8 cycles each) and 20 of shared-memory reads, which two warps per
+// scheduler overlap only in part, and the longest histories run on after the others. A
+// 128-row tcgen05 tile would leave half or more of its rows empty here and would have to clear the
+// ends of the cache in shared memory; here the copies zero-fill what lies behind the last key.
+// One user alone (4,096 keys: 10.9 us) pays for its launch, three dependent reads and the joining.
 //
 // Shape: a block of 4 warps takes up to 64 rows of one (user, key head) and walks 64-key tiles
 // through a ring of stages filled by 16-byte asynchronous copies. With 64 rows each warp owns 16 of
@@ -89,18 +92,20 @@ __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// RW warps of 16 rows, times KW warps that share the rows and split the keys of a tile. (Eight warps
+// for 64 rows, two to a row group, measured slower: 272 us against 222 on the 256 users with trees.)
 template <int D, int RW, bool TREE>
 struct CCfg {
   static constexpr int CH = D / 8;                        // 16-byte chunks of a row
   static constexpr int RB = 16 * RW;                      // rows of a block
-  static constexpr int KW = 4 / RW;                       // warps that share rows, by keys
+  static constexpr int KW = 4 / RW;
   static constexpr int KPW = kBK / KW;                    // keys of a tile per warp
   static constexpr int TILE = kBK * D * 2;                // bytes of a K or V tile
   static constexpr int STAGE = 2 * TILE;
@@ -151,10 +156,20 @@ __global__ void __launch_bounds__(kThr, 2) cache_attn_kernel(const CacheArgs a) 
   const int G = a.H / a.Hkv;
   const IdxT* off = static_cast<const IdxT*>(a.off);
 
-  // An error recorded earlier makes the call a no-op. Blocks of a cluster could see a status that
-  // another user's block sets meanwhile at different times, so a block that sees one keeps in step
-  // with its cluster and only tells the others, at the joining, that it has nothing to add.
-  const bool skip = __syncthreads_or(tid == 0 && *a.status != 0);
+  // The user's numbers, all loads under way before the first is used.
+  const int64_t off0 = off[b], off1 = off[b + 1];
+  int64_t h0 = 0, h1 = 0, len = 0;
+  if constexpr (TREE) {
+    h0 = static_cast<const IdxT*>(a.hist_off)[b];
+    h1 = static_cast<const IdxT*>(a.hist_off)[b + 1];
+  }
+  if (a.len) len = static_cast<const IdxT*>(a.len)[b];
+  const int before = *a.status;
+  // An error recorded earlier makes the call a no-op. Threads and blocks of a cluster could see a
+  // status that another user's block sets meanwhile at different times, so all threads of a block
+  // go by one vote, and a block that sees an error keeps in step with its cluster and only tells
+  // the others, at the joining, that it has nothing to add.
+  const bool skip = __syncthreads_or(tid == 0 && before != 0);
   if (skip && a.split == 1) return;
 
   // The user's keys and rows; every block of a user takes the same decisions.
@@ -163,8 +178,7 @@ __global__ void __launch_bounds__(kThr, 2) cache_attn_kernel(const CacheArgs a) 
   int nt = 0;                         // key tiles
   int64_t row0 = 0;                   // token of row 0 of the user in q
   if constexpr (TREE) {
-    const IdxT* ho = static_cast<const IdxT*>(a.hist_off);
-    const int64_t s = off[b], e = off[b + 1], hs = ho[b], he = ho[b + 1];
+    const int64_t s = off0, e = off1, hs = h0, he = h1;
     int bad = 0;
     int64_t hl = he - hs;
     if (s < 0 || s > e || e > a.N || (b == 0 && s != 0) || (b == a.B - 1 && e != a.N) || hs < 0 ||
@@ -173,7 +187,7 @@ __global__ void __launch_bounds__(kThr, 2) cache_attn_kernel(const CacheArgs a) 
     } else if (e - s > a.max_cand) {
       bad = JCA_STATUS_BAD_TREE;
     } else if (a.len) {
-      hl = static_cast<const IdxT*>(a.len)[b];
+      hl = len;
       if (hl < 0 || hl > he - hs) bad = JCA_STATUS_BAD_LENGTH;
     }
     const int n = bad ? 0 : (int)(e - s);
@@ -202,7 +216,8 @@ __global__ void __launch_bounds__(kThr, 2) cache_attn_kernel(const CacheArgs a) 
     uint32_t* bits = reinterpret_cast<uint32_t*>(smem + C::OFF_BITS);
     int* tiles = reinterpret_cast<int*>(smem + C::OFF_TILES);   // [16] tiles, [16] count, [17] flags
     const int tok0 = rb * C::RB / G, ntok = (rb * C::RB + rows - 1) / G - tok0 + 1;
-    for (int i = tid; i < ntok * kTreeWords; i += kThr) bits[i] = 0;
+    const int words = 2 * ((n + kBK - 1) / kBK);   // whole tiles
+    for (int i = tid; i < ntok * words; i += kThr) bits[i / words * kTreeWords + i % words] = 0;
     if (tid == 0) tiles[17] = 0;
     __syncthreads();
     if (tid < ntok) {
@@ -222,7 +237,7 @@ __global__ void __launch_bounds__(kThr, 2) cache_attn_kernel(const CacheArgs a) 
     __syncthreads();
     nt = k.own_tile + tiles[16];
   } else {
-    const int64_t s = off[b], e = off[b + 1], p = static_cast<const IdxT*>(a.len)[b];
+    const int64_t s = off0, e = off1, p = len;
     int bad = 0;
     if (s < 0 || s > e || e > a.R) bad = JCA_STATUS_BAD_OFFSETS;
     else if (p < -1 || (p >= 0 && p >= e - s)) bad = JCA_STATUS_BAD_LENGTH;
@@ -259,43 +274,67 @@ __global__ void __launch_bounds__(kThr, 2) cache_attn_kernel(const CacheArgs a) 
   const int per = (nt + a.split - 1) / a.split;
   const int t0 = min(nt, rank * per), t1 = skip ? t0 : min(nt, t0 + per);
 
+  // This thread's share of a tile: chunk tid % CH of rows r0, r0 + kStep, ...
+  constexpr int kStep = kThr / C::CH, kRows = kBK / kStep;
   const int64_t cstride = (int64_t)a.Hkv * D, hoff = (int64_t)hk * D;
+  const int ch = tid % C::CH, r0 = tid / C::CH;
+  auto copy = [&](uint32_t st, int i, const bf16* pk, const bf16* pv, bool real) {
+    const uint32_t at = st + swz<D>(r0 + i * kStep, ch);
+    cp16(at, pk, real);
+    cp16(at + C::TILE, pv, real);
+  };
+  // Rows [row, row + 64) of the cache, of which the first n are real; 0 < n.
+  auto load_run = [&](uint32_t st, int64_t row, int n) {
+    const int64_t at = (row + r0) * cstride + hoff + ch * 8;
+    const bf16 *pk = a.kc + at, *pv = a.vc + at;
+    const int64_t step = kStep * cstride;
+    if (n >= kBK) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i, pk += step, pv += step) copy(st, i, pk, pv, true);
+    } else {
+#pragma unroll 2
+      for (int i = 0; i < kRows; ++i, pk += step, pv += step) {
+        const bool real = r0 + i * kStep < n;
+        copy(st, i, real ? pk : a.k, real ? pv : a.v, real);
+      }
+    }
+  };
   auto load_tile = [&](int t) {
     const uint32_t st = sb + (uint32_t)(t - t0) % C::STAGES * C::STAGE;
-    const int c = tid % C::CH;
-#pragma unroll 4
-    for (int i = 0; i < C::CH / 2; ++i) {
-      const int r = tid / C::CH + i * (kThr / C::CH);
-      const bf16 *pk = a.k, *pv = a.v;
-      bool real;
-      if constexpr (TREE) {
-        if (t < k.own_tile) {
-          const int x = t * kBK + r;
-          real = x < k.n1;
-          const int64_t at = (k.base + x) * cstride + hoff;
-          if (real) pk = a.kc + at, pv = a.vc + at;
-        } else {
-          const int x = reinterpret_cast<const int*>(smem + C::OFF_TILES)[t - k.own_tile] * kBK + r;
-          real = x < k.n_own;
-          if (real) {
-            pk = a.k + (k.own + x) * a.k_stride + hoff;
-            pv = a.v + (k.own + x) * a.v_stride + hoff;
-          }
-        }
-      } else {
-        const int x = t * kBK + r;
-        real = x <= k.n1 + k.n2;
-        if (x < k.n1 + k.n2) {
-          const int64_t row = x < k.n1 ? k.base + x : k.base2 + (x - k.n1);
-          pk = a.kc + row * cstride + hoff;
-          pv = a.vc + row * cstride + hoff;
-        } else if (real) {
-          pk = a.k + k.own * a.k_stride + hoff;
-          pv = a.v + k.own * a.v_stride + hoff;
-        }
+    if constexpr (TREE) {
+      if (t < k.own_tile) {
+        load_run(st, k.base + (int64_t)t * kBK, k.n1 - t * kBK);
+        return;
       }
-      cp16(st + swz<D>(r, c), pk + (real ? c * 8 : 0), real);
-      cp16(st + C::TILE + swz<D>(r, c), pv + (real ? c * 8 : 0), real);
+      const int x0 = reinterpret_cast<const int*>(smem + C::OFF_TILES)[t - k.own_tile] * kBK;
+#pragma unroll 2
+      for (int i = 0; i < kRows; ++i) {
+        const int x = x0 + r0 + i * kStep;
+        const bool real = x < k.n_own;
+        copy(st, i, real ? a.k + (k.own + x) * a.k_stride + hoff + ch * 8 : a.k,
+             real ? a.v + (k.own + x) * a.v_stride + hoff + ch * 8 : a.v, real);
+      }
+    } else {
+      const int x0 = t * kBK, cached = k.n1 + k.n2;
+      if (x0 >= k.n1 && x0 + kBK <= cached) {
+        load_run(st, k.base2 + (x0 - k.n1), kBK);
+        return;
+      }
+      // A tile with first tokens, or with the new token at its end.
+#pragma unroll 2
+      for (int i = 0; i < kRows; ++i) {
+        const int x = x0 + r0 + i * kStep;
+        const bf16 *pk = a.k, *pv = a.v;
+        if (x < cached) {
+          const int64_t row = x < k.n1 ? k.base + x : k.base2 + (x - k.n1);
+          pk = a.kc + row * cstride + hoff + ch * 8;
+          pv = a.vc + row * cstride + hoff + ch * 8;
+        } else if (x == cached) {
+          pk = a.k + k.own * a.k_stride + hoff + ch * 8;
+          pv = a.v + k.own * a.v_stride + hoff + ch * 8;
+        }
+        copy(st, i, pk, pv, x <= cached);
+      }
     }
   };
 
@@ -338,66 +377,85 @@ __global__ void __launch_bounds__(kThr, 2) cache_attn_kernel(const CacheArgs a) 
     float s[C::KPW / 8][4];
 #pragma unroll
     for (int n = 0; n < C::KPW / 8; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+    // Step by step along the head, so that consecutive products go to different sums.
 #pragma unroll
-    for (int n = 0; n < C::KPW / 16; ++n) {
-      const int key = wk * C::KPW + n * 16 + (lane & 7) + ((lane >> 4) << 3);
+    for (int kk = 0; kk < D / 16; ++kk) {
+      uint32_t f[C::KPW / 16][4];
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        uint32_t f[4];
-        ldsm4(st + swz<D>(key, 2 * kk + ((lane >> 3) & 1)), f);
-        mma16816(s[2 * n], qf[kk], f[0], f[1]);
-        mma16816(s[2 * n + 1], qf[kk], f[2], f[3]);
+      for (int n = 0; n < C::KPW / 16; ++n) {
+        const int key = wk * C::KPW + n * 16 + (lane & 7) + ((lane >> 4) << 3);
+        ldsm4(st + swz<D>(key, 2 * kk + ((lane >> 3) & 1)), f[n]);
+      }
+#pragma unroll
+      for (int n = 0; n < C::KPW / 16; ++n) {
+        mma16816(s[2 * n], qf[kk], f[n][0], f[n][1]);
+        mma16816(s[2 * n + 1], qf[kk], f[n][2], f[n][3]);
       }
     }
-    // Scores in log2 units; keys behind the list, and drafted tokens off the path, drop out.
-    const int col0 = wk * C::KPW + 2 * (lane & 3);  // this thread's columns: col0 + 8 n + {0, 1}
+    // Keys behind the list, and drafted tokens off the path, drop out.
     int limit = kBK;                                // visible columns of a tile of cached keys
-    uint64_t path[2] = {~0ull, ~0ull};
+    bool own = false;
     if constexpr (TREE) {
-      if (t < k.own_tile) {
-        limit = min(kBK, k.n1 - t * kBK);
-      } else {
-        const uint32_t* bits = reinterpret_cast<const uint32_t*>(smem + C::OFF_BITS);
-        const int w = 2 * reinterpret_cast<const int*>(smem + C::OFF_TILES)[t - k.own_tile];
-        const int tok0 = rb * C::RB / G;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = min(ra + 8 * h, rows - 1);
-          const uint32_t* x = bits + ((rb * C::RB + r) / G - tok0) * kTreeWords + w;
-          path[h] = (uint64_t)x[0] | ((uint64_t)x[1] << 32);
-        }
-      }
+      own = t >= k.own_tile;
+      if (!own) limit = min(kBK, k.n1 - t * kBK);
     } else {
       limit = min(kBK, k.n1 + k.n2 + 1 - t * kBK);
     }
-    const bool whole = limit == kBK && (!TREE || t < k.own_tile);
-    float mx[2] = {m[0], m[1]};
+    if (own || limit < kBK) {
+      const int col0 = wk * C::KPW + 2 * (lane & 3);   // columns col0 + 8 n + {0, 1}
+      uint64_t seen[2];
+      seen[0] = seen[1] = limit >= 64 ? ~0ull : (1ull << limit) - 1;
+      if constexpr (TREE) {
+        if (own) {
+          const uint32_t* bits = reinterpret_cast<const uint32_t*>(smem + C::OFF_BITS);
+          const int w = 2 * reinterpret_cast<const int*>(smem + C::OFF_TILES)[t - k.own_tile];
+          const int tok0 = rb * C::RB / G;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int r = min(ra + 8 * h, rows - 1);
+            const uint32_t* x = bits + ((rb * C::RB + r) / G - tok0) * kTreeWords + w;
+            seen[h] = (uint64_t)x[0] | ((uint64_t)x[1] << 32);
+          }
+        }
+      }
+      seen[0] >>= col0;
+      seen[1] >>= col0;
+#pragma unroll
+      for (int n = 0; n < C::KPW / 8; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (!((seen[j >> 1] >> (8 * n + (j & 1))) & 1)) s[n][j] = -INFINITY;
+    }
+    float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int n = 0; n < C::KPW / 8; ++n) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[n][j] *= a.scale_log2;
-        const int col = col0 + 8 * n + (j & 1);
-        if (!whole && (col >= limit || !((path[j >> 1] >> col) & 1))) s[n][j] = -INFINITY;
-        mx[j >> 1] = fmaxf(mx[j >> 1], s[n][j]);
-      }
+      mx[0] = fmax3(mx[0], s[n][0], s[n][1]);
+      mx[1] = fmax3(mx[1], s[n][2], s[n][3]);
     }
     float al[2], ref[2];
+    bool grew = false;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
       mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-      al[h] = m[h] == -INFINITY ? 0.f : fast_exp2(m[h] - mx[h]);
-      ref[h] = mx[h] == -INFINITY ? 0.f : mx[h];
-      m[h] = mx[h];
+      // Log2 units (the scale is positive). The reference moves only when the maximum grows by
+      // more than 2^8: the weights stay below 2^8, and O and l keep the same reference.
+      const float top = fmaxf(m[h], mx[h] * a.scale_log2);
+      const bool moves = top > m[h] + 8.0f;
+      al[h] = moves ? (m[h] == -INFINITY ? 0.f : fast_exp2(m[h] - top)) : 1.f;
+      m[h] = moves ? top : m[h];
+      ref[h] = m[h] == -INFINITY ? 0.f : m[h];
       l[h] *= al[h];
+      grew |= moves;
     }
+    if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n) {
-      o[n][0] *= al[0];
-      o[n][1] *= al[0];
-      o[n][2] *= al[1];
-      o[n][3] *= al[1];
+      for (int n = 0; n < D / 8; ++n) {
+        o[n][0] *= al[0];
+        o[n][1] *= al[0];
+        o[n][2] *= al[1];
+        o[n][3] *= al[1];
+      }
     }
     // O += P V, P rounded to bf16 as the tensor instruction's operand; l sums it in fp32.
 #pragma unroll
@@ -407,7 +465,7 @@ __global__ void __launch_bounds__(kThr, 2) cache_attn_kernel(const CacheArgs a) 
       for (int j = 0; j < 2; ++j) {
         float* x = s[2 * n + j];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = fast_exp2(x[i] - ref[i >> 1]);
+        for (int i = 0; i < 4; ++i) x[i] = fast_exp2(fmaf(x[i], a.scale_log2, -ref[i >> 1]));
         l[0] += x[0] + x[1];
         l[1] += x[2] + x[3];
         p[2 * j] = pack_bf16x2(x[0], x[1]);
@@ -426,6 +484,37 @@ __global__ void __launch_bounds__(kThr, 2) cache_attn_kernel(const CacheArgs a) 
   cp_wait<0>();
   __syncthreads();
 
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+  }
+  // Row r of the block in the output.
+  auto out_row = [&](int r) -> bf16* {
+    const int g = rb * C::RB + r;
+    return a.out + ((row0 + g / G) * a.H + (int64_t)hk * G + g % G) * D;
+  };
+  if (C::KW == 1 && a.split == 1) {
+    // Nothing to join: each warp puts its 16 rows into shared memory as bf16 and writes them out.
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float inv = 1.f / l[h];
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n)
+        *reinterpret_cast<uint32_t*>(smem + swz<D>(ra + 8 * h, n) + 4 * (lane & 3)) =
+            pack_bf16x2(o[n][2 * h] * inv, o[n][2 * h + 1] * inv);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16 * C::CH / 32; ++i) {
+      const int r = wr * 16 + (lane + 32 * i) / C::CH, c = (lane + 32 * i) % C::CH;
+      if (r < rows)
+        *reinterpret_cast<uint4*>(out_row(r) + c * 8) =
+            *reinterpret_cast<const uint4*>(smem + swz<D>(r, c));
+    }
+    return;
+  }
+
   // Joining: every warp's (m, l, O) to shared memory, then the block's key groups, then the cluster.
   float* part = reinterpret_cast<float*>(smem);                       // [KW][RB][D]
   float* pm = reinterpret_cast<float*>(smem + C::OFF_ML);             // [KW][RB]
@@ -434,8 +523,6 @@ __global__ void __launch_bounds__(kThr, 2) cache_attn_kernel(const CacheArgs a) 
   float* jl = jm + C::RB;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
     const int r = ra + 8 * h;
     if ((lane & 3) == 0) {
       pm[wk * C::RB + r] = m[h];
@@ -479,9 +566,7 @@ __global__ void __launch_bounds__(kThr, 2) cache_attn_kernel(const CacheArgs a) 
   }
   const int n4 = rows * D / 4;
   auto store = [&](int i, float4 x) {
-    const int g = rb * C::RB + i / (D / 4);
-    bf16* dst = a.out + ((row0 + g / G) * a.H + (int64_t)hk * G + g % G) * D + (i % (D / 4)) * 4;
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+    *reinterpret_cast<uint2*>(out_row(i / (D / 4)) + i % (D / 4) * 4) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
   };
   if (a.split == 1) {
     for (int i = tid; i < n4; i += kThr) {
@@ -547,8 +632,11 @@ int cache_check(int64_t B, int64_t rows, int64_t R, int H, int Hkv, int d, int64
 
 constexpr int kMaxDevices = 64;
 
-// `keys`: about how many keys a unit walks. The key list is split while there are fewer blocks than
-// two per SM and each part keeps at least two tiles.
+// `keys`: no unit walks more. The key list is split while the blocks fit the device at two per SM and
+// the longest list leaves each part a tile: with few units the longest list sets the time (4 users
+// with trees: 14.3 us whole, 11.2 in two parts, 9.7 in eight; one token over 4,096 keys: 24.6 us in
+// two parts, 10.9 in eight), with many the parts only cost (256 users with trees 222 us, in two
+// parts 284 us).
 template <int D, int RW, bool TREE, typename IdxT>
 int launch_cache(CacheArgs a, int64_t max_rows, int64_t keys, int dev, int sms, cudaStream_t st) {
   using C = CCfg<D, RW, TREE>;
@@ -556,7 +644,7 @@ int launch_cache(CacheArgs a, int64_t max_rows, int64_t keys, int dev, int sms, 
   const int64_t units = a.B * a.Hkv * a.row_blocks;
   const int64_t tiles = (keys + kBK - 1) / kBK;
   a.split = 1;
-  while (a.split < kMaxSplit && units * a.split < 2 * sms && tiles >= 4 * a.split) a.split *= 2;
+  while (a.split < kMaxSplit && units * a.split <= sms && tiles >= 2 * a.split) a.split *= 2;
   if (units * a.split >= (int64_t)INT_MAX) return JCA_ERR_SHAPE;
   auto kernel = cache_attn_kernel<D, RW, TREE, IdxT>;
   static std::atomic<bool> set[kMaxDevices];
@@ -698,7 +786,7 @@ extern "C" int cand_tree_attn_fwd(const void* cand_q, const void* own_k, const v
   a.max_cand = max_cand;
   a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)d_head)) * 1.4426950408889634f;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int64_t max_rows = (int64_t)max_cand * (H / Hkv), keys = R / B + max_cand;
+  const int64_t max_rows = (int64_t)max_cand * (H / Hkv), keys = R + max_cand;
   return idx_bits == 32 ? launch_heads<true, int32_t>(a, d_head, max_rows, keys, dev, sms, st)
                         : launch_heads<true, int64_t>(a, d_head, max_rows, keys, dev, sms, st);
 }
