@@ -76,6 +76,36 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// The same wait for kernels with many waiting warps: the hardware may keep the thread suspended for
+// up to a millisecond per try, so that a waiting warp takes next to no issue slots from the warps it
+// shares a scheduler with.
+__device__ __forceinline__ bool mbar_try_wait_long(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity), "r"(1000000u)
+      : "memory");
+  return done != 0;
+}
+
+__device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity,
+                                               volatile int* abort_flag, int32_t* status) {
+  if (mbar_try_wait_long(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (mbar_try_wait_long(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > kWaitTimeoutNs) {
+      *abort_flag = 1;
+      atomicCAS(status, 0, (int32_t)JCA_STATUS_TIMEOUT);
+      return false;
+    }
+  }
+}
+
 // Teardown wait: ignores the abort flag, bounded by kDrainTimeoutNs.
 __device__ __forceinline__ bool mbar_wait_drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = global_timer_ns();

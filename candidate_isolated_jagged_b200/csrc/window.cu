@@ -207,7 +207,7 @@ __device__ __forceinline__ bool ring_take(Ring& r, const FwdArgs& a, Item& w,
                                           volatile int* abort_flag, bool& ok, int row = 0,
                                           int* start = nullptr) {
   const int s = (int)(r.k % kRing);
-  ok = mbar_wait(r.full + 8 * s, (r.k / kRing) & 1, abort_flag, a.status);
+  ok = mbar_wait_long(r.full + 8 * s, (r.k / kRing) & 1, abort_flag, a.status);
   if (!ok) return false;
   const volatile int* e = r.slot + kEntry * s;
   const bool more = e[0] >= 0;
@@ -234,7 +234,7 @@ __device__ void claim_role(const FwdArgs& a, Ring r, volatile int* abort_flag, i
         start[i] = a.row_start[min(q0 + 32 * i + lane, a.T - 1)];
     }
     const int s = (int)(r.k % kRing);
-    const bool ok = mbar_wait(r.empty + 8 * s, ((r.k / kRing) & 1) ^ 1, abort_flag, a.status);
+    const bool ok = mbar_wait_long(r.empty + 8 * s, ((r.k / kRing) & 1) ^ 1, abort_flag, a.status);
     if (!__all_sync(0xffffffffu, ok)) return;
     volatile int* e = r.slot + kEntry * s;
     if (lane == 0) e[0] = q0;
@@ -263,7 +263,7 @@ __device__ void producer_role(const CUtensorMap* tmQ, const CUtensorMap* tmKV, c
     const int hk = w.h / a.group;
     for (int j = 0; ok && j < w.n_tiles; ++j) {
       const int s = (int)(g % C::KVS);
-      ok = mbar_wait(bars + 8 * (empty + s), ((g / C::KVS) & 1) ^ 1, abort_flag, a.status);
+      ok = mbar_wait_long(bars + 8 * (empty + s), ((g / C::KVS) & 1) ^ 1, abort_flag, a.status);
       if (!ok) break;
       mbar_arrive_expect_tx(bars + 8 * (full + s), C::TILE_BYTES);
 #pragma unroll
@@ -275,7 +275,7 @@ __device__ void producer_role(const CUtensorMap* tmQ, const CUtensorMap* tmKV, c
       // The item's Q tiles go out behind its first K tile, whose stage was freed earlier.
       for (int t = 0; t < (w.has_b ? 2 : 1); ++t) {
         const int slot = t * C::QS + (int)(nq[t] % C::QS);
-        ok = mbar_wait(bars + 8 * (C::B_QEMPTY + slot), ((nq[t] / C::QS) & 1) ^ 1, abort_flag,
+        ok = mbar_wait_long(bars + 8 * (C::B_QEMPTY + slot), ((nq[t] / C::QS) & 1) ^ 1, abort_flag,
                        a.status);
         if (!ok) break;
         mbar_arrive_expect_tx(bars + 8 * (C::B_QFULL + slot), C::TILE_BYTES);
@@ -318,7 +318,7 @@ __device__ void padding_role(const FwdArgs& a, uint32_t sbase, uint32_t bars,
         const int k = row + 32 * c + lane;
         pad[c] = __ballot_sync(0xffffffffu, k < a.T && !a.valid[k]);
       }
-      ok = mbar_wait(bars + 8 * (C::B_VFULL + s), (g / C::KVS) & 1, abort_flag, a.status);
+      ok = mbar_wait_long(bars + 8 * (C::B_VFULL + s), (g / C::KVS) & 1, abort_flag, a.status);
       if (!__all_sync(0xffffffffu, ok)) return;
       const uint32_t tile = sbase + C::OFF_V + s * C::TILE_BYTES;
 #pragma unroll
@@ -364,15 +364,15 @@ __device__ void mma_role(const FwdArgs& a, uint32_t sbase, uint32_t bars, uint32
   bool pv_first = false, pv_last = false;
   auto issue_pv = [&]() -> bool {
     const int s = (int)(pv_g % C::KVS);
-    if (!mbar_wait(bars + 8 * (vfull + s), (pv_g / C::KVS) & 1, abort_flag, a.status)) return false;
+    if (!mbar_wait_long(bars + 8 * (vfull + s), (pv_g / C::KVS) & 1, abort_flag, a.status)) return false;
     if (pv_k == 0) {   // not read by this query tile
       mbar_arrive(bars + 8 * (C::B_VEMPTY + s));
       return true;
     }
     if (pv_first && items > 0 &&
-        !mbar_wait(bars + 8 * (C::B_OFREE + grp), (items - 1) & 1, abort_flag, a.status))
+        !mbar_wait_long(bars + 8 * (C::B_OFREE + grp), (items - 1) & 1, abort_flag, a.status))
       return false;
-    if (!mbar_wait(bars + 8 * (C::B_PFULL + grp), pvs & 1, abort_flag, a.status)) return false;
+    if (!mbar_wait_long(bars + 8 * (C::B_PFULL + grp), pvs & 1, abort_flag, a.status)) return false;
     ++pvs;
     tc_fence_after();
     // O (+)= P V; P sits in TMEM as bf16 pairs, 8 columns per 16 keys.
@@ -401,13 +401,13 @@ __device__ void mma_role(const FwdArgs& a, uint32_t sbase, uint32_t bars, uint32
       const int s = (int)(g % C::KVS);
       const bool reads = grp ? w.b_reads(j) : w.a_reads(j);
       const int keys = w.is_sink(j) ? (w.n_sink + 15) & ~15 : C::BN;
-      ok = mbar_wait(bars + 8 * (C::B_KFULL + s), (g / C::KVS) & 1, abort_flag, a.status);
+      ok = mbar_wait_long(bars + 8 * (C::B_KFULL + s), (g / C::KVS) & 1, abort_flag, a.status);
       if (!ok) break;
       if (reads) {
         if (!seen)
-          ok = mbar_wait(bars + 8 * (C::B_QFULL + slot), (qn / C::QS) & 1, abort_flag, a.status);
+          ok = mbar_wait_long(bars + 8 * (C::B_QFULL + slot), (qn / C::QS) & 1, abort_flag, a.status);
         if (C::SEP_P && ok && steps > 0)
-          ok = mbar_wait(bars + 8 * (C::B_SREAD + grp), (steps - 1) & 1, abort_flag, a.status);
+          ok = mbar_wait_long(bars + 8 * (C::B_SREAD + grp), (steps - 1) & 1, abort_flag, a.status);
         if (!ok) break;
         tc_fence_after();
         const uint64_t k = dk + (uint64_t)((s * C::TILE_BYTES) >> 4);
@@ -553,7 +553,7 @@ __device__ void softmax_role(const FwdArgs& a, uint32_t bars, uint32_t tmem,
         }
       }
       ok = __all_sync(0xffffffffu,
-                      mbar_wait(bars + 8 * (C::B_SFULL + grp), lt & 1, abort_flag, a.status));
+                      mbar_wait_long(bars + 8 * (C::B_SFULL + grp), lt & 1, abort_flag, a.status));
       if (!ok) break;
       ++lt;
       tc_fence_after();
@@ -590,7 +590,7 @@ __device__ void softmax_role(const FwdArgs& a, uint32_t bars, uint32_t tmem,
       const float2 sl2v = make_float2(sl2, sl2), negv = make_float2(neg_m, neg_m);
       if (C::SEP_P && lt > 1) {
         // The PV before has read the weights that these replace, and O is stable.
-        ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (C::B_PVDONE + grp), lt & 1, abort_flag,
+        ok = __all_sync(0xffffffffu, mbar_wait_long(bars + 8 * (C::B_PVDONE + grp), lt & 1, abort_flag,
                                                a.status));
         if (!ok) break;
         tc_fence_after();
@@ -619,7 +619,7 @@ __device__ void softmax_role(const FwdArgs& a, uint32_t bars, uint32_t tmem,
     }
     if (!ok) break;
     ok = __all_sync(0xffffffffu,
-                    mbar_wait(bars + 8 * (C::B_OREADY + grp), oi & 1, abort_flag, a.status));
+                    mbar_wait_long(bars + 8 * (C::B_OREADY + grp), oi & 1, abort_flag, a.status));
     if (!ok) break;
     ++oi;
     tc_fence_after();

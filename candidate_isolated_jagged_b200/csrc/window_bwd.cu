@@ -14,7 +14,7 @@
 //     long history for its few first tokens.
 // Row tiles are cut from the packed rows whatever users they hold, as in the forward.
 //
-// Kernel (one persistent block per SM, 12 warps; tcgen05 with TMEM accumulators, TMA loads). O1/O2 are
+// Kernel (one persistent block per SM, 16 warps; tcgen05 with TMEM accumulators, TMA loads). O1/O2 are
 // the unit's outer tiles, I1/I2 the inner tiles streamed through a ring:
 //   S = O1 I1^T,  dP = O2 I2^T  (SS MMAs)   ->   dS (and P) as bf16 in TMEM   ->   TS MMAs
 //   dQ  (O1 = Q, O2 = dO, I1 = K, I2 = V):   acc0 += dS I1
@@ -22,9 +22,10 @@
 // An inner tile is taken as two half steps of 64 rows, so that S and dP fit twice in TMEM and the
 // tensor core works on step t + 1 while the compute warps do step t. Columns a warp's rows do not
 // see are decided per 32 columns: none (zeros are written), all (no masking) or some.
-//   warp 0      TMA loads;  warp 1  MMA issue (one thread);  warps 2..9  compute, a row a thread,
-//   two warps per 32 rows (32 of the 64 columns each);  warp 10  with padding: zeroes the padding
-//   rows of the inner tiles;  warp 11  claims units and posts them to a ring.
+//   warp 0      TMA loads;  warp 1  MMA issue (one thread);  warp 2  with padding: zeroes the padding
+//   rows of the inner tiles;  warp 3  claims units and posts them to a ring;  warps 4..11  compute, a
+//   row a thread, two warps per 32 rows (32 of the 64 columns each);  warps 12..15  write a unit's
+//   accumulators out while the others are at the next unit.
 //
 // What bounds it: seven products per pair instead of five (S and dP are formed in both passes) on
 // the tensor core, whose 64-column steps cost the issuing thread about what 128-column ones would.
@@ -47,8 +48,11 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 constexpr int kDQ = 0, kDKV = 1, kSink = 2;   // kSink: dKV of first tokens from behind the window
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kCompute = 256;
+constexpr int kEpilogue = 128;
+// Registers a thread: 512 x 128 at launch, shared out anew (72 + 2 x 168 + 104 = 4 x 128).
+constexpr int kRegsRoles = 72, kRegsCompute = 168, kRegsEpilogue = 104;
 constexpr int kStages = 2;
 constexpr int kHalf = 64;        // inner rows of a half step
 // Query rows of a kSink unit: 256 rows keep the longest unit at 8 half steps (16 users: 14 us, with
@@ -76,6 +80,7 @@ struct BwdArgs {
   int32_t* counter;
   int32_t* status;
   int T, H, Hkv, group, window, n_sinks, n_units;
+  int v8;                     // gradients can be written with 32-byte stores
   float scale, scale_log2;
 };
 
@@ -183,7 +188,7 @@ template <int MODE>
 __device__ __forceinline__ bool ring_take(Ring& r, const BwdArgs& a, Unit& u,
                                           volatile int* abort_flag, bool& ok) {
   const int s = (int)(r.k % kRing);
-  ok = mbar_wait(r.full + 8 * s, (r.k / kRing) & 1, abort_flag, a.status);
+  ok = mbar_wait_long(r.full + 8 * s, (r.k / kRing) & 1, abort_flag, a.status);
   if (!ok) return false;
   const volatile int* e = r.slot + kEntry * s;
   const bool more = e[0] >= 0;
@@ -224,7 +229,7 @@ __device__ void claim_role(const BwdArgs& a, Ring r, volatile int* abort_flag) {
       }
     }
     const int s = (int)(r.k % kRing);
-    if (!mbar_wait(r.empty + 8 * s, ((r.k / kRing) & 1) ^ 1, abort_flag, a.status)) return;
+    if (!mbar_wait_long(r.empty + 8 * s, ((r.k / kRing) & 1) ^ 1, abort_flag, a.status)) return;
 #pragma unroll
     for (int i = 0; i < kEntry; ++i) r.slot[kEntry * s + i] = e[i];
     mbar_arrive(r.full + 8 * s);
@@ -244,7 +249,7 @@ __device__ void producer_role(const CUtensorMap* tmO1, const CUtensorMap* tmO2,
   while (ok && ring_take<MODE>(ring, a, u, abort_flag, ok)) {
     for (int i = 0; i < u.n_in; ++i) {
       const int s = (int)(g % kStages);
-      ok = mbar_wait(bars + 8 * (C::B_INEMPTY + s), ((g / kStages) & 1) ^ 1, abort_flag, a.status);
+      ok = mbar_wait_long(bars + 8 * (C::B_INEMPTY + s), ((g / kStages) & 1) ^ 1, abort_flag, a.status);
       if (!ok) break;
       mbar_arrive_expect_tx(bars + 8 * (C::B_INFULL + s), 2 * C::TILE_BYTES);
       const uint32_t dst = sbase + C::OFF_IN + s * 2 * C::TILE_BYTES;
@@ -259,7 +264,7 @@ __device__ void producer_role(const CUtensorMap* tmO1, const CUtensorMap* tmO2,
       ++g;
       if (i > 0) continue;
       // The outer tiles go out behind the unit's first inner tiles, whose stage was freed earlier.
-      ok = mbar_wait(bars + 8 * C::B_OUTEMPTY, (units & 1) ^ 1, abort_flag, a.status);
+      ok = mbar_wait_long(bars + 8 * C::B_OUTEMPTY, (units & 1) ^ 1, abort_flag, a.status);
       if (!ok) break;
       mbar_arrive_expect_tx(bars + 8 * C::B_OUTFULL, 2 * C::TILE_BYTES);
       ++units;
@@ -300,7 +305,7 @@ __device__ void padding_role(const BwdArgs& a, uint32_t sbase, uint32_t bars,
         const int k = row + 32 * c + lane;
         pad[c] = __ballot_sync(0xffffffffu, k < a.T && !a.valid[k]);
       }
-      ok = mbar_wait(bars + 8 * (C::B_INFULL + s), (g / kStages) & 1, abort_flag, a.status);
+      ok = mbar_wait_long(bars + 8 * (C::B_INFULL + s), (g / kStages) & 1, abort_flag, a.status);
       if (!__all_sync(0xffffffffu, ok)) return;
       const uint32_t tile = sbase + C::OFF_IN + s * 2 * C::TILE_BYTES;
 #pragma unroll
@@ -382,13 +387,13 @@ __device__ void mma_role(const BwdArgs& a, uint32_t sbase, uint32_t bars, uint32
     ++steps;
   };
   auto issue_ts = [&](const HalfStep& h, uint32_t stage, bool first, bool closes) -> bool {
-    if (!mbar_wait(bars + 8 * (C::B_DSFULL + (int)(ts_steps & 1)), (ts_steps >> 1) & 1, abort_flag,
+    if (!mbar_wait_long(bars + 8 * (C::B_DSFULL + (int)(ts_steps & 1)), (ts_steps >> 1) & 1, abort_flag,
                    a.status))
       return false;
     const uint32_t buf = (ts_steps & 1) * C::TMEM_BUF;
     ++ts_steps;
     if (first && acc_units > 0 &&
-        !mbar_wait(bars + 8 * C::B_ACCFREE, (acc_units - 1) & 1, abort_flag, a.status))
+        !mbar_wait_long(bars + 8 * C::B_ACCFREE, (acc_units - 1) & 1, abort_flag, a.status))
       return false;
     tc_fence_after();
     const int ksteps = (h.valid + 15) >> 4;
@@ -405,7 +410,7 @@ __device__ void mma_role(const BwdArgs& a, uint32_t sbase, uint32_t bars, uint32
     return true;
   };
   auto wait_in = [&](uint32_t stage) -> bool {
-    if (!mbar_wait(bars + 8 * (infull + (int)stage), (g / kStages) & 1, abort_flag, a.status))
+    if (!mbar_wait_long(bars + 8 * (infull + (int)stage), (g / kStages) & 1, abort_flag, a.status))
       return false;
     tc_fence_after();
     return true;
@@ -416,15 +421,17 @@ __device__ void mma_role(const BwdArgs& a, uint32_t sbase, uint32_t bars, uint32
     uint32_t stage = g % kStages;
     ok = wait_in(stage);
     if (!ok) break;
-    ok = mbar_wait(bars + 8 * C::B_OUTFULL, units & 1, abort_flag, a.status);
+    ok = mbar_wait_long(bars + 8 * C::B_OUTFULL, units & 1, abort_flag, a.status);
     if (!ok) break;
     ++units;
     tc_fence_after();
     issue_ss(cur, stage);
-    bool first = true;
+    HalfStep nxt = cur;
+    bool more = next_half<MODE>(u, nxt), first = true;
+    // The outer tiles are free once the unit's last S and dP are formed: the next unit's load then
+    // runs beside the last half step.
+    if (!more) tc_commit(bars + 8 * C::B_OUTEMPTY);
     for (;;) {
-      HalfStep nxt = cur;
-      const bool more = next_half<MODE>(u, nxt);
       uint32_t nstage = stage;
       if (more && nxt.hh == 0) {
         ++g;
@@ -432,17 +439,24 @@ __device__ void mma_role(const BwdArgs& a, uint32_t sbase, uint32_t bars, uint32
         ok = wait_in(nstage);
         if (!ok) break;
       }
-      if (more) issue_ss(nxt, nstage);
-      ok = issue_ts(cur, stage, first, !(more && nxt.hh == 1));
+      const bool closes = !(more && nxt.hh == 1);
+      const HalfStep ahead = nxt;
+      bool more_ahead = false;
+      if (more) {
+        issue_ss(nxt, nstage);
+        more_ahead = next_half<MODE>(u, nxt);
+        if (!more_ahead) tc_commit(bars + 8 * C::B_OUTEMPTY);
+      }
+      ok = issue_ts(cur, stage, first, closes);
       if (!ok) break;
       first = false;
       if (!more) break;
-      cur = nxt;
+      cur = ahead;
       stage = nstage;
+      more = more_ahead;
     }
     if (!ok) break;
     ++g;
-    tc_commit(bars + 8 * C::B_OUTEMPTY);
     tc_commit(bars + 8 * C::B_ACCFULL);
     ++acc_units;
   }
@@ -460,26 +474,18 @@ __device__ __forceinline__ uint32_t range_bits(int a, int b) {
   return a >= 32 ? 0u : below_b & (0xffffffffu << a);
 }
 
-__device__ __forceinline__ void store_bf16x8(bf16* p, const float* o) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
-                                            pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
-}
-
 template <int D, int MODE>
 __device__ void compute_role(const BwdArgs& a, uint32_t bars, uint32_t tmem, float* cols,
                              volatile int* abort_flag, int warp, int lane, Ring ring) {
   using C = Cfg<D>;
   const int quarter = warp & 3;
-  const int ch = (warp - 2) >> 2;               // 32-column half of every half step
+  const int ch = (warp - 4) >> 2;               // 32-column half of every half step
   const int r = quarter * 32 + lane;            // outer row of this thread inside its tile
   const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
   const uint32_t t_s = t_lane + C::TMEM_S + 32 * ch, t_p = t_lane + C::TMEM_P + 32 * ch;
-  constexpr int HD = D / 2;                     // accumulator columns of this warp
-  constexpr int CW = HD < 32 ? HD : 32;
-  const uint32_t t_a0 = t_lane + C::TMEM_A0 + ch * HD, t_a1 = t_lane + C::TMEM_A1 + ch * HD;
   const float2 sl2v = make_float2(a.scale_log2, a.scale_log2);
   const size_t T = (size_t)a.T;
-  uint32_t sp_seen = 0, acc_seen = 0, cols_n = 0;
+  uint32_t sp_seen = 0, cols_n = 0;
   bool ok = true;
   Unit u;
   for (;;) {
@@ -525,7 +531,7 @@ __device__ void compute_role(const BwdArgs& a, uint32_t bars, uint32_t tmem, flo
         cl[ch * kTileN + r] = next_stat;
         mbar_arrive(bars + 8 * (C::B_COLS + (cols_n & 1)));
         if (i + 1 < u.n_in) next_stat = col_stat(i + 1);
-        ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (C::B_COLS + (cols_n & 1)),
+        ok = __all_sync(0xffffffffu, mbar_wait_long(bars + 8 * (C::B_COLS + (cols_n & 1)),
                                                (cols_n >> 1) & 1, abort_flag, a.status));
         ++cols_n;
         if (!ok) break;
@@ -545,7 +551,7 @@ __device__ void compute_role(const BwdArgs& a, uint32_t bars, uint32_t tmem, flo
         }
         const bool any = __any_sync(0xffffffffu, bits != 0u);
         const bool all = __all_sync(0xffffffffu, bits == 0xffffffffu);
-        ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * (C::B_SPFULL + b), (sp_seen >> 1) & 1,
+        ok = __all_sync(0xffffffffu, mbar_wait_long(bars + 8 * (C::B_SPFULL + b), (sp_seen >> 1) & 1,
                                                abort_flag, a.status));
         if (!ok) break;
         ++sp_seen;
@@ -601,79 +607,82 @@ __device__ void compute_role(const BwdArgs& a, uint32_t bars, uint32_t tmem, flo
       if (!ok) break;
     }
     if (!ok) break;
-    ok = __all_sync(0xffffffffu,
-                    mbar_wait(bars + 8 * C::B_ACCFULL, acc_seen & 1, abort_flag, a.status));
-    if (!ok) break;
-    ++acc_seen;
-    tc_fence_after();
-    // Epilogue: this warp's half of the accumulator columns.
-    const size_t base = ((size_t)row * (MODE == kDQ ? a.H : a.Hkv) + u.oh) * D + ch * HD;
-    if (MODE == kDQ) {
+  }
+}
+
+// Writes a unit's accumulators out, a row a thread, while the compute warps are at the next unit.
+template <int D, int MODE>
+__device__ void epilogue_role(const BwdArgs& a, uint32_t bars, uint32_t tmem,
+                              volatile int* abort_flag, int warp, int lane, Ring ring) {
+  using C = Cfg<D>;
+  constexpr int CW = 16;
+  const int r = (warp & 3) * 32 + lane;
+  const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+  const uint32_t t_a0 = t_lane + C::TMEM_A0, t_a1 = t_lane + C::TMEM_A1;
+  uint32_t seen = 0;
+  bool ok = true;
+  Unit u;
+  auto put = [&](bf16* dst, const uint32_t* x, float f) {
+    uint32_t p[8];
 #pragma unroll
-      for (int c0 = 0; c0 < HD; c0 += CW) {
-        uint32_t acc[CW];
-        tmem_ld_cols<CW>(t_a0 + c0, acc);
-        tmem_wait_ld();
-        reg_fence_cols<CW>(acc);
-        if (c0 + CW >= HD) {
-          tc_fence_before();
-          mbar_arrive(bars + 8 * C::B_ACCFREE);
-        }
-        if (!row_ok) continue;
-#pragma unroll
-        for (int x = 0; x < CW; x += 8) {
-          float o[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = a.scale * __uint_as_float(acc[x + e]);
-          store_bf16x8(a.dq + base + c0 + x, o);
-        }
-      }
-      continue;
+    for (int k = 0; k < 8; ++k)
+      p[k] = pack_bf16x2(__uint_as_float(x[2 * k]) * f, __uint_as_float(x[2 * k + 1]) * f);
+    if (a.v8) {
+      st_global_v8(dst, p);
+    } else {
+      reinterpret_cast<uint4*>(dst)[0] = make_uint4(p[0], p[1], p[2], p[3]);
+      reinterpret_cast<uint4*>(dst)[1] = make_uint4(p[4], p[5], p[6], p[7]);
     }
+  };
+  for (;;) {
+    const bool more = ring_take<MODE>(ring, a, u, abort_flag, ok);
+    if (!__all_sync(0xffffffffu, more)) break;
+    const int row = u.orow0 + r;
+    const bool row_ok = row < a.T;
     // Sums of first tokens that rows behind the window see too stay in fp32 partials.
     float* mine = nullptr;
     bool writes = row_ok;
     if (MODE == kSink) {
       writes = r < a.n_sinks;
-      mine = a.part + (((size_t)u.slot * a.Hkv + u.oh) * a.n_sinks + r) * 2 * D + ch * HD;
-    } else if (a.part && row_ok && row - start < a.n_sinks &&
-               a.row_end[row] - start > a.window) {
-      const size_t slot = (size_t)a.window_slot + a.row_user[row];
-      mine = a.part + ((slot * a.Hkv + u.oh) * a.n_sinks + (row - start)) * 2 * D + ch * HD;
+      mine = a.part + (((size_t)u.slot * a.Hkv + u.oh) * a.n_sinks + r) * 2 * D;
+    } else if (MODE == kDKV && a.part && row_ok) {
+      const int start = a.row_start[row];
+      if (row - start < a.n_sinks && a.row_end[row] - start > a.window) {
+        const size_t slot = (size_t)a.window_slot + a.row_user[row];
+        mine = a.part + ((slot * a.Hkv + u.oh) * a.n_sinks + (row - start)) * 2 * D;
+      }
     }
-#pragma unroll
-    for (int c0 = 0; c0 < HD; c0 += CW) {
-      uint32_t dvv[CW], dkk[CW];
-      tmem_ld_cols<CW>(t_a0 + c0, dvv);
-      tmem_ld_cols<CW>(t_a1 + c0, dkk);
+    const size_t base = ((size_t)row * (MODE == kDQ ? a.H : a.Hkv) + u.oh) * D;
+    ok = __all_sync(0xffffffffu,
+                    mbar_wait_long(bars + 8 * C::B_ACCFULL, seen & 1, abort_flag, a.status));
+    if (!ok) break;
+    ++seen;
+    tc_fence_after();
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += CW) {
+      uint32_t x[CW], y[CW];
+      tmem_ld_x16(t_a0 + c0, x);
+      if (MODE != kDQ) tmem_ld_x16(t_a1 + c0, y);
       tmem_wait_ld();
-      reg_fence_cols<CW>(dvv);
-      reg_fence_cols<CW>(dkk);
-      if (c0 + CW >= HD) {
+      reg_fence16(x);
+      if (MODE != kDQ) reg_fence16(y);
+      if (c0 + CW >= D) {
         tc_fence_before();
         mbar_arrive(bars + 8 * C::B_ACCFREE);
       }
       if (!writes) continue;
+      if (MODE == kDQ) {
+        put(a.dq + base + c0, x, a.scale);
+      } else if (mine) {
+        uint4* m = reinterpret_cast<uint4*>(mine + c0);
 #pragma unroll
-      for (int x = 0; x < CW; x += 8) {
-        float v[8], k[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          v[e] = __uint_as_float(dvv[x + e]);
-          k[e] = __uint_as_float(dkk[x + e]);
+        for (int k = 0; k < CW / 4; ++k) {
+          m[k] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+          m[D / 4 + k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
         }
-        if (mine) {
-          float4* m = reinterpret_cast<float4*>(mine + c0 + x);
-          m[0] = make_float4(v[0], v[1], v[2], v[3]);
-          m[1] = make_float4(v[4], v[5], v[6], v[7]);
-          m[D / 4] = make_float4(k[0], k[1], k[2], k[3]);
-          m[D / 4 + 1] = make_float4(k[4], k[5], k[6], k[7]);
-        } else if (MODE == kDKV) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) k[e] *= a.scale;
-          store_bf16x8(a.dv + base + c0 + x, v);
-          store_bf16x8(a.dk + base + c0 + x, k);
-        }
+      } else if (MODE == kDKV) {
+        put(a.dv + base + c0, x, 1.f);
+        put(a.dk + base + c0, y, a.scale);
       }
     }
   }
@@ -699,12 +708,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     *skip = *a.status != 0;   // an error recorded earlier makes the launch a no-op
     for (int i = 0; i < C::NUM_BARS; ++i) {
       uint32_t n = 1;
-      if (i == C::B_DSFULL || i == C::B_DSFULL + 1 || i == C::B_ACCFREE || i == C::B_COLS ||
-          i == C::B_COLS + 1)
+      if (i == C::B_DSFULL || i == C::B_DSFULL + 1 || i == C::B_COLS || i == C::B_COLS + 1)
         n = kCompute;
+      if (i == C::B_ACCFREE) n = kEpilogue;
       if (i >= C::B_INREADY && i < C::B_INREADY + kStages) n = 32;
-      // Readers of the ring: the producer and MMA threads, the compute warps, the padding warp.
-      if (i >= C::B_RINGEMPTY) n = 2 + kCompute + (a.valid ? 32 : 0);
+      // Readers of the ring: producer and MMA threads, compute, epilogue and padding warps.
+      if (i >= C::B_RINGEMPTY) n = 2 + kCompute + kEpilogue + (a.valid ? 32 : 0);
       mbar_init(bars + 8 * i, n);
     }
     *abort_flag = 0;
@@ -727,20 +736,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;
   Ring ring{reinterpret_cast<volatile int*>(smem + C::OFF_RING), bars + 8 * C::B_RINGFULL,
             bars + 8 * C::B_RINGEMPTY, 0u};
-  if (!*skip) {
-    if (warp == 0) {
+  if (warp < 4) {
+    set_max_regs_dec<kRegsRoles>();
+    if (*skip) {
+    } else if (warp == 0) {
       if (lane == 0)
         producer_role<D, MODE>(&tmO1, &tmO2, &tmI1, &tmI2, a, sbase, bars, abort_flag, ring);
     } else if (warp == 1) {
       if (lane == 0) mma_role<D, MODE>(a, sbase, bars, tmem, abort_flag, ring);
-    } else if (warp < 10) {
-      compute_role<D, MODE>(a, bars, tmem, reinterpret_cast<float*>(smem + C::OFF_COLS),
-                            abort_flag, warp, lane, ring);
-    } else if (warp == 10) {
+    } else if (warp == 2) {
       if (a.valid) padding_role<D, MODE>(a, sbase, bars, abort_flag, lane, ring);
     } else if (lane == 0) {
       claim_role<MODE>(a, ring, abort_flag);
     }
+  } else if (warp < 12) {
+    set_max_regs_inc<kRegsCompute>();
+    if (!*skip)
+      compute_role<D, MODE>(a, bars, tmem, reinterpret_cast<float*>(smem + C::OFF_COLS),
+                            abort_flag, warp, lane, ring);
+  } else {
+    set_max_regs_dec<kRegsEpilogue>();
+    if (!*skip) epilogue_role<D, MODE>(a, bars, tmem, abort_flag, warp, lane, ring);
   }
   tc_fence_before();
   __syncthreads();
@@ -989,6 +1005,7 @@ extern "C" int jagged_window_attn_bwd(const void* q, const void* k, const void* 
   a.group = H / Hkv;
   a.window = (int)(window < T ? window : (T > 0 ? T : 1));
   a.n_sinks = n_sinks;
+  a.v8 = aligned(dq, 32) && aligned(dk, 32) && aligned(dv, 32);
   a.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)d_head);
   a.scale_log2 = a.scale * 1.4426950408889634f;
   rc = window_plan(offsets, B, T, idx_bits, reinterpret_cast<int32_t*>(ws + L.row_start),
