@@ -207,7 +207,7 @@ __device__ __forceinline__ bool ring_take(Ring& r, const FwdArgs& a, Item& w,
                                           volatile int* abort_flag, bool& ok, int row = 0,
                                           int* start = nullptr) {
   const int s = (int)(r.k % kRing);
-  ok = mbar_wait_long(r.full + 8 * s, (r.k / kRing) & 1, abort_flag, a.status);
+  ok = mbar_wait(r.full + 8 * s, (r.k / kRing) & 1, abort_flag, a.status);
   if (!ok) return false;
   const volatile int* e = r.slot + kEntry * s;
   const bool more = e[0] >= 0;
@@ -263,7 +263,7 @@ __device__ void producer_role(const CUtensorMap* tmQ, const CUtensorMap* tmKV, c
     const int hk = w.h / a.group;
     for (int j = 0; ok && j < w.n_tiles; ++j) {
       const int s = (int)(g % C::KVS);
-      ok = mbar_wait_long(bars + 8 * (empty + s), ((g / C::KVS) & 1) ^ 1, abort_flag, a.status);
+      ok = mbar_wait(bars + 8 * (empty + s), ((g / C::KVS) & 1) ^ 1, abort_flag, a.status);
       if (!ok) break;
       mbar_arrive_expect_tx(bars + 8 * (full + s), C::TILE_BYTES);
 #pragma unroll
@@ -275,7 +275,7 @@ __device__ void producer_role(const CUtensorMap* tmQ, const CUtensorMap* tmKV, c
       // The item's Q tiles go out behind its first K tile, whose stage was freed earlier.
       for (int t = 0; t < (w.has_b ? 2 : 1); ++t) {
         const int slot = t * C::QS + (int)(nq[t] % C::QS);
-        ok = mbar_wait_long(bars + 8 * (C::B_QEMPTY + slot), ((nq[t] / C::QS) & 1) ^ 1, abort_flag,
+        ok = mbar_wait(bars + 8 * (C::B_QEMPTY + slot), ((nq[t] / C::QS) & 1) ^ 1, abort_flag,
                        a.status);
         if (!ok) break;
         mbar_arrive_expect_tx(bars + 8 * (C::B_QFULL + slot), C::TILE_BYTES);

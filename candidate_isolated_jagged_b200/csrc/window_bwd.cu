@@ -22,10 +22,11 @@
 // An inner tile is taken as two half steps of 64 rows, so that S and dP fit twice in TMEM and the
 // tensor core works on step t + 1 while the compute warps do step t. Columns a warp's rows do not
 // see are decided per 32 columns: none (zeros are written), all (no masking) or some.
-//   warp 0      TMA loads;  warp 1  MMA issue (one thread);  warp 2  with padding: zeroes the padding
-//   rows of the inner tiles;  warp 3  claims units and posts them to a ring;  warps 4..11  compute, a
-//   row a thread, two warps per 32 rows (32 of the 64 columns each);  warps 12..15  write a unit's
-//   accumulators out while the others are at the next unit.
+//   warp 0      lane 0: TMA loads, lane 1: claims units and posts them to a ring;
+//   warps 1, 2  one thread each issues the SS and the TS MMAs;
+//   warp 3      with padding: zeroes the padding rows of the inner tiles;
+//   warps 4..11 compute, a row a thread, two warps per 32 rows (32 of the 64 columns each);
+//   warps 12..15 write a unit's accumulators out while the others are at the next unit.
 //
 // What bounds it: seven products per pair instead of five (S and dP are formed in both passes) on
 // the tensor core, whose 64-column steps cost the issuing thread about what 128-column ones would.
@@ -109,8 +110,9 @@ struct Cfg {
   static constexpr int B_ACCFULL = B_DSFULL + 2;
   static constexpr int B_ACCFREE = B_ACCFULL + 1;
   static constexpr int B_COLS = B_ACCFREE + 1;                        // [2] column statistics
-  static constexpr int B_DRAIN = B_COLS + 2;
-  static constexpr int B_RINGFULL = B_DRAIN + 1;
+  static constexpr int B_BUFFREE = B_COLS + 2;                        // [2] S and dP read by TS
+  static constexpr int B_DRAIN = B_BUFFREE + 2;                       // [2] MMA threads
+  static constexpr int B_RINGFULL = B_DRAIN + 2;
   static constexpr int B_RINGEMPTY = B_RINGFULL + kRing;
   static constexpr int NUM_BARS = B_RINGEMPTY + kRing;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
@@ -188,7 +190,7 @@ template <int MODE>
 __device__ __forceinline__ bool ring_take(Ring& r, const BwdArgs& a, Unit& u,
                                           volatile int* abort_flag, bool& ok) {
   const int s = (int)(r.k % kRing);
-  ok = mbar_wait_long(r.full + 8 * s, (r.k / kRing) & 1, abort_flag, a.status);
+  ok = mbar_wait(r.full + 8 * s, (r.k / kRing) & 1, abort_flag, a.status);
   if (!ok) return false;
   const volatile int* e = r.slot + kEntry * s;
   const bool more = e[0] >= 0;
@@ -229,7 +231,7 @@ __device__ void claim_role(const BwdArgs& a, Ring r, volatile int* abort_flag) {
       }
     }
     const int s = (int)(r.k % kRing);
-    if (!mbar_wait_long(r.empty + 8 * s, ((r.k / kRing) & 1) ^ 1, abort_flag, a.status)) return;
+    if (!mbar_wait(r.empty + 8 * s, ((r.k / kRing) & 1) ^ 1, abort_flag, a.status)) return;
 #pragma unroll
     for (int i = 0; i < kEntry; ++i) r.slot[kEntry * s + i] = e[i];
     mbar_arrive(r.full + 8 * s);
@@ -249,7 +251,7 @@ __device__ void producer_role(const CUtensorMap* tmO1, const CUtensorMap* tmO2,
   while (ok && ring_take<MODE>(ring, a, u, abort_flag, ok)) {
     for (int i = 0; i < u.n_in; ++i) {
       const int s = (int)(g % kStages);
-      ok = mbar_wait_long(bars + 8 * (C::B_INEMPTY + s), ((g / kStages) & 1) ^ 1, abort_flag, a.status);
+      ok = mbar_wait(bars + 8 * (C::B_INEMPTY + s), ((g / kStages) & 1) ^ 1, abort_flag, a.status);
       if (!ok) break;
       mbar_arrive_expect_tx(bars + 8 * (C::B_INFULL + s), 2 * C::TILE_BYTES);
       const uint32_t dst = sbase + C::OFF_IN + s * 2 * C::TILE_BYTES;
@@ -264,7 +266,7 @@ __device__ void producer_role(const CUtensorMap* tmO1, const CUtensorMap* tmO2,
       ++g;
       if (i > 0) continue;
       // The outer tiles go out behind the unit's first inner tiles, whose stage was freed earlier.
-      ok = mbar_wait_long(bars + 8 * C::B_OUTEMPTY, (units & 1) ^ 1, abort_flag, a.status);
+      ok = mbar_wait(bars + 8 * C::B_OUTEMPTY, (units & 1) ^ 1, abort_flag, a.status);
       if (!ok) break;
       mbar_arrive_expect_tx(bars + 8 * C::B_OUTFULL, 2 * C::TILE_BYTES);
       ++units;
@@ -345,124 +347,135 @@ __device__ __forceinline__ bool next_half(const Unit& u, HalfStep& h) {
   return true;
 }
 
+// The S and dP products of every half step, one thread. A buffer is formed anew once the TS products of
+// two half steps before have read it.
 template <int D, int MODE>
-__device__ void mma_role(const BwdArgs& a, uint32_t sbase, uint32_t bars, uint32_t tmem,
-                         volatile int* abort_flag, Ring ring) {
+__device__ void ss_role(const BwdArgs& a, uint32_t sbase, uint32_t bars, uint32_t tmem,
+                        volatile int* abort_flag, Ring ring) {
   using C = Cfg<D>;
   constexpr uint32_t kIdescSS = idesc_bf16_f32(C::BM, kHalf, false, false);
   constexpr uint32_t kIdesc0 = kIdescSS & ~(0x3Fu << 17);
-  constexpr uint32_t kIdescTS = idesc_bf16_f32(C::BM, D, false, true);
   constexpr uint32_t kHalfRows = (kHalf * C::SW) >> 4;
-  constexpr uint32_t kStep = (16 * C::SW) >> 4;
   const int infull = a.valid ? C::B_INREADY : C::B_INFULL;
   const uint64_t o1 = smem_desc(sbase + C::OFF_OUT, 16, 8 * C::SW, C::LAYOUT);
   const uint64_t o2 = o1 + (uint64_t)(C::TILE_BYTES >> 4);
   const uint64_t in_k = smem_desc(sbase + C::OFF_IN, 16, 8 * C::SW, C::LAYOUT);
-  const uint64_t in_mn = smem_desc(sbase + C::OFF_IN, C::BLK_BYTES, 8 * C::SW, C::LAYOUT);
-  uint32_t units = 0, g = 0, steps = 0, ts_steps = 0, acc_units = 0;
+  uint32_t units = 0, g = 0, steps = 0;
   bool ok = true;
   Unit u;
-  auto ss = [&](uint32_t d_tmem, uint64_t x, uint64_t y, uint32_t idesc) {
-#pragma unroll
-    for (int kk = 0; kk < C::KSTEPS_QK; ++kk) {
-      const uint32_t off = ((kk / C::KSTEPS_PER_BLK) * C::BLK_BYTES +
-                            (kk % C::KSTEPS_PER_BLK) * 32) >> 4;
-      tc_mma(d_tmem, x + off, y + off, idesc, kk > 0 ? 1u : 0u);
-    }
-  };
-  // The pairs of a half step sit in two 16-column runs, one per compute warp of a lane quarter.
-  auto ts = [&](uint32_t acc, uint32_t p, uint64_t y, int ksteps, bool overwrite) {
-    for (int kk = 0; kk < ksteps; ++kk)
-      tc_mma_ts(acc, p + (uint32_t)(kk >> 1) * 32u + (uint32_t)(kk & 1) * 8u,
-                y + (uint64_t)(kk * kStep), kIdescTS, (overwrite && kk == 0) ? 0u : 1u);
-  };
-  auto issue_ss = [&](const HalfStep& h, uint32_t stage) {
-    const uint32_t idesc = kIdesc0 | ((uint32_t)(((h.valid + 15) & ~15) >> 3) << 17);
-    const uint64_t i1 = in_k + (uint64_t)((stage * 2 * C::TILE_BYTES) >> 4) +
-                        (uint64_t)(h.hh * kHalfRows);
-    const uint32_t buf = (steps & 1) * C::TMEM_BUF;
-    ss(tmem + buf + C::TMEM_S, o1, i1, idesc);
-    ss(tmem + buf + C::TMEM_P, o2, i1 + (uint64_t)(C::TILE_BYTES >> 4), idesc);
-    tc_commit(bars + 8 * (C::B_SPFULL + (int)(steps & 1)));
-    ++steps;
-  };
-  auto issue_ts = [&](const HalfStep& h, uint32_t stage, bool first, bool closes) -> bool {
-    if (!mbar_wait_long(bars + 8 * (C::B_DSFULL + (int)(ts_steps & 1)), (ts_steps >> 1) & 1, abort_flag,
-                   a.status))
-      return false;
-    const uint32_t buf = (ts_steps & 1) * C::TMEM_BUF;
-    ++ts_steps;
-    if (first && acc_units > 0 &&
-        !mbar_wait_long(bars + 8 * C::B_ACCFREE, (acc_units - 1) & 1, abort_flag, a.status))
-      return false;
-    tc_fence_after();
-    const int ksteps = (h.valid + 15) >> 4;
-    const uint64_t m1 = in_mn + (uint64_t)((stage * 2 * C::TILE_BYTES) >> 4) +
-                        (uint64_t)(h.hh * kHalfRows);
-    if (MODE == kDQ) {
-      ts(tmem + C::TMEM_A0, tmem + buf + C::TMEM_P, m1, ksteps, first);
-    } else {
-      ts(tmem + C::TMEM_A0, tmem + buf + C::TMEM_S, m1 + (uint64_t)(C::TILE_BYTES >> 4), ksteps,
-         first);
-      ts(tmem + C::TMEM_A1, tmem + buf + C::TMEM_P, m1, ksteps, first);
-    }
-    if (closes) tc_commit(bars + 8 * (C::B_INEMPTY + (int)stage));
-    return true;
-  };
-  auto wait_in = [&](uint32_t stage) -> bool {
-    if (!mbar_wait_long(bars + 8 * (infull + (int)stage), (g / kStages) & 1, abort_flag, a.status))
-      return false;
-    tc_fence_after();
-    return true;
-  };
   while (ok && ring_take<MODE>(ring, a, u, abort_flag, ok)) {
-    // One half step of lookahead: S/dP of step t + 1 are issued before the TS MMAs of step t.
-    HalfStep cur{0, 0, min(kHalf, in_valid<MODE>(u, 0))};
-    uint32_t stage = g % kStages;
-    ok = wait_in(stage);
-    if (!ok) break;
     ok = mbar_wait_long(bars + 8 * C::B_OUTFULL, units & 1, abort_flag, a.status);
     if (!ok) break;
     ++units;
-    tc_fence_after();
-    issue_ss(cur, stage);
-    HalfStep nxt = cur;
-    bool more = next_half<MODE>(u, nxt), first = true;
-    // The outer tiles are free once the unit's last S and dP are formed: the next unit's load then
-    // runs beside the last half step.
-    if (!more) tc_commit(bars + 8 * C::B_OUTEMPTY);
-    for (;;) {
-      uint32_t nstage = stage;
-      if (more && nxt.hh == 0) {
-        ++g;
-        nstage = g % kStages;
-        ok = wait_in(nstage);
-        if (!ok) break;
-      }
-      const bool closes = !(more && nxt.hh == 1);
-      const HalfStep ahead = nxt;
-      bool more_ahead = false;
-      if (more) {
-        issue_ss(nxt, nstage);
-        more_ahead = next_half<MODE>(u, nxt);
-        if (!more_ahead) tc_commit(bars + 8 * C::B_OUTEMPTY);
-      }
-      ok = issue_ts(cur, stage, first, closes);
+    HalfStep h{0, 0, min(kHalf, in_valid<MODE>(u, 0))};
+    for (bool more = true; more;) {
+      const uint32_t stage = g % kStages, b = steps & 1;
+      if (h.hh == 0)
+        ok = mbar_wait_long(bars + 8 * (infull + (int)stage), (g / kStages) & 1, abort_flag,
+                            a.status);
+      if (ok && steps >= 2)
+        ok = mbar_wait_long(bars + 8 * (C::B_BUFFREE + (int)b), ((steps >> 1) - 1) & 1, abort_flag,
+                            a.status);
       if (!ok) break;
-      first = false;
-      if (!more) break;
-      cur = ahead;
-      stage = nstage;
-      more = more_ahead;
+      tc_fence_after();
+      const uint32_t idesc = kIdesc0 | ((uint32_t)(((h.valid + 15) & ~15) >> 3) << 17);
+      const uint64_t i1 = in_k + (uint64_t)((stage * 2 * C::TILE_BYTES) >> 4) +
+                          (uint64_t)(h.hh * kHalfRows);
+      const uint32_t buf = tmem + b * C::TMEM_BUF;
+#pragma unroll
+      for (int kk = 0; kk < C::KSTEPS_QK; ++kk) {
+        const uint32_t off = ((kk / C::KSTEPS_PER_BLK) * C::BLK_BYTES +
+                              (kk % C::KSTEPS_PER_BLK) * 32) >> 4;
+        tc_mma(buf + C::TMEM_S, o1 + off, i1 + off, idesc, kk > 0 ? 1u : 0u);
+      }
+#pragma unroll
+      for (int kk = 0; kk < C::KSTEPS_QK; ++kk) {
+        const uint32_t off = ((kk / C::KSTEPS_PER_BLK) * C::BLK_BYTES +
+                              (kk % C::KSTEPS_PER_BLK) * 32) >> 4;
+        tc_mma(buf + C::TMEM_P, o2 + off, i1 + (uint64_t)(C::TILE_BYTES >> 4) + off, idesc,
+               kk > 0 ? 1u : 0u);
+      }
+      tc_commit(bars + 8 * (C::B_SPFULL + (int)b));
+      ++steps;
+      more = next_half<MODE>(u, h);
+      // The outer tiles are free once the unit's last S and dP are formed: the next unit's load runs
+      // beside the last half steps.
+      if (!more) tc_commit(bars + 8 * C::B_OUTEMPTY);
+      if (!more || h.hh == 0) ++g;
     }
-    if (!ok) break;
-    ++g;
-    tc_commit(bars + 8 * C::B_ACCFULL);
-    ++acc_units;
   }
   if (!ok) {
+    // Aborting: wait until every MMA this thread issued has completed.
     tc_commit(bars + 8 * C::B_DRAIN);
     mbar_wait_drain(bars + 8 * C::B_DRAIN, 0);
+  }
+}
+
+// The TS products, which add to the unit's accumulators; another thread, so that neither its waits
+// for the compute warps nor its issue hold up the next S and dP (one thread for both: 2,400 cycles
+// a half step at d = 128, of which the tensor core needs about 1,250).
+template <int D, int MODE>
+__device__ void ts_role(const BwdArgs& a, uint32_t sbase, uint32_t bars, uint32_t tmem,
+                        volatile int* abort_flag, Ring ring) {
+  using C = Cfg<D>;
+  constexpr uint32_t kIdescTS = idesc_bf16_f32(C::BM, D, false, true);
+  constexpr uint32_t kHalfRows = (kHalf * C::SW) >> 4;
+  constexpr uint32_t kStep = (16 * C::SW) >> 4;
+  const int infull = a.valid ? C::B_INREADY : C::B_INFULL;
+  const uint64_t in_mn = smem_desc(sbase + C::OFF_IN, C::BLK_BYTES, 8 * C::SW, C::LAYOUT);
+  uint32_t g = 0, steps = 0, units = 0;
+  bool ok = true;
+  Unit u;
+  // The pairs of a half step sit in two 16-column runs, one per compute warp of a lane quarter.
+  auto ts = [&](uint32_t acc, uint32_t p, uint64_t y, int ksteps, bool overwrite) {
+#pragma unroll
+    for (int kk = 0; kk < kHalf / 16; ++kk)
+      if (kk < ksteps)
+        tc_mma_ts(acc, p + (uint32_t)(kk >> 1) * 32u + (uint32_t)(kk & 1) * 8u,
+                  y + (uint64_t)(kk * kStep), kIdescTS, (overwrite && kk == 0) ? 0u : 1u);
+  };
+  while (ok && ring_take<MODE>(ring, a, u, abort_flag, ok)) {
+    HalfStep h{0, 0, min(kHalf, in_valid<MODE>(u, 0))};
+    bool first = true;
+    for (bool more = true; more;) {
+      const uint32_t stage = g % kStages, b = steps & 1;
+      // The tile has landed (S was formed from it); this thread sees that for itself.
+      if (h.hh == 0)
+        ok = mbar_wait_long(bars + 8 * (infull + (int)stage), (g / kStages) & 1, abort_flag,
+                            a.status);
+      if (ok && first && units > 0)
+        ok = mbar_wait_long(bars + 8 * C::B_ACCFREE, (units - 1) & 1, abort_flag, a.status);
+      if (ok)
+        ok = mbar_wait_long(bars + 8 * (C::B_DSFULL + (int)b), (steps >> 1) & 1, abort_flag,
+                            a.status);
+      if (!ok) break;
+      tc_fence_after();
+      const int ksteps = (h.valid + 15) >> 4;
+      const uint32_t buf = tmem + b * C::TMEM_BUF;
+      const uint64_t m1 = in_mn + (uint64_t)((stage * 2 * C::TILE_BYTES) >> 4) +
+                          (uint64_t)(h.hh * kHalfRows);
+      if (MODE == kDQ) {
+        ts(tmem + C::TMEM_A0, buf + C::TMEM_P, m1, ksteps, first);
+      } else {
+        ts(tmem + C::TMEM_A0, buf + C::TMEM_S, m1 + (uint64_t)(C::TILE_BYTES >> 4), ksteps, first);
+        ts(tmem + C::TMEM_A1, buf + C::TMEM_P, m1, ksteps, first);
+      }
+      tc_commit(bars + 8 * (C::B_BUFFREE + (int)b));
+      ++steps;
+      first = false;
+      more = next_half<MODE>(u, h);
+      if (!more || h.hh == 0) {
+        tc_commit(bars + 8 * (C::B_INEMPTY + (int)stage));
+        ++g;
+      }
+    }
+    if (!ok) break;
+    tc_commit(bars + 8 * C::B_ACCFULL);
+    ++units;
+  }
+  if (!ok) {
+    tc_commit(bars + 8 * (C::B_DRAIN + 1));
+    mbar_wait_drain(bars + 8 * (C::B_DRAIN + 1), 0);
   }
 }
 
@@ -713,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i == C::B_ACCFREE) n = kEpilogue;
       if (i >= C::B_INREADY && i < C::B_INREADY + kStages) n = 32;
       // Readers of the ring: producer and MMA threads, compute, epilogue and padding warps.
-      if (i >= C::B_RINGEMPTY) n = 2 + kCompute + kEpilogue + (a.valid ? 32 : 0);
+      if (i >= C::B_RINGEMPTY) n = 3 + kCompute + kEpilogue + (a.valid ? 32 : 0);
       mbar_init(bars + 8 * i, n);
     }
     *abort_flag = 0;
@@ -742,12 +755,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 0) {
       if (lane == 0)
         producer_role<D, MODE>(&tmO1, &tmO2, &tmI1, &tmI2, a, sbase, bars, abort_flag, ring);
+      else if (lane == 1)
+        claim_role<MODE>(a, ring, abort_flag);
     } else if (warp == 1) {
-      if (lane == 0) mma_role<D, MODE>(a, sbase, bars, tmem, abort_flag, ring);
+      if (lane == 0) ss_role<D, MODE>(a, sbase, bars, tmem, abort_flag, ring);
     } else if (warp == 2) {
-      if (a.valid) padding_role<D, MODE>(a, sbase, bars, abort_flag, lane, ring);
-    } else if (lane == 0) {
-      claim_role<MODE>(a, ring, abort_flag);
+      if (lane == 0) ts_role<D, MODE>(a, sbase, bars, tmem, abort_flag, ring);
+    } else if (a.valid) {
+      padding_role<D, MODE>(a, sbase, bars, abort_flag, lane, ring);
     }
   } else if (warp < 12) {
     set_max_regs_inc<kRegsCompute>();
