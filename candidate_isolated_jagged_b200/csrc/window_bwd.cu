@@ -19,9 +19,9 @@
 //   S = O1 I1^T,  dP = O2 I2^T  (SS MMAs)   ->   dS (and P) as bf16 in TMEM   ->   TS MMAs
 //   dQ  (O1 = Q, O2 = dO, I1 = K, I2 = V):   acc0 += dS I1
 //   dKV (O1 = K, O2 = V, I1 = Q, I2 = dO):   acc0 (dV) += P^T I2,  acc1 (dK) += dS^T I1
-// An inner tile is taken as two half steps of 64 rows, so that S and dP fit twice in TMEM and the
-// tensor core works on step t + 1 while the compute warps do step t. Columns a warp's rows do not
-// see are decided per 32 columns: none (zeros are written), all (no masking) or some.
+// A step takes 64 inner rows, so that S and dP fit two or three times beside the accumulators in TMEM
+// and the tensor core works ahead of the compute warps. Columns a warp's rows do not see are
+// decided per 32 columns: none (zeros are written), all (no masking) or some.
 //   warp 0      lane 0: TMA loads, lane 1: claims units and posts them to a ring;
 //   warps 1, 2  one thread each issues the SS and the TS MMAs;
 //   warp 3      with padding: zeroes the padding rows of the inner tiles;
@@ -54,10 +54,9 @@ constexpr int kCompute = 256;
 constexpr int kEpilogue = 128;
 // Registers a thread: 512 x 128 at launch, shared out anew (72 + 2 x 168 + 104 = 4 x 128).
 constexpr int kRegsRoles = 72, kRegsCompute = 168, kRegsEpilogue = 104;
-constexpr int kStages = 2;
-constexpr int kHalf = 64;        // inner rows of a half step
-// Query rows of a kSink unit: 256 rows keep the longest unit at 8 half steps (16 users: 14 us, with
-// 1024 rows 36 us; 256 users 153 and 164 us).
+constexpr int kStep = 64;        // inner rows of a step
+// Query rows of a kSink unit: 256 rows keep the longest unit short (16 users: 14 us, with 1024 rows
+// 36 us; 256 users 153 and 164 us).
 constexpr int kChunk = 256;
 constexpr int kRing = 4;
 constexpr int kEntry = 6;        // ints of a ring entry
@@ -85,7 +84,7 @@ struct BwdArgs {
   float scale, scale_log2;
 };
 
-template <int D>
+template <int D, int MODE>
 struct Cfg {
   static constexpr int BM = kTileM;
   static constexpr int ROW_BYTES = D * 2;
@@ -97,44 +96,50 @@ struct Cfg {
   static constexpr uint32_t LAYOUT = SW == 128 ? 2u : (SW == 64 ? 4u : 6u);
   static constexpr int KSTEPS_QK = D / 16;
   static constexpr int KSTEPS_PER_BLK = SW / 32;
-  static constexpr int OFF_OUT = 0;                                   // 2 tiles
-  static constexpr int OFF_IN = 2 * TILE_BYTES;                       // kStages x 2 tiles
-  static constexpr int OFF_BAR = OFF_IN + kStages * 2 * TILE_BYTES;
-  static constexpr int B_OUTFULL = 0;
-  static constexpr int B_OUTEMPTY = 1;
-  static constexpr int B_INFULL = 2;                                  // [kStages]
-  static constexpr int B_INREADY = B_INFULL + kStages;                // padding rows zeroed
-  static constexpr int B_INEMPTY = B_INREADY + kStages;
-  static constexpr int B_SPFULL = B_INEMPTY + kStages;                // [2] S and dP written
-  static constexpr int B_DSFULL = B_SPFULL + 2;                       // [2] dS (and P) written
-  static constexpr int B_ACCFULL = B_DSFULL + 2;
+  static constexpr int IN_BLK = kStep * SW;                           // column block of an inner tile
+  static constexpr int IN_TILE = kStep * ROW_BYTES;
+  static constexpr int IN_STAGE = 2 * IN_TILE;                        // I1, I2
+  static constexpr int STAGES = D == 128 ? 3 : 6;
+  // S and dP buffers, 128 columns each: what the accumulators leave of the 512 columns.
+  static constexpr int BUFS = (MODE == kDQ || D <= 64) ? 3 : 2;
+  static constexpr int OFF_OUT = 0;                                   // [2] O1, O2
+  static constexpr int OFF_IN = 4 * TILE_BYTES;
+  static constexpr int OFF_BAR = OFF_IN + STAGES * IN_STAGE;
+  static constexpr int B_OUTFULL = 0;                                 // [2]
+  static constexpr int B_OUTEMPTY = 2;                                // [2]
+  static constexpr int B_INFULL = 4;                                  // [STAGES]
+  static constexpr int B_INREADY = B_INFULL + STAGES;                 // padding rows zeroed
+  static constexpr int B_INEMPTY = B_INREADY + STAGES;
+  static constexpr int B_SPFULL = B_INEMPTY + STAGES;                 // [BUFS] S and dP written
+  static constexpr int B_DSFULL = B_SPFULL + BUFS;                    // [BUFS] dS (and P) written
+  static constexpr int B_BUFFREE = B_DSFULL + BUFS;                   // [BUFS] read by TS
+  static constexpr int B_ACCFULL = B_BUFFREE + BUFS;
   static constexpr int B_ACCFREE = B_ACCFULL + 1;
   static constexpr int B_COLS = B_ACCFREE + 1;                        // [2] column statistics
-  static constexpr int B_BUFFREE = B_COLS + 2;                        // [2] S and dP read by TS
-  static constexpr int B_DRAIN = B_BUFFREE + 2;                       // [2] MMA threads
+  static constexpr int B_DRAIN = B_COLS + 2;                          // [2] MMA threads
   static constexpr int B_RINGFULL = B_DRAIN + 2;
   static constexpr int B_RINGEMPTY = B_RINGFULL + kRing;
   static constexpr int NUM_BARS = B_RINGEMPTY + kRing;
   static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
   static constexpr int OFF_RING = OFF_MISC + 16;
-  static constexpr int OFF_COLS = (OFF_RING + kRing * kEntry * 4 + 15) / 16 * 16;   // [2][2][128]
-  static constexpr int SMEM_USED = OFF_COLS + 2 * 2 * BM * 4;
+  static constexpr int OFF_COLS = (OFF_RING + kRing * kEntry * 4 + 15) / 16 * 16;   // [2][2][64]
+  static constexpr int SMEM_USED = OFF_COLS + 2 * 2 * kStep * 4;
   static constexpr int SMEM_RAW = SMEM_USED + 1024;
   // At least 120 KB so that a second block never shares the SM (and its TMEM).
   static constexpr int SMEM_ALLOC = SMEM_RAW > 120 * 1024 ? SMEM_RAW : 120 * 1024;
-  static constexpr uint32_t TMEM_S = 0, TMEM_P = 64, TMEM_BUF = 128, TMEM_A0 = 256,
-                            TMEM_A1 = 384, TMEM_COLS = 512;
+  static constexpr uint32_t TMEM_S = 0, TMEM_P = 64, TMEM_BUF = 128, TMEM_A0 = BUFS * 128,
+                            TMEM_A1 = TMEM_A0 + (D < 64 ? 64 : D), TMEM_COLS = 512;
+  static_assert(TMEM_A0 + (MODE == kDQ ? 1 : 2) * D <= TMEM_COLS, "TMEM budget");
   static_assert(SMEM_ALLOC <= 227 * 1024, "shared memory budget");
 };
 
-// A unit as every role derives it from a ring entry. Inner tile i is rows [in_row(i), + in_valid(i))
-// of head in_head(i).
+// A unit as every role derives it from a ring entry: its outer tile, and the rows that its inner steps
+// walk, up to 64 at a time.
 struct Unit {
   int orow0, oh;                // outer rows and head (dQ: query head, else key head)
-  int n_in;
-  int base, n_run;              // inner tiles: n_run of 128 rows from base on, per head
-  int end;                      // dKV, kSink: inner rows stop here
-  int sink0, n_sink;            // dQ: rows of the first tokens' tile, which comes first
+  int n_in;                     // steps
+  int base, end, n_run;         // rows [base, end) in n_run steps (dKV, kSink: once per query head)
+  int sink0, n_sink, n_first;   // dQ: rows of the first tokens, which come first, in n_first steps
   int slot, uend;               // kSink: partial sum's slot, end of the user
 };
 
@@ -143,19 +148,20 @@ __device__ __forceinline__ Unit make_unit(const volatile int* e, const BwdArgs& 
   Unit u;
   u.orow0 = e[0];
   u.oh = e[1];
-  u.sink0 = u.n_sink = u.slot = u.uend = 0;
+  u.sink0 = u.n_sink = u.n_first = u.slot = u.uend = 0;
   if (MODE == kDQ) {
     const int lo = e[2], start = e[3];
-    u.base = lo & ~(kTileN - 1);
+    u.base = lo & ~(kStep - 1);
+    u.end = min(u.orow0 + kTileM, a.T);
     u.sink0 = start;
     u.n_sink = max(0, min(a.n_sinks, u.base - start));
-    u.n_run = (u.orow0 + kTileM - u.base) / kTileN;
-    u.end = a.T;
-    u.n_in = u.n_run + (u.n_sink ? 1 : 0);
+    u.n_first = (u.n_sink + kStep - 1) / kStep;
+    u.n_run = (u.end - u.base + kStep - 1) / kStep;
+    u.n_in = u.n_first + u.n_run;
   } else {
     u.base = e[2];
     u.end = e[3];
-    u.n_run = (u.end - u.base + kTileN - 1) / kTileN;
+    u.n_run = (u.end - u.base + kStep - 1) / kStep;
     u.n_in = u.n_run * a.group;
     u.slot = e[4];
     u.uend = e[5];
@@ -163,23 +169,36 @@ __device__ __forceinline__ Unit make_unit(const volatile int* e, const BwdArgs& 
   return u;
 }
 
+// A unit's steps in order: rows [row, row + valid) of head `head`.
 template <int MODE>
-__device__ __forceinline__ int in_row(const Unit& u, int i) {
-  if (MODE == kDQ) {
-    if (!u.n_sink) return u.base + i * kTileN;
-    return i == 0 ? u.sink0 : u.base + (i - 1) * kTileN;
+struct Walk {
+  int i, t, row, valid, head;
+  __device__ __forceinline__ void place(const Unit& u) {
+    if (MODE == kDQ && i < u.n_first) {
+      row = u.sink0 + i * kStep;
+      valid = min(kStep, u.n_sink - i * kStep);
+    } else {
+      row = u.base + t * kStep;
+      valid = min(kStep, u.end - row);
+    }
   }
-  return u.base + (i % u.n_run) * kTileN;
-}
-template <int MODE>
-__device__ __forceinline__ int in_head(const Unit& u, int i, const BwdArgs& a) {
-  return MODE == kDQ ? u.oh / a.group : u.oh * a.group + i / u.n_run;
-}
-template <int MODE>
-__device__ __forceinline__ int in_valid(const Unit& u, int i) {
-  if (MODE == kDQ && u.n_sink && i == 0) return u.n_sink;
-  return min(kTileN, u.end - in_row<MODE>(u, i));
-}
+  __device__ __forceinline__ void begin(const Unit& u, const BwdArgs& a) {
+    i = t = 0;
+    head = MODE == kDQ ? u.oh / a.group : u.oh * a.group;
+    place(u);
+  }
+  // The next step; false behind the last.
+  __device__ __forceinline__ bool next(const Unit& u) {
+    if (MODE != kDQ || i >= u.n_first) ++t;
+    ++i;
+    if (MODE != kDQ && t == u.n_run) {
+      t = 0;
+      ++head;
+    }
+    place(u);
+    return i < u.n_in;
+  }
+};
 
 struct Ring {
   volatile int* slot;
@@ -212,7 +231,7 @@ __device__ void claim_role(const BwdArgs& a, Ring r, volatile int* abort_flag) {
       if (MODE == kSink) {
         const int4 x = a.sinks[v / heads];   // {first row, end, chunk, slot}
         e[0] = x.x;
-        e[2] = max(x.x + a.window, x.z * kChunk) & ~(kTileN - 1);
+        e[2] = max(x.x + a.window, x.z * kChunk) & ~(kStep - 1);
         e[3] = (int)min((long long)x.y, (long long)(x.z + 1) * kChunk);
         e[4] = x.w;
         e[5] = x.y;
@@ -244,46 +263,50 @@ template <int D, int MODE>
 __device__ void producer_role(const CUtensorMap* tmO1, const CUtensorMap* tmO2,
                               const CUtensorMap* tmI1, const CUtensorMap* tmI2, const BwdArgs& a,
                               uint32_t sbase, uint32_t bars, volatile int* abort_flag, Ring ring) {
-  using C = Cfg<D>;
+  using C = Cfg<D, MODE>;
   uint32_t units = 0, g = 0;
   bool ok = true;
   Unit u;
+  Walk<MODE> w;
   while (ok && ring_take<MODE>(ring, a, u, abort_flag, ok)) {
-    for (int i = 0; i < u.n_in; ++i) {
-      const int s = (int)(g % kStages);
-      ok = mbar_wait(bars + 8 * (C::B_INEMPTY + s), ((g / kStages) & 1) ^ 1, abort_flag, a.status);
+    // The outer tiles have two slots, so a unit's arrive while the one before is worked on.
+    const int slot = (int)(units & 1);
+    ok = mbar_wait(bars + 8 * (C::B_OUTEMPTY + slot), ((units >> 1) & 1) ^ 1, abort_flag, a.status);
+    if (!ok) break;
+    const uint32_t obar = bars + 8 * (C::B_OUTFULL + slot);
+    mbar_arrive_expect_tx(obar, 2 * C::TILE_BYTES);
+    ++units;
+    const uint32_t out = sbase + C::OFF_OUT + slot * 2 * C::TILE_BYTES;
+#pragma unroll
+    for (int c = 0; c < C::NBLK; ++c)
+#pragma unroll
+      for (int x = 0; x < kTileM / kStep; ++x) {
+        const uint32_t at = out + c * C::BLK_BYTES + x * C::IN_BLK;
+        tma_load_3d(at, tmO1, obar, c * C::BOX_X, u.oh, u.orow0 + x * kStep);
+        tma_load_3d(at + C::TILE_BYTES, tmO2, obar, c * C::BOX_X, u.oh, u.orow0 + x * kStep);
+      }
+    w.begin(u, a);
+    for (bool more = true; more; more = w.next(u)) {
+      const int s = (int)(g % C::STAGES);
+      ok = mbar_wait(bars + 8 * (C::B_INEMPTY + s), ((g / C::STAGES) & 1) ^ 1, abort_flag, a.status);
       if (!ok) break;
-      mbar_arrive_expect_tx(bars + 8 * (C::B_INFULL + s), 2 * C::TILE_BYTES);
-      const uint32_t dst = sbase + C::OFF_IN + s * 2 * C::TILE_BYTES;
-      const int row = in_row<MODE>(u, i), h = in_head<MODE>(u, i, a);
+      const uint32_t ibar = bars + 8 * (C::B_INFULL + s);
+      mbar_arrive_expect_tx(ibar, C::IN_STAGE);
+      const uint32_t dst = sbase + C::OFF_IN + s * C::IN_STAGE;
 #pragma unroll
       for (int c = 0; c < C::NBLK; ++c) {
-        tma_load_3d(dst + c * C::BLK_BYTES, tmI1, bars + 8 * (C::B_INFULL + s), c * C::BOX_X, h,
-                    row);
-        tma_load_3d(dst + C::TILE_BYTES + c * C::BLK_BYTES, tmI2, bars + 8 * (C::B_INFULL + s),
-                    c * C::BOX_X, h, row);
+        tma_load_3d(dst + c * C::IN_BLK, tmI1, ibar, c * C::BOX_X, w.head, w.row);
+        tma_load_3d(dst + C::IN_TILE + c * C::IN_BLK, tmI2, ibar, c * C::BOX_X, w.head, w.row);
       }
       ++g;
-      if (i > 0) continue;
-      // The outer tiles go out behind the unit's first inner tiles, whose stage was freed earlier.
-      ok = mbar_wait(bars + 8 * C::B_OUTEMPTY, (units & 1) ^ 1, abort_flag, a.status);
-      if (!ok) break;
-      mbar_arrive_expect_tx(bars + 8 * C::B_OUTFULL, 2 * C::TILE_BYTES);
-      ++units;
-#pragma unroll
-      for (int c = 0; c < C::NBLK; ++c) {
-        tma_load_3d(sbase + C::OFF_OUT + c * C::BLK_BYTES, tmO1, bars + 8 * C::B_OUTFULL,
-                    c * C::BOX_X, u.oh, u.orow0);
-        tma_load_3d(sbase + C::OFF_OUT + C::TILE_BYTES + c * C::BLK_BYTES, tmO2,
-                    bars + 8 * C::B_OUTFULL, c * C::BOX_X, u.oh, u.orow0);
-      }
     }
   }
   if (!ok) {
     // Aborting: let the copies this thread started land before the block exits.
-    if (units > 0) mbar_wait_drain(bars + 8 * C::B_OUTFULL, (units - 1) & 1);
-    for (uint32_t n = g > (uint32_t)kStages ? g - kStages : 0; n < g; ++n)
-      mbar_wait_drain(bars + 8 * (C::B_INFULL + (int)(n % kStages)), (n / kStages) & 1);
+    for (uint32_t n = units > 2 ? units - 2 : 0; n < units; ++n)
+      mbar_wait_drain(bars + 8 * (C::B_OUTFULL + (int)(n & 1)), (n >> 1) & 1);
+    for (uint32_t n = g > (uint32_t)C::STAGES ? g - C::STAGES : 0; n < g; ++n)
+      mbar_wait_drain(bars + 8 * (C::B_INFULL + (int)(n % C::STAGES)), (n / C::STAGES) & 1);
   }
 }
 
@@ -291,36 +314,38 @@ __device__ void producer_role(const CUtensorMap* tmO1, const CUtensorMap* tmO2,
 template <int D, int MODE>
 __device__ void padding_role(const BwdArgs& a, uint32_t sbase, uint32_t bars,
                              volatile int* abort_flag, int lane, Ring ring) {
-  using C = Cfg<D>;
+  using C = Cfg<D, MODE>;
   constexpr int CH = C::ROW_BYTES / 16, CB = C::SW / 16;
   uint32_t g = 0;
   bool ok = true;
   Unit u;
+  Walk<MODE> w;
   for (;;) {
-    const bool more = ring_take<MODE>(ring, a, u, abort_flag, ok);
-    if (!__all_sync(0xffffffffu, more)) return;
-    for (int i = 0; i < u.n_in; ++i, ++g) {
-      const int s = (int)(g % kStages), row = in_row<MODE>(u, i);
-      uint32_t pad[4];
+    const bool taken = ring_take<MODE>(ring, a, u, abort_flag, ok);
+    if (!__all_sync(0xffffffffu, taken)) return;
+    w.begin(u, a);
+    for (bool more = true; more; more = w.next(u), ++g) {
+      const int s = (int)(g % C::STAGES);
+      uint32_t pad[2];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int k = row + 32 * c + lane;
+      for (int c = 0; c < 2; ++c) {
+        const int k = w.row + 32 * c + lane;
         pad[c] = __ballot_sync(0xffffffffu, k < a.T && !a.valid[k]);
       }
-      ok = mbar_wait_long(bars + 8 * (C::B_INFULL + s), (g / kStages) & 1, abort_flag, a.status);
+      ok = mbar_wait_long(bars + 8 * (C::B_INFULL + s), (g / C::STAGES) & 1, abort_flag, a.status);
       if (!__all_sync(0xffffffffu, ok)) return;
-      const uint32_t tile = sbase + C::OFF_IN + s * 2 * C::TILE_BYTES;
+      const uint32_t tile = sbase + C::OFF_IN + s * C::IN_STAGE;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
         if (!pad[c]) continue;
         // A row's bytes of a column block are contiguous; the swizzle only reorders them.
+#pragma unroll 1
         for (int y = lane; y < 32 * CH; y += 32) {
           const int r = y / CH, x = y % CH;
           if (!((pad[c] >> r) & 1)) continue;
-          const uint32_t at =
-              tile + (x / CB) * C::BLK_BYTES + (32 * c + r) * C::SW + (x % CB) * 16;
+          const uint32_t at = tile + (x / CB) * C::IN_BLK + (32 * c + r) * C::SW + (x % CB) * 16;
           st_shared_v4(at, 0u, 0u, 0u, 0u);
-          st_shared_v4(at + C::TILE_BYTES, 0u, 0u, 0u, 0u);
+          st_shared_v4(at + C::IN_TILE, 0u, 0u, 0u, 0u);
         }
       }
       fence_proxy_async_smem();
@@ -329,79 +354,53 @@ __device__ void padding_role(const BwdArgs& a, uint32_t sbase, uint32_t bars,
   }
 }
 
-// Half steps of a unit; the second half of an inner tile exists when it has more than 64 rows.
-struct HalfStep {
-  int i, hh, valid;
-};
-
-template <int MODE>
-__device__ __forceinline__ bool next_half(const Unit& u, HalfStep& h) {
-  if (h.hh == 0 && in_valid<MODE>(u, h.i) > kHalf) {
-    h.hh = 1;
-  } else {
-    if (h.i + 1 >= u.n_in) return false;
-    ++h.i;
-    h.hh = 0;
-  }
-  h.valid = min(kHalf, in_valid<MODE>(u, h.i) - h.hh * kHalf);
-  return true;
-}
-
-// The S and dP products of every half step, one thread. A buffer is formed anew once the TS products of
-// two half steps before have read it.
+// The S and dP products of every step, one thread. A buffer is formed anew once the TS products that
+// read it last are done.
 template <int D, int MODE>
 __device__ void ss_role(const BwdArgs& a, uint32_t sbase, uint32_t bars, uint32_t tmem,
                         volatile int* abort_flag, Ring ring) {
-  using C = Cfg<D>;
-  constexpr uint32_t kIdescSS = idesc_bf16_f32(C::BM, kHalf, false, false);
+  using C = Cfg<D, MODE>;
+  constexpr uint32_t kIdescSS = idesc_bf16_f32(C::BM, kStep, false, false);
   constexpr uint32_t kIdesc0 = kIdescSS & ~(0x3Fu << 17);
-  constexpr uint32_t kHalfRows = (kHalf * C::SW) >> 4;
   const int infull = a.valid ? C::B_INREADY : C::B_INFULL;
-  const uint64_t o1 = smem_desc(sbase + C::OFF_OUT, 16, 8 * C::SW, C::LAYOUT);
-  const uint64_t o2 = o1 + (uint64_t)(C::TILE_BYTES >> 4);
-  const uint64_t in_k = smem_desc(sbase + C::OFF_IN, 16, 8 * C::SW, C::LAYOUT);
-  uint32_t units = 0, g = 0, steps = 0;
+  const uint64_t out = smem_desc(sbase + C::OFF_OUT, 16, 8 * C::SW, C::LAYOUT);
+  const uint64_t in = smem_desc(sbase + C::OFF_IN, 16, 8 * C::SW, C::LAYOUT);
+  uint32_t units = 0, g = 0;
   bool ok = true;
   Unit u;
+  Walk<MODE> w;
   while (ok && ring_take<MODE>(ring, a, u, abort_flag, ok)) {
-    ok = mbar_wait_long(bars + 8 * C::B_OUTFULL, units & 1, abort_flag, a.status);
+    const int slot = (int)(units & 1);
+    ok = mbar_wait_long(bars + 8 * (C::B_OUTFULL + slot), (units >> 1) & 1, abort_flag, a.status);
     if (!ok) break;
     ++units;
-    HalfStep h{0, 0, min(kHalf, in_valid<MODE>(u, 0))};
-    for (bool more = true; more;) {
-      const uint32_t stage = g % kStages, b = steps & 1;
-      if (h.hh == 0)
-        ok = mbar_wait_long(bars + 8 * (infull + (int)stage), (g / kStages) & 1, abort_flag,
-                            a.status);
-      if (ok && steps >= 2)
-        ok = mbar_wait_long(bars + 8 * (C::B_BUFFREE + (int)b), ((steps >> 1) - 1) & 1, abort_flag,
+    const uint64_t o1 = out + (uint64_t)((slot * 2 * C::TILE_BYTES) >> 4);
+    w.begin(u, a);
+    for (bool more = true; more; ++g) {
+      const int s = (int)(g % C::STAGES), b = (int)(g % C::BUFS);
+      ok = mbar_wait_long(bars + 8 * (infull + s), (g / C::STAGES) & 1, abort_flag, a.status);
+      if (ok && g >= (uint32_t)C::BUFS)
+        ok = mbar_wait_long(bars + 8 * (C::B_BUFFREE + b), (g / C::BUFS - 1) & 1, abort_flag,
                             a.status);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t idesc = kIdesc0 | ((uint32_t)(((h.valid + 15) & ~15) >> 3) << 17);
-      const uint64_t i1 = in_k + (uint64_t)((stage * 2 * C::TILE_BYTES) >> 4) +
-                          (uint64_t)(h.hh * kHalfRows);
+      const uint32_t idesc = kIdesc0 | ((uint32_t)(((w.valid + 15) & ~15) >> 3) << 17);
+      const uint64_t i1 = in + (uint64_t)((s * C::IN_STAGE) >> 4);
       const uint32_t buf = tmem + b * C::TMEM_BUF;
 #pragma unroll
-      for (int kk = 0; kk < C::KSTEPS_QK; ++kk) {
-        const uint32_t off = ((kk / C::KSTEPS_PER_BLK) * C::BLK_BYTES +
-                              (kk % C::KSTEPS_PER_BLK) * 32) >> 4;
-        tc_mma(buf + C::TMEM_S, o1 + off, i1 + off, idesc, kk > 0 ? 1u : 0u);
-      }
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int kk = 0; kk < C::KSTEPS_QK; ++kk) {
-        const uint32_t off = ((kk / C::KSTEPS_PER_BLK) * C::BLK_BYTES +
-                              (kk % C::KSTEPS_PER_BLK) * 32) >> 4;
-        tc_mma(buf + C::TMEM_P, o2 + off, i1 + (uint64_t)(C::TILE_BYTES >> 4) + off, idesc,
-               kk > 0 ? 1u : 0u);
-      }
-      tc_commit(bars + 8 * (C::B_SPFULL + (int)b));
-      ++steps;
-      more = next_half<MODE>(u, h);
-      // The outer tiles are free once the unit's last S and dP are formed: the next unit's load runs
-      // beside the last half steps.
-      if (!more) tc_commit(bars + 8 * C::B_OUTEMPTY);
-      if (!more || h.hh == 0) ++g;
+        for (int kk = 0; kk < C::KSTEPS_QK; ++kk) {
+          constexpr int PB = C::KSTEPS_PER_BLK;
+          const uint32_t k32 = (kk % PB) * 32;
+          tc_mma(buf + (x ? C::TMEM_P : C::TMEM_S),
+                 o1 + (uint32_t)((x * C::TILE_BYTES + kk / PB * C::BLK_BYTES + k32) >> 4),
+                 i1 + (uint32_t)((x * C::IN_TILE + kk / PB * C::IN_BLK + k32) >> 4), idesc,
+                 kk > 0 ? 1u : 0u);
+        }
+      tc_commit(bars + 8 * (C::B_SPFULL + b));
+      more = w.next(u);
+      if (!more) tc_commit(bars + 8 * (C::B_OUTEMPTY + slot));
     }
   }
   if (!ok) {
@@ -413,61 +412,50 @@ __device__ void ss_role(const BwdArgs& a, uint32_t sbase, uint32_t bars, uint32_
 
 // The TS products, which add to the unit's accumulators; another thread, so that neither its waits
 // for the compute warps nor its issue hold up the next S and dP (one thread for both: 2,400 cycles
-// a half step at d = 128, of which the tensor core needs about 1,250).
+// a step at d = 128, of which the tensor core needs about 1,250).
 template <int D, int MODE>
 __device__ void ts_role(const BwdArgs& a, uint32_t sbase, uint32_t bars, uint32_t tmem,
                         volatile int* abort_flag, Ring ring) {
-  using C = Cfg<D>;
+  using C = Cfg<D, MODE>;
   constexpr uint32_t kIdescTS = idesc_bf16_f32(C::BM, D, false, true);
-  constexpr uint32_t kHalfRows = (kHalf * C::SW) >> 4;
-  constexpr uint32_t kStep = (16 * C::SW) >> 4;
+  constexpr uint32_t kRows16 = (16 * C::SW) >> 4;
   const int infull = a.valid ? C::B_INREADY : C::B_INFULL;
-  const uint64_t in_mn = smem_desc(sbase + C::OFF_IN, C::BLK_BYTES, 8 * C::SW, C::LAYOUT);
-  uint32_t g = 0, steps = 0, units = 0;
+  const uint64_t in = smem_desc(sbase + C::OFF_IN, C::IN_BLK, 8 * C::SW, C::LAYOUT);
+  uint32_t g = 0, units = 0;
   bool ok = true;
   Unit u;
-  // The pairs of a half step sit in two 16-column runs, one per compute warp of a lane quarter.
+  Walk<MODE> w;
+  // The pairs of a step sit in two 16-column runs, one per compute warp of a lane quarter.
   auto ts = [&](uint32_t acc, uint32_t p, uint64_t y, int ksteps, bool overwrite) {
 #pragma unroll
-    for (int kk = 0; kk < kHalf / 16; ++kk)
+    for (int kk = 0; kk < kStep / 16; ++kk)
       if (kk < ksteps)
         tc_mma_ts(acc, p + (uint32_t)(kk >> 1) * 32u + (uint32_t)(kk & 1) * 8u,
-                  y + (uint64_t)(kk * kStep), kIdescTS, (overwrite && kk == 0) ? 0u : 1u);
+                  y + (uint64_t)(kk * kRows16), kIdescTS, (overwrite && kk == 0) ? 0u : 1u);
   };
   while (ok && ring_take<MODE>(ring, a, u, abort_flag, ok)) {
-    HalfStep h{0, 0, min(kHalf, in_valid<MODE>(u, 0))};
-    bool first = true;
-    for (bool more = true; more;) {
-      const uint32_t stage = g % kStages, b = steps & 1;
+    w.begin(u, a);
+    for (bool more = true, first = true; more; ++g, first = false, more = w.next(u)) {
+      const int s = (int)(g % C::STAGES), b = (int)(g % C::BUFS);
       // The tile has landed (S was formed from it); this thread sees that for itself.
-      if (h.hh == 0)
-        ok = mbar_wait_long(bars + 8 * (infull + (int)stage), (g / kStages) & 1, abort_flag,
-                            a.status);
+      ok = mbar_wait_long(bars + 8 * (infull + s), (g / C::STAGES) & 1, abort_flag, a.status);
       if (ok && first && units > 0)
         ok = mbar_wait_long(bars + 8 * C::B_ACCFREE, (units - 1) & 1, abort_flag, a.status);
       if (ok)
-        ok = mbar_wait_long(bars + 8 * (C::B_DSFULL + (int)b), (steps >> 1) & 1, abort_flag,
-                            a.status);
+        ok = mbar_wait_long(bars + 8 * (C::B_DSFULL + b), (g / C::BUFS) & 1, abort_flag, a.status);
       if (!ok) break;
       tc_fence_after();
-      const int ksteps = (h.valid + 15) >> 4;
+      const int ksteps = (w.valid + 15) >> 4;
       const uint32_t buf = tmem + b * C::TMEM_BUF;
-      const uint64_t m1 = in_mn + (uint64_t)((stage * 2 * C::TILE_BYTES) >> 4) +
-                          (uint64_t)(h.hh * kHalfRows);
+      const uint64_t i1 = in + (uint64_t)((s * C::IN_STAGE) >> 4);
       if (MODE == kDQ) {
-        ts(tmem + C::TMEM_A0, buf + C::TMEM_P, m1, ksteps, first);
+        ts(tmem + C::TMEM_A0, buf + C::TMEM_P, i1, ksteps, first);
       } else {
-        ts(tmem + C::TMEM_A0, buf + C::TMEM_S, m1 + (uint64_t)(C::TILE_BYTES >> 4), ksteps, first);
-        ts(tmem + C::TMEM_A1, buf + C::TMEM_P, m1, ksteps, first);
+        ts(tmem + C::TMEM_A0, buf + C::TMEM_S, i1 + (uint64_t)(C::IN_TILE >> 4), ksteps, first);
+        ts(tmem + C::TMEM_A1, buf + C::TMEM_P, i1, ksteps, first);
       }
-      tc_commit(bars + 8 * (C::B_BUFFREE + (int)b));
-      ++steps;
-      first = false;
-      more = next_half<MODE>(u, h);
-      if (!more || h.hh == 0) {
-        tc_commit(bars + 8 * (C::B_INEMPTY + (int)stage));
-        ++g;
-      }
+      tc_commit(bars + 8 * (C::B_BUFFREE + b));
+      tc_commit(bars + 8 * (C::B_INEMPTY + s));
     }
     if (!ok) break;
     tc_commit(bars + 8 * C::B_ACCFULL);
@@ -490,17 +478,19 @@ __device__ __forceinline__ uint32_t range_bits(int a, int b) {
 template <int D, int MODE>
 __device__ void compute_role(const BwdArgs& a, uint32_t bars, uint32_t tmem, float* cols,
                              volatile int* abort_flag, int warp, int lane, Ring ring) {
-  using C = Cfg<D>;
+  using C = Cfg<D, MODE>;
   const int quarter = warp & 3;
-  const int ch = (warp - 4) >> 2;               // 32-column half of every half step
+  const int ch = (warp - 4) >> 2;               // 32-column half of every step
+  const int tid = (warp - 4) * 32 + lane;
   const int r = quarter * 32 + lane;            // outer row of this thread inside its tile
   const uint32_t t_lane = tmem + ((uint32_t)(quarter * 32) << 16);
   const uint32_t t_s = t_lane + C::TMEM_S + 32 * ch, t_p = t_lane + C::TMEM_P + 32 * ch;
   const float2 sl2v = make_float2(a.scale_log2, a.scale_log2);
   const size_t T = (size_t)a.T;
-  uint32_t sp_seen = 0, cols_n = 0;
+  uint32_t g = 0;                               // steps so far
   bool ok = true;
   Unit u;
+  Walk<MODE> w;
   for (;;) {
     const bool more = ring_take<MODE>(ring, a, u, abort_flag, ok);
     if (!__all_sync(0xffffffffu, more)) break;
@@ -524,37 +514,36 @@ __device__ void compute_role(const BwdArgs& a, uint32_t bars, uint32_t tmem, flo
       }
     }
     // dQ: this row's statistics.
-    const size_t stat = (size_t)u.oh * T + (size_t)row;
-    const float lse2 = (MODE == kDQ && row_ok) ? a.lse2[stat] : INFINITY;
-    const float dsum = (MODE == kDQ && row_ok) ? a.dsum[stat] : 0.f;
+    const size_t own = (size_t)u.oh * T + (size_t)row;
+    const float lse2 = (MODE == kDQ && row_ok) ? a.lse2[own] : INFINITY;
+    const float dsum = (MODE == kDQ && row_ok) ? a.dsum[own] : 0.f;
     const float2 nlv = make_float2(-lse2, -lse2), ndv = make_float2(-dsum, -dsum);
-    // dKV: column statistics of the query tiles, negated in shared memory (warps of column half 0
-    // fill -lse2, half 1 -D); the next tile's are fetched while this one is computed.
-    auto col_stat = [&](int i) -> float {
-      const int q = in_row<MODE>(u, i) + r;
-      if (q >= a.T) return ch == 0 ? -INFINITY : 0.f;
-      const size_t at = (size_t)in_head<MODE>(u, i, a) * T + (size_t)q;
-      return ch == 0 ? -a.lse2[at] : -a.dsum[at];
+    // dKV: column statistics of a step's query rows, negated in shared memory (-lse2 of the 64 rows,
+    // then -D), one value from each of 128 threads; the next step's are fetched while this one is
+    // computed.
+    auto col_stat = [&](const Walk<MODE>& x) -> float {
+      const int q = x.row + (tid & 63);
+      if (tid >= 2 * kStep || q >= a.T) return tid < kStep ? -INFINITY : 0.f;
+      const size_t at = (size_t)x.head * T + (size_t)q;
+      return tid < kStep ? -a.lse2[at] : -a.dsum[at];
     };
-    float next_stat = MODE != kDQ ? col_stat(0) : 0.f;
-    for (int i = 0; i < u.n_in; ++i) {
-      const int valid = in_valid<MODE>(u, i), irow = in_row<MODE>(u, i);
-      float* cl = cols + (cols_n & 1) * 2 * kTileN;
+    w.begin(u, a);
+    float stat = MODE != kDQ ? col_stat(w) : 0.f;
+    for (bool more = true; more; ++g) {
+      const int b = (int)(g % C::BUFS), c0 = w.row + 32 * ch;
+      const int cvalid = w.valid - 32 * ch;     // of this warp's columns
+      const float* cl = cols + (g & 1) * 2 * kStep;
+      more = w.next(u);
       if (MODE != kDQ) {
-        cl[ch * kTileN + r] = next_stat;
-        mbar_arrive(bars + 8 * (C::B_COLS + (cols_n & 1)));
-        if (i + 1 < u.n_in) next_stat = col_stat(i + 1);
-        ok = __all_sync(0xffffffffu, mbar_wait_long(bars + 8 * (C::B_COLS + (cols_n & 1)),
-                                               (cols_n >> 1) & 1, abort_flag, a.status));
-        ++cols_n;
+        if (tid < 2 * kStep) cols[(g & 1) * 2 * kStep + tid] = stat;
+        mbar_arrive(bars + 8 * (C::B_COLS + (int)(g & 1)));
+        if (more) stat = col_stat(w);
+        ok = __all_sync(0xffffffffu, mbar_wait_long(bars + 8 * (C::B_COLS + (int)(g & 1)),
+                                                    (g >> 1) & 1, abort_flag, a.status));
         if (!ok) break;
       }
-      for (int hh = 0; hh < 2; ++hh) {
-        const int cvalid = min(kHalf, valid - hh * kHalf) - 32 * ch;   // of this warp's columns
-        if (valid - hh * kHalf <= 0) break;
-        const int b = (int)(sp_seen & 1);
+      {
         // Which of the warp's 32 columns each row pairs with.
-        const int c0 = irow + hh * kHalf + 32 * ch;
         uint32_t bits = range_bits(lo - c0, hi - c0);
         if (MODE == kDQ) bits |= range_bits(start - c0, first - c0);
         if (cvalid < 32) bits &= range_bits(0, cvalid);
@@ -564,10 +553,9 @@ __device__ void compute_role(const BwdArgs& a, uint32_t bars, uint32_t tmem, flo
         }
         const bool any = __any_sync(0xffffffffu, bits != 0u);
         const bool all = __all_sync(0xffffffffu, bits == 0xffffffffu);
-        ok = __all_sync(0xffffffffu, mbar_wait_long(bars + 8 * (C::B_SPFULL + b), (sp_seen >> 1) & 1,
-                                               abort_flag, a.status));
+        ok = __all_sync(0xffffffffu, mbar_wait_long(bars + 8 * (C::B_SPFULL + b), (g / C::BUFS) & 1,
+                                                    abort_flag, a.status));
         if (!ok) break;
-        ++sp_seen;
         tc_fence_after();
         const uint32_t buf = b * C::TMEM_BUF;
         // The bf16 pairs go to the first 16 columns of the warp's own chunk of S (P) and dP (dS).
@@ -589,13 +577,13 @@ __device__ void compute_role(const BwdArgs& a, uint32_t bars, uint32_t tmem, flo
               dp[j] = ((bits >> j) & 1u) ? dp[j] : 0u;
             }
           }
-          const float* cln = cl + hh * kHalf + 32 * ch;
+          const float* cln = cl + 32 * ch;
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
             float2 nl = nlv, nd = ndv;
             if (MODE != kDQ) {
               nl = *reinterpret_cast<const float2*>(cln + j);
-              nd = *reinterpret_cast<const float2*>(cln + kTileN + j);
+              nd = *reinterpret_cast<const float2*>(cln + kStep + j);
             }
             const float2 x = __ffma2_rn(make_float2(__uint_as_float(sv[j]),
                                                     __uint_as_float(sv[j + 1])), sl2v, nl);
@@ -617,7 +605,6 @@ __device__ void compute_role(const BwdArgs& a, uint32_t bars, uint32_t tmem, flo
         tc_fence_before();
         mbar_arrive(bars + 8 * (C::B_DSFULL + b));
       }
-      if (!ok) break;
     }
     if (!ok) break;
   }
@@ -627,7 +614,7 @@ __device__ void compute_role(const BwdArgs& a, uint32_t bars, uint32_t tmem, flo
 template <int D, int MODE>
 __device__ void epilogue_role(const BwdArgs& a, uint32_t bars, uint32_t tmem,
                               volatile int* abort_flag, int warp, int lane, Ring ring) {
-  using C = Cfg<D>;
+  using C = Cfg<D, MODE>;
   constexpr int CW = 16;
   const int r = (warp & 3) * 32 + lane;
   const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
@@ -707,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap tmO2,
                       const __grid_constant__ CUtensorMap tmI1,
                       const __grid_constant__ CUtensorMap tmI2, const BwdArgs a) {
-  using C = Cfg<D>;
+  using C = Cfg<D, MODE>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
@@ -721,10 +708,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     *skip = *a.status != 0;   // an error recorded earlier makes the launch a no-op
     for (int i = 0; i < C::NUM_BARS; ++i) {
       uint32_t n = 1;
-      if (i == C::B_DSFULL || i == C::B_DSFULL + 1 || i == C::B_COLS || i == C::B_COLS + 1)
-        n = kCompute;
+      if (i >= C::B_DSFULL && i < C::B_DSFULL + C::BUFS) n = kCompute;
+      if (i >= C::B_COLS && i < C::B_COLS + 2) n = kCompute;
       if (i == C::B_ACCFREE) n = kEpilogue;
-      if (i >= C::B_INREADY && i < C::B_INREADY + kStages) n = 32;
+      if (i >= C::B_INREADY && i < C::B_INREADY + C::STAGES) n = 32;
       // Readers of the ring: producer and MMA threads, compute, epilogue and padding warps.
       if (i >= C::B_RINGEMPTY) n = 3 + kCompute + kEpilogue + (a.valid ? 32 : 0);
       mbar_init(bars + 8 * i, n);
@@ -900,7 +887,7 @@ struct Maps {
 template <int D, int MODE>
 int launch_pass(BwdArgs a, const Maps& m, int counter, int units, int dev, int sms,
                 cudaStream_t st) {
-  using C = Cfg<D>;
+  using C = Cfg<D, MODE>;
   static std::atomic<bool> set[64];
   if (!set[dev].load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(window_bwd_kernel<D, MODE>,
@@ -926,10 +913,10 @@ int launch_bwd(const BwdArgs& a, const void* q, const void* k, const void* v, co
                int4* sink_users, int32_t* n_sinks, int64_t slots, int dev, int sms,
                cudaStream_t st) {
   Maps m;
-  if (!make_strided_map_bf16(&m.q, q, a.T, a.H, D, qs, kTileM) ||
-      !make_strided_map_bf16(&m.k, k, a.T, a.Hkv, D, ks, kTileM) ||
-      !make_strided_map_bf16(&m.v, v, a.T, a.Hkv, D, vs, kTileM) ||
-      !make_rows_map_bf16(&m.dout, dout, a.T, a.H, D, kTileM))
+  if (!make_strided_map_bf16(&m.q, q, a.T, a.H, D, qs, kStep) ||
+      !make_strided_map_bf16(&m.k, k, a.T, a.Hkv, D, ks, kStep) ||
+      !make_strided_map_bf16(&m.v, v, a.T, a.Hkv, D, vs, kStep) ||
+      !make_rows_map_bf16(&m.dout, dout, a.T, a.H, D, kStep))
     return JCA_ERR_CUDA;
   const int64_t want = ((int64_t)a.T * a.H * (D / 8) + 255) / 256;
   const int grid = (int)(want < (int64_t)sms * 16 ? want : (int64_t)sms * 16);
