@@ -47,6 +47,7 @@ constexpr int kThr = 128;          // threads of a block
 constexpr int kBK = 64;            // keys of a tile
 constexpr int kMaxSplit = 8;       // blocks of a cluster
 constexpr int kTreeWords = kMaxTree / 32;
+constexpr int kGroup = 256;        // users that are put in order together
 
 struct CacheArgs {
   const bf16* q;
@@ -62,6 +63,7 @@ struct CacheArgs {
   int32_t* status;
   int64_t B, N, R, window, n_sinks, q_stride, k_stride, v_stride;
   int H, Hkv, max_cand, row_blocks, split;
+  int longest_first;        // tree: users in the order of longest_first()
   float scale_log2;
 };
 
@@ -141,6 +143,80 @@ struct Keys {
   int own_tile;       // tree: first tile of own rows
 };
 
+// The user that takes place b when the users of each group of 256 go by the length of their history,
+// longest first. Blocks start in the order of their index, so a long history that starts late runs
+// on alone after the others (256 users with trees of 64 tokens: 222 us in the order of the batch).
+// A sort by quarter octaves is close enough and cheap: counts, a scan, the bucket that holds the
+// place, the place's bit among its members. It depends on the lengths only, so all blocks agree
+// whatever the lengths hold. `w`: 128 + 16 words of shared memory.
+template <typename IdxT>
+__device__ int64_t longest_first(const CacheArgs& a, int64_t b, uint32_t* w) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t g0 = b - b % kGroup;
+  const IdxT* ho = static_cast<const IdxT*>(a.hist_off);
+  const IdxT* len = static_cast<const IdxT*>(a.len);
+  int bucket[kGroup / kThr];
+  w[tid] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kGroup / kThr; ++i) {
+    const int64_t u = g0 + i * kThr + tid;
+    bucket[i] = -1;
+    if (u < a.B) {
+      const int64_t n = len ? (int64_t)len[u] : (int64_t)ho[u + 1] - (int64_t)ho[u];
+      const uint32_t x = (uint32_t)max((int64_t)4, min(n, (int64_t)INT_MAX));
+      const int e = 31 - __clz(x);
+      bucket[i] = 127 - (4 * e + (int)((x >> (e - 2)) & 3));
+      atomicAdd(&w[bucket[i]], 1u);
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t c[4], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum += c[i] = w[4 * lane + i];
+    uint32_t at = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, at, d);
+      if (lane >= d) at += y;
+    }
+    at -= sum;
+    const uint32_t place = (uint32_t)(b - g0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (place >= at && place < at + c[i]) {
+        w[128] = 4 * lane + i;
+        w[129] = place - at;
+      }
+      at += c[i];
+    }
+  }
+  __syncthreads();
+  const int want = (int)w[128];
+  int k = (int)w[129];
+#pragma unroll
+  for (int i = 0; i < kGroup / kThr; ++i) {
+    const uint32_t m = __ballot_sync(0xffffffffu, bucket[i] == want);
+    if (lane == 0) w[130 + i * (kThr / 32) + warp] = m;
+  }
+  __syncthreads();
+  int64_t user = g0;
+  bool found = false;
+#pragma unroll
+  for (int i = 0; i < kGroup / 32; ++i) {
+    const uint32_t m = w[130 + i];
+    const int c = __popc(m);
+    if (!found && k < c) {
+      user = g0 + i * 32 + __fns(m, 0, k + 1);
+      found = true;
+    }
+    k -= c;
+  }
+  __syncthreads();
+  return user;
+}
+
 template <int D, int RW, bool TREE, typename IdxT>
 __global__ void __launch_bounds__(kThr, 2) cache_attn_kernel(const CacheArgs a) {
   using C = CCfg<D, RW, TREE>;
@@ -152,7 +228,9 @@ __global__ void __launch_bounds__(kThr, 2) cache_attn_kernel(const CacheArgs a) 
   const int rb = (int)(unit % a.row_blocks);
   unit /= a.row_blocks;
   const int hk = (int)(unit % a.Hkv);
-  const int64_t b = unit / a.Hkv;
+  int64_t b = unit / a.Hkv;
+  if constexpr (TREE)
+    if (a.longest_first) b = longest_first<IdxT>(a, b, reinterpret_cast<uint32_t*>(smem));
   const int G = a.H / a.Hkv;
   const IdxT* off = static_cast<const IdxT*>(a.off);
 
@@ -646,6 +724,8 @@ int launch_cache(CacheArgs a, int64_t max_rows, int64_t keys, int dev, int sms, 
   a.split = 1;
   while (a.split < kMaxSplit && units * a.split <= sms && tiles >= 2 * a.split) a.split *= 2;
   if (units * a.split >= (int64_t)INT_MAX) return JCA_ERR_SHAPE;
+  // Blocks that all fit the device at once start together, in whatever order.
+  a.longest_first = TREE && a.B > 1 && units > 2 * (int64_t)sms;
   auto kernel = cache_attn_kernel<D, RW, TREE, IdxT>;
   static std::atomic<bool> set[kMaxDevices];
   if (!set[dev].load(std::memory_order_acquire)) {
