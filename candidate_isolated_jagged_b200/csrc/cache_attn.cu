@@ -8,10 +8,10 @@
 // What bounds it: reading the cache. A user's n tokens times the G = H / Hkv query heads of a key
 // head are the rows of one product against that head's keys, so a key's 4 d bytes (K and V) serve
 // n G rows. With few rows (256 users, one token each, 4 heads to a key head: 68 us, 0.90 of the copy
-// bandwidth) nothing else counts. With 64 rows (256 users with trees of 64 tokens: 222 us, 0.41) a
+// bandwidth) nothing else counts. With 64 rows (256 users with trees of 64 tokens: 151 us, 0.60) a
 // key of d = 128 takes an SM 22 cycles to read at the copy bandwidth, 16 of the warp-level tensor
-// instruction (m16n8k16, 8 cycles each) and 20 of shared-memory reads, which two warps per
-// scheduler overlap only in part, and the longest histories run on after the others. A
+// instruction (m16n8k16, 8 cycles each) and 20 of shared-memory reads, which three warps per
+// scheduler overlap (two: 165 us), and the longest history, 65 tiles in one block, ends last. A
 // 128-row tcgen05 tile would leave half or more of its rows empty here and would have to clear the
 // ends of the cache in shared memory; here the copies zero-fill what lies behind the last key.
 // One user alone (4,096 keys: 10.9 us) pays for its launch, three dependent reads and the joining.
@@ -102,7 +102,8 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 // RW warps of 16 rows, times KW warps that share the rows and split the keys of a tile. (Eight warps
-// for 64 rows, two to a row group, measured slower: 272 us against 222 on the 256 users with trees.)
+// for 64 rows, two to a row group, measured slower: 272 us against 222 on the 256 users with trees,
+// with the users in the order of the batch.)
 template <int D, int RW, bool TREE>
 struct CCfg {
   static constexpr int CH = D / 8;                        // 16-byte chunks of a row
@@ -111,16 +112,17 @@ struct CCfg {
   static constexpr int KPW = kBK / KW;                    // keys of a tile per warp
   static constexpr int TILE = kBK * D * 2;                // bytes of a K or V tile
   static constexpr int STAGE = 2 * TILE;
-  static constexpr int STAGES = D == 128 ? 3 : 4;
+  static constexpr int STAGES = D == 128 ? (RW == 4 ? 2 : 3) : 4;
+  static constexpr int BPS = RW == 4 ? 3 : 2;             // blocks per SM
   static constexpr int OFF_ML = STAGES * STAGE;           // [KW][RB] m and l, then [RB] joined
   static constexpr int OFF_BITS = OFF_ML + (2 * KW + 2) * RB * 4;
-  static constexpr int OFF_PAR = OFF_BITS + (TREE ? RB * kTreeWords * 4 : 0);
-  static constexpr int OFF_TILES = OFF_PAR + (TREE ? kMaxTree * 2 : 0);
+  static constexpr int OFF_PAR = 0;                       // in the ring, before its first tile
+  static constexpr int OFF_TILES = OFF_BITS + (TREE ? RB * kTreeWords * 4 : 0);
   static constexpr int SMEM = OFF_TILES + (TREE ? 128 : 16);
   // Partial results [KW][RB][D] fp32 reuse the ring.
   static_assert(KW * RB * D * 4 <= STAGES * STAGE, "partials fit the ring");
   static_assert(RB * D * 2 <= STAGE, "Q fits one stage");
-  static_assert(SMEM <= 113 * 1024, "two blocks per SM");
+  static_assert(BPS * (SMEM + 1024) <= 228 * 1024, "blocks per SM");
 };
 
 // Shared-memory byte offset of chunk c of row r: chunks are XORed with the row so that eight rows'
@@ -145,7 +147,7 @@ struct Keys {
 
 // The user that takes place b when the users of each group of 256 go by the length of their history,
 // longest first. Blocks start in the order of their index, so a long history that starts late runs
-// on alone after the others (256 users with trees of 64 tokens: 222 us in the order of the batch).
+// on alone after the others (256 users with trees of 64 tokens, two blocks to an SM: 222 us in the order of the batch, 165 us so).
 // A sort by quarter octaves is close enough and cheap: counts, a scan, the bucket that holds the
 // place, the place's bit among its members. It depends on the lengths only, so all blocks agree
 // whatever the lengths hold. `w`: 128 + 16 words of shared memory.
@@ -218,7 +220,7 @@ __device__ int64_t longest_first(const CacheArgs& a, int64_t b, uint32_t* w) {
 }
 
 template <int D, int RW, bool TREE, typename IdxT>
-__global__ void __launch_bounds__(kThr, 2) cache_attn_kernel(const CacheArgs a) {
+__global__ void __launch_bounds__(kThr, CCfg<D, RW, TREE>::BPS) cache_attn_kernel(const CacheArgs a) {
   using C = CCfg<D, RW, TREE>;
   extern __shared__ __align__(128) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
@@ -714,7 +716,8 @@ constexpr int kMaxDevices = 64;
 // the longest list leaves each part a tile: with few units the longest list sets the time (4 users
 // with trees: 14.3 us whole, 11.2 in two parts, 9.7 in eight; one token over 4,096 keys: 24.6 us in
 // two parts, 10.9 in eight), with many the parts only cost (256 users with trees 222 us, in two
-// parts 284 us).
+// parts 284 us, and 290 us when only lists of more than 16 tiles are split; measured before users went
+// by length).
 template <int D, int RW, bool TREE, typename IdxT>
 int launch_cache(CacheArgs a, int64_t max_rows, int64_t keys, int dev, int sms, cudaStream_t st) {
   using C = CCfg<D, RW, TREE>;
@@ -725,7 +728,7 @@ int launch_cache(CacheArgs a, int64_t max_rows, int64_t keys, int dev, int sms, 
   while (a.split < kMaxSplit && units * a.split <= sms && tiles >= 2 * a.split) a.split *= 2;
   if (units * a.split >= (int64_t)INT_MAX) return JCA_ERR_SHAPE;
   // Blocks that all fit the device at once start together, in whatever order.
-  a.longest_first = TREE && a.B > 1 && units > 2 * (int64_t)sms;
+  a.longest_first = TREE && a.B > 1 && units > C::BPS * (int64_t)sms;
   auto kernel = cache_attn_kernel<D, RW, TREE, IdxT>;
   static std::atomic<bool> set[kMaxDevices];
   if (!set[dev].load(std::memory_order_acquire)) {
