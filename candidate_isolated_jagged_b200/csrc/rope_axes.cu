@@ -294,6 +294,8 @@ int rope_axes(const void* q, const void* k, void* q_out, void* k_out, const void
   if (!aligned(q, 16) || !aligned(q_out, 16) || qs % per16 || qos % per16 ||
       (k && (!aligned(k, 16) || !aligned(k_out, 16) || ks % per16 || kos % per16)))
     return JCA_ERR_ALIGN;
+  // In place row by row only: with another stride a row's result would land in one not yet read.
+  if (T > 1 && ((q == q_out && qs != qos) || (k && k == k_out && ks != kos))) return JCA_ERR_SHAPE;
   int dev = 0, sms = 0;
   const int rc = current_device(&dev, &sms);
   if (rc) return rc;

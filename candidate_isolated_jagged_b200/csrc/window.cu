@@ -57,7 +57,7 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-// Checks the offsets and writes each row's user bounds; one block per user. Zeroes the counter from
+// Checks the offsets and writes each row's user bounds; a block per user and share of its rows. Zeroes the counter from
 // which the attention kernel claims its blocks.
 template <typename IdxT>
 __global__ void __launch_bounds__(128)
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(128)
                        int32_t* __restrict__ row_start, int32_t* __restrict__ row_end,
                        int32_t* __restrict__ row_user, int32_t* counters, int n_counters,
                        int32_t* status) {
-  if (blockIdx.x == 0 && (int)threadIdx.x < n_counters) counters[threadIdx.x] = 0;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && (int)threadIdx.x < n_counters) counters[threadIdx.x] = 0;
   if (*status != 0) return;
   for (int64_t b = blockIdx.x; b < B; b += gridDim.x) {
     const long long s = (long long)off[b], e = (long long)off[b + 1];
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(128)
       if (threadIdx.x == 0) atomicCAS(status, 0, (int32_t)JCA_STATUS_BAD_OFFSETS);
       continue;
     }
-    for (long long i = s + threadIdx.x; i < e; i += blockDim.x) {
+    for (long long i = s + blockIdx.y * 128 + threadIdx.x; i < e; i += gridDim.y * 128) {
       row_start[i] = (int32_t)s;
       if (row_end) row_end[i] = (int32_t)e;
       if (row_user) row_user[i] = (int32_t)b;
@@ -113,7 +113,6 @@ struct Cfg {
   static constexpr uint32_t LAYOUT = SW == 128 ? 2u : (SW == 64 ? 4u : 6u);
   static constexpr int KSTEPS_QK = D / 16;
   static constexpr int KSTEPS_PER_BLK = SW / 32;
-  static constexpr int KSTEPS_PV = BN / 16;
   // Ring depths; d = 128 fills shared memory (192 KB) with one Q buffer per tile and two stages.
   static constexpr int QS = D >= 128 ? 1 : 2;
   static constexpr int KVS = D >= 128 ? 2 : 4;
@@ -790,7 +789,9 @@ int window_check(int64_t B, int64_t T, int H, int Hkv, int d, int64_t window, in
 int window_plan(const void* offsets, int64_t B, int64_t T, int idx_bits, int32_t* row_start,
                 int32_t* row_end, int32_t* row_user, int32_t* counters, int n_counters,
                 int32_t* status, cudaStream_t st) {
-  const unsigned grid = (unsigned)(B < (1 << 20) ? B : (1 << 20));
+  // About four rows a thread on average, so that a few long users do not wait for one block each.
+  const int64_t x = B < (1 << 20) ? B : (1 << 20), share = T / (B * 512);
+  const dim3 grid((unsigned)x, (unsigned)(share < 1 ? 1 : share < 256 ? share : 256));
   if (idx_bits == 32)
     window_plan_kernel<int32_t><<<grid, 128, 0, st>>>(static_cast<const int32_t*>(offsets), B, T,
                                                       row_start, row_end, row_user, counters,

@@ -8,6 +8,7 @@ the library is missing, ``lib()`` raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -628,9 +629,20 @@ def _heads(name: str, t: torch.Tensor):
     return t.shape
 
 
-def _status_on(status: Optional[torch.Tensor], device) -> torch.Tensor:
+def _on(stream, device):
+    """Context in which a call's own scratch is made: on the call's stream, so that its first fill
+    comes before the kernels and its memory is not handed out again before they are done."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _status_on(status: Optional[torch.Tensor], device, stream) -> torch.Tensor:
     if status is None:
-        return new_status(device)
+        with _on(stream, device):
+            return new_status(device)
     _vector("status", status, 1, torch.int32, device)
     return status
 
@@ -716,12 +728,13 @@ def jca_window_bwd_workspace_bytes(B: int, T: int, H: int, Hkv: int, d_head: int
     return int(lib().jca_window_bwd_workspace_bytes(B, T, H, Hkv, d_head, n_sinks))
 
 
-def _window_scratch(workspace, status, nbytes, dev):
+def _window_scratch(workspace, status, nbytes, dev, stream):
     if workspace is None:
-        workspace = torch.empty(nbytes(), dtype=torch.uint8, device=dev)
+        with _on(stream, dev):
+            workspace = torch.empty(nbytes(), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {dev}")
-    return workspace, _status_on(status, dev)
+    return workspace, _status_on(status, dev, stream)
 
 
 def jagged_window_attn_fwd(q, k, v, out, offsets, window: int, n_sinks: int = 0, valid=None,
@@ -741,7 +754,8 @@ def jagged_window_attn_fwd(q, k, v, out, offsets, window: int, n_sinks: int = 0,
     _vector("valid", valid, T, torch.uint8, dev)
     _vector("lse", lse, T * H, torch.float32, dev)
     workspace, status = _window_scratch(
-        workspace, status, lambda: jca_window_workspace_bytes(B, T, H, Hkv, d, n_sinks), dev)
+        workspace, status, lambda: jca_window_workspace_bytes(B, T, H, Hkv, d, n_sinks), dev,
+        stream)
     return _call("jagged_window_attn_fwd", dev, stream, _at(q), _at(k), _at(v), _at(out), _at(lse),
                  _at(offsets), _at(valid), B, T, H, Hkv, d, int(window), int(n_sinks), qs, ks, vs,
                  float(scale), _idx_bits(offsets), _at(workspace),
@@ -766,7 +780,8 @@ def jagged_window_attn_bwd(q, k, v, out, dout, lse, dq, dk, dv, offsets, window:
     _vector("valid", valid, T, torch.uint8, dev)
     _vector("lse", lse, T * H, torch.float32, dev)
     workspace, status = _window_scratch(
-        workspace, status, lambda: jca_window_bwd_workspace_bytes(B, T, H, Hkv, d, n_sinks), dev)
+        workspace, status, lambda: jca_window_bwd_workspace_bytes(B, T, H, Hkv, d, n_sinks),
+        dev, stream)
     return _call("jagged_window_attn_bwd", dev, stream, _at(q), _at(k), _at(v), _at(out), _at(dout),
                  _at(lse), _at(dq), _at(dk), _at(dv), _at(offsets), _at(valid), B, T, H, Hkv, d,
                  int(window), int(n_sinks), qs, ks, vs, float(scale), _idx_bits(offsets),
@@ -790,7 +805,7 @@ def jagged_window_decode_fwd(q, k_new, v_new, k_cache, v_cache, out, cache_offse
     _packed("out", out, B, H, d, t16, dev)
     _vector("cache_offsets", cache_offsets, B + 1, cache_offsets.dtype, dev)
     _vector("cache_len", cache_len, B, cache_offsets.dtype, dev)
-    status = _status_on(status, dev)
+    status = _status_on(status, dev, stream)
     return _call("jagged_window_decode_fwd", dev, stream, _at(q), _at(k_new), _at(v_new),
                  _at(k_cache), _at(v_cache), _at(out), _at(cache_offsets), _at(cache_len), B, R, H,
                  Hkv, d, int(window), int(n_sinks), qs, ks, vs, float(scale),
@@ -817,7 +832,7 @@ def cand_tree_attn_fwd(cand_q, own_k, own_v, cand_offsets, parent, hist_k, hist_
     _vector("hist_offsets", hist_offsets, B + 1, cand_offsets.dtype, dev)
     _vector("hist_len", hist_len, B, cand_offsets.dtype, dev)
     _vector("parent", parent, N, torch.int32, dev)
-    status = _status_on(status, dev)
+    status = _status_on(status, dev, stream)
     return _call("cand_tree_attn_fwd", dev, stream, _at(cand_q), _at(own_k), _at(own_v),
                  _at(cand_offsets), _at(parent), _at(hist_k), _at(hist_v), _at(hist_offsets),
                  _at(hist_len), _at(out), B, N, R, H, Hkv, d, int(max_cand), qs, ks, vs,

@@ -557,7 +557,8 @@ int jca_stack_fwd(const void* x, void* x_out, const void* weights, int n_layers,
  *     be NULL (Hkv is then ignored). Heads are packed (head stride d_head); consecutive tokens are
  *     q_stride / k_stride elements apart (>= heads * d_head), so slices of a fused projection work.
  *   q_out, k_out: the same shapes, rows q_out_stride / k_out_stride apart, written. q_out may be q
- *     with the same stride (in place), and k_out k; other overlaps are not allowed.
+ *     with the same stride (in place; another stride is JCA_ERR_SHAPE), and k_out k; other overlaps
+ *     are not allowed.
  *   positions [T, n_axes] int32 or int64 (idx_bits), packed, read. Any value is valid.
  *   sections  [n_axes] HOST memory, read before the call returns; n_axes in 1..4, each >= 0, sum
  *     <= d_head/2. base > 1.
@@ -599,6 +600,8 @@ int jca_rope_axes_bwd(const void* dq_out, const void* dk_out, void* dq, void* dk
  *   scale    <= 0 selects 1/sqrt(d_head). H a multiple of Hkv.
  *   workspace >= jca_window_workspace_bytes(...) bytes, 256-byte aligned, no part of it needs to
  *            start at zero. Calls that may overlap on the GPU need a workspace each.
+ * The outputs overlap no input. A real token's q, k and v are finite: an Inf or NaN there may reach
+ * other rows of its tile of 128 rows, those of a neighbouring user among them.
  * Device errors: bad offsets -> JCA_STATUS_BAD_OFFSETS (nothing is written then);
  * JCA_STATUS_TIMEOUT.
  * ------------------------------------------------------------------------------------------- */

@@ -289,6 +289,75 @@ def test_window_two_streams():
         b.check_forward(100, 4)
 
 
+def test_calls_on_a_given_stream_make_their_scratch_there():
+    """With a stream and no workspace or status, the scratch must outlive the call: memory of its
+    size is taken and overwritten on the current stream while the given stream is still busy."""
+    b, t = Window([150, 420, 64], 4, 4, 64, seed=13), Tree([9, 20], [200, 77], 4, 2, 64, seed=13)
+    side, busy = torch.cuda.Stream(), torch.randn(4096, 4096, device=dev())
+    b.forward(100, 4)
+    b.backward(100, 4)
+    want = [b.out.clone()] + [x.clone() for x in b.grads]
+    got = [torch.full_like(x, float("nan")) for x in want]
+    lse = b.lse
+    fwd = torch.empty_like(lse)
+    n = [jca.jca_window_workspace_bytes(3, b.T, 4, 4, 64, 4),
+         jca.jca_window_bwd_workspace_bytes(3, b.T, 4, 4, 64, 4), 4]
+    fresh = torch.empty_like(b.out)
+    for handle in (side, side.cuda_stream):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                busy = busy @ busy * 1e-2
+        jca.jagged_window_attn_fwd(b.q, b.k, b.v, fresh, b.off, 100, 4, lse=fwd, stream=handle)
+        jca.jagged_window_attn_bwd(b.q, b.k, b.v, b.out, b.dout, lse, *got[1:], b.off, 100, 4, stream=handle)
+        jca.cand_tree_attn_fwd(t.q, t.k, t.v, t.off, t.parent, t.hk, t.hv, t.ho, t.out, 20, stream=handle)
+        junk = [torch.full((x,), 255, dtype=torch.uint8, device=dev()) for x in n for _ in range(4)]
+        torch.cuda.synchronize()
+        del junk
+        for x, y in zip(got[1:], want[1:]):
+            assert torch.equal(x, y)
+        t.check()
+        b.out, b.lse = fresh, fwd
+        b.check_forward(100, 4)
+        b.out, b.lse = want[0], lse
+        for x in got + [fresh, fwd, t.out]:
+            x.fill_(float("nan"))
+
+
+def test_window_writes_its_rows_only():
+    """Gradients and outputs that lie inside larger buffers: the rows before and behind stay. The
+    last user is shorter than the first tokens of the call."""
+    b = Window([300, 140, 3], 4, 2, 32, seed=14)
+    big = {n: torch.full((b.T + 64, h, 32), 3.0, dtype=torch.bfloat16, device=dev())
+           for n, h in (("out", 4), ("dq", 4), ("dk", 2), ("dv", 2))}
+    lse = torch.full((b.T + 64, 4), 3.0, device=dev())
+    mid = slice(32, 32 + b.T)
+    for window, sinks in ((2, 8), (1, 128), (50, 5)):
+        b.backward(window, sinks)
+        want = b.grads
+        jca.jagged_window_attn_fwd(b.q, b.k, b.v, big["out"][mid], b.off, window, sinks, lse=lse[mid], status=b.st)
+        jca.jagged_window_attn_bwd(b.q, b.k, b.v, b.out, b.dout, b.lse, *(big[n][mid] for n in ("dq", "dk", "dv")),
+                                   b.off, window, sinks, status=b.st)
+        for n, w in zip(("dq", "dk", "dv"), want):
+            assert torch.equal(big[n][mid], w)
+        b.check_backward(window, sinks)
+        b.out, b.lse = big["out"][mid], lse[mid]
+        b.check_forward(window, sinks)
+        for x in list(big.values()) + [lse]:
+            assert bool((x[:32] == 3.0).all()) and bool((x[32 + b.T:] == 3.0).all())
+
+
+def test_window_backward_on_many_users_twice():
+    """More users than units run at once, and equal bits from equal calls."""
+    rng = np.random.default_rng(3)
+    b = Window(list(rng.integers(0, 120, 700)), 2, 1, 64, seed=15)
+    first = [x.clone() for x in b.backward(20, 3)]
+    again = b.backward(20, 3)
+    for x, y in zip(first, again):
+        assert torch.equal(x, y)
+    b.check_backward(20, 3)
+
+
 def test_window_rows_beyond_32_bit_offsets():
     """2^31 elements and more in q and out; sampled users at both ends."""
     lengths = [1000] * 1050
@@ -425,6 +494,54 @@ def test_decode_bad_users_leave_the_others():
         assert bool((out[bad] == 7.0).all())
 
 
+def test_decode_captured_twice_and_two_streams():
+    """Two graphs over one cache, replayed in turn with the lengths counted on the device, and two
+    batches on two streams."""
+    a, b = (Decode([5, 600, -1], [40, 700, 3], 8, 2, 64, seed=s) for s in (3, 4))
+    graphs = []
+    for x in (a, b):
+        x.run(200, 2)
+        x.check(200, 2)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            x.run(200, 2)
+        graphs.append(g)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for x in (a, b):
+        x.out.fill_(float("nan"))
+    torch.cuda.synchronize()
+    for g, s in zip(graphs, streams):
+        with torch.cuda.stream(s):
+            g.replay()
+    torch.cuda.synchronize()
+    for x in (a, b):
+        x.check(200, 2)
+        # One token further.
+        x.len += (x.len >= 0).long()
+        torch.cuda.synchronize()
+    for x, g in zip((a, b), graphs):
+        g.replay()
+        torch.cuda.synchronize()
+        for u, p in enumerate(x.lens):
+            if p >= 0:
+                s = int(x.off_np[u])
+                x.kc_cpu[s + p], x.vc_cpu[s + p] = x.kn_cpu[u], x.vn_cpu[u]
+                x.lens[u] = p + 1
+        x.check(200, 2)
+
+
+def test_decode_many_users_equal_bits():
+    rng = np.random.default_rng(8)
+    lens = list(rng.integers(-1, 300, 700))
+    b = Decode(lens, [int(n) + 2 for n in lens], 8, 2, 128, seed=9)
+    b.run(128, 4)
+    b.check(128, 4)
+    first = b.out.clone()
+    b.run(128, 4)
+    assert torch.equal(first, b.out)
+
+
 # ------------------------------------------------------------------------------------------------
 # Trees of drafted tokens
 # ------------------------------------------------------------------------------------------------
@@ -528,6 +645,43 @@ def test_star_tree_is_the_candidate_only_layer():
     jca.check_status(st)
     b.check()
     torch.testing.assert_close(b.out.float(), out.float(), atol=3e-2, rtol=2.0**-6)
+
+
+@pytest.mark.parametrize("B,H,Hkv,lens", [(600, 2, 2, True), (257, 8, 8, False), (300, 48, 2, True), (450, 1, 1, False)])
+def test_tree_many_users_in_any_order(B, H, Hkv, lens):
+    """More blocks than run at once: users are then taken by length, in groups of 256."""
+    rng = np.random.default_rng(B)
+    hist = [int(x) for x in np.floor(rng.lognormal(3.0, 1.5, B)).clip(0, 2000)]
+    hist[5], hist[B - 1], hist[B // 2] = 0, 700, 0
+    use = [int(rng.integers(0, n + 1)) for n in hist] if lens else None
+    b = Tree([int(x) for x in rng.integers(0, 6, B)], hist, H, Hkv, 32, seed=B, hist_len=use)
+    b.run()
+    b.check()
+    first = b.out.clone()
+    b.run()
+    assert torch.equal(first, b.out)
+
+
+def test_tree_many_users_with_a_bad_one():
+    """Lengths that mean nothing change no other user's place."""
+    n = 500
+    for name, at, x, code in (("hl", 300, -5, 1), ("hl", 7, 1 << 40, 1), ("ho", n, 1 << 40, 2)):
+        b = Tree([2] * n, [10] * n, 2, 2, 16, seed=1, hist_len=[10] * n)
+        want = torch.empty_like(b.out)
+        b.run()
+        b.check()
+        want.copy_(b.out)
+        user = at if name == "hl" else n - 1
+        getattr(b, name)[at] = x
+        b.out.fill_(7.0)
+        b.run()
+        torch.cuda.synchronize()
+        assert int(b.st.item()) == code
+        assert bool((b.out[2 * user:2 * user + 2] == 7.0).all())
+        rest = torch.ones(2 * n, dtype=torch.bool, device=dev())
+        rest[2 * user:2 * user + 2] = False
+        same = (b.out == want).flatten(1).all(1) | (b.out == 7.0).flatten(1).all(1)
+        assert bool(same[rest].all())          # right, or not written
 
 
 def test_tree_bad_users_leave_the_others():

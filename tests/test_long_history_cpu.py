@@ -174,3 +174,25 @@ def test_wrappers_refuse_cpu_tensors_and_shapes(L):
 
 def test_status_names(L):
     assert "parent" in jca.status_string(8) and "type" in jca.status_string(-10)
+
+
+def test_rope_axes_in_place_needs_one_stride(L):
+    sec = (ctypes.c_int32 * 1)(4)
+    for fn in (L.jca_rope_axes_fwd, L.jca_rope_axes_bwd):
+        call = _caller(fn, q=P, k=P, qo=P, ko=P, pos=P, sec=sec, n_axes=1, per_axis=0, T=5, H=4, Hkv=2,
+                       d=16, qs=64, ks=32, qos=64, kos=32, base=10000.0, dtype=0, idx_bits=64,
+                       stream=None)
+        assert call(qs=128) == -2
+        assert call(kos=64) == -2
+
+
+def test_wrappers_refuse_scratch_of_another_kind(L):
+    dev = torch.device("cpu")
+    with pytest.raises(TypeError, match="status"):
+        jca._status_on(torch.zeros(1), dev, None)
+    with pytest.raises(ValueError, match="status"):
+        jca._status_on(torch.zeros(2, dtype=torch.int32), dev, None)
+    status = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="workspace"):
+        jca._window_scratch(torch.zeros(8, 2, dtype=torch.uint8)[:, 0], status, lambda: 0, dev, None)
+    assert jca._status_on(status, dev, None) is status
