@@ -19,6 +19,7 @@
 //   S = O1 I1^T,  dP = O2 I2^T  (SS MMAs)   ->   dS (and P) as bf16 in TMEM   ->   TS MMAs
 //   dQ  (O1 = Q, O2 = dO, I1 = K, I2 = V):   acc0 += dS I1
 //   dKV (O1 = K, O2 = V, I1 = Q, I2 = dO):   acc0 (dV) += P^T I2,  acc1 (dK) += dS^T I1
+// The blocks of the three parts share one launch.
 // A step takes 64 inner rows, so that S and dP fit two or three times beside the accumulators in TMEM
 // and the tensor core works ahead of the compute warps. Columns a warp's rows do not see are
 // decided per 32 columns: none (zeros are written), all (no masking) or some.
@@ -28,8 +29,14 @@
 //   warps 4..11 compute, a row a thread, two warps per 32 rows (32 of the 64 columns each);
 //   warps 12..15 write a unit's accumulators out while the others are at the next unit.
 //
-// What bounds it: seven products per pair instead of five (S and dP are formed in both passes) on
-// the tensor core, whose 64-column steps cost the issuing thread about what 128-column ones would.
+// What bounds it (256 users, window 256, d = 128: dKV 437 us, dQ 373, first tokens 118; 0.33 of the copy
+// bandwidth with the statistics before and the joining behind): the tensor core's part of the
+// chain S, dP -> dS -> products. Seven products are formed per pair instead of five (S and dP in both
+// passes), and those of 64 columns take nearly as long as those of 128 (about 60 cycles for 16 of
+// the head) but leave room for three score buffers, which overlap the exponentials and conversions
+// (256 users 1.10 ms in steps of 128 columns, 1.04 ms in steps of 64). For first tokens a 128-row
+// tile holds n_sinks keys.
+#include <algorithm>
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -55,8 +62,8 @@ constexpr int kEpilogue = 128;
 // Registers a thread: 512 x 128 at launch, shared out anew (72 + 2 x 168 + 104 = 4 x 128).
 constexpr int kRegsRoles = 72, kRegsCompute = 168, kRegsEpilogue = 104;
 constexpr int kStep = 64;        // inner rows of a step
-// Query rows of a kSink unit: 256 rows keep the longest unit short (16 users: 14 us, with 1024 rows
-// 36 us; 256 users 153 and 164 us).
+// Query rows of a kSink unit: 256 rows keep the longest unit short (16 users: 14 us alone, with 1024
+// rows 36 us; on 256 users 1024 rows took 7 % more).
 constexpr int kChunk = 256;
 constexpr int kRing = 4;
 constexpr int kEntry = 6;        // ints of a ring entry
@@ -77,9 +84,11 @@ struct BwdArgs {
   const int4* sink_users;     // their users {first row, end, user, 0}
   const int32_t* n_sink_units;
   const int32_t* n_sink_users;
-  int32_t* counter;
+  int32_t* counter;           // [3] next unit of each part
   int32_t* status;
-  int T, H, Hkv, group, window, n_sinks, n_units;
+  int T, H, Hkv, group, window, n_sinks;
+  int units_dq, units_dkv;
+  int blocks_sink, blocks_dkv;   // the launch's blocks in this order, those of kDQ last
   int v8;                     // gradients can be written with 32-byte stores
   float scale, scale_log2;
 };
@@ -222,9 +231,11 @@ __device__ __forceinline__ bool ring_take(Ring& r, const BwdArgs& a, Unit& u,
 template <int MODE>
 __device__ void claim_role(const BwdArgs& a, Ring r, volatile int* abort_flag) {
   const int heads = MODE == kDQ ? a.H : a.Hkv;
-  const int n = MODE == kSink ? *a.n_sink_units * heads : a.n_units;
+  const int n = MODE == kSink  ? *a.n_sink_units * heads
+                : MODE == kDQ ? a.units_dq
+                              : a.units_dkv;
   for (;;) {
-    const int v = atomicAdd(a.counter, 1);
+    const int v = atomicAdd(a.counter + MODE, 1);
     int e[kEntry] = {-1, 0, 0, 0, 0, 0};
     if (v < n) {
       e[1] = v % heads;
@@ -689,11 +700,9 @@ __device__ void epilogue_role(const BwdArgs& a, uint32_t bars, uint32_t tmem,
 }
 
 template <int D, int MODE>
-__global__ void __launch_bounds__(kThreads, 1)
-    window_bwd_kernel(const __grid_constant__ CUtensorMap tmO1,
-                      const __grid_constant__ CUtensorMap tmO2,
-                      const __grid_constant__ CUtensorMap tmI1,
-                      const __grid_constant__ CUtensorMap tmI2, const BwdArgs a) {
+__device__ __forceinline__ void bwd_block(const CUtensorMap& tmO1, const CUtensorMap& tmO2,
+                                          const CUtensorMap& tmI1, const CUtensorMap& tmI2,
+                                          const BwdArgs& a) {
   using C = Cfg<D, MODE>;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -766,6 +775,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
+}
+
+// The three parts are independent, so one launch holds the blocks of all: a small batch's parts run side
+// by side (16 users 16 us; three launches 38 us), and a large one's blocks of the next part start
+// where blocks of the one before end (256 users 919 us, one after the other 928 us). First tokens
+// come first: behind the others a few blocks would take all their units in a row (16 users 43 us).
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
+                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const BwdArgs a) {
+  const int b = (int)blockIdx.x;
+  if (b < a.blocks_sink) bwd_block<D, kSink>(tmK, tmV, tmQ, tmDO, a);
+  else if (b < a.blocks_sink + a.blocks_dkv) bwd_block<D, kDKV>(tmK, tmV, tmQ, tmDO, a);
+  else bwd_block<D, kDQ>(tmQ, tmDO, tmK, tmV, a);
 }
 
 // Statistics of every row and head, [H][T]: the log-sum-exp in log2 units (+inf for a row that sees no
@@ -884,30 +908,27 @@ struct Maps {
   CUtensorMap q, k, v, dout;
 };
 
-template <int D, int MODE>
-int launch_pass(BwdArgs a, const Maps& m, int counter, int units, int dev, int sms,
-                cudaStream_t st) {
-  using C = Cfg<D, MODE>;
+// Every part gets a block per unit, or per SM where it has more units than the device SMs.
+template <int D>
+int launch_parts(BwdArgs a, const Maps& m, int64_t sink_units, int dev, int sms, cudaStream_t st) {
+  constexpr int kBytes = std::max({Cfg<D, kDQ>::SMEM_ALLOC, Cfg<D, kDKV>::SMEM_ALLOC,
+                                   Cfg<D, kSink>::SMEM_ALLOC});
   static std::atomic<bool> set[64];
   if (!set[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(window_bwd_kernel<D, MODE>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::SMEM_ALLOC) != cudaSuccess)
+    if (cudaFuncSetAttribute(window_bwd_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kBytes) != cudaSuccess)
       return JCA_ERR_CUDA;
     set[dev].store(true, std::memory_order_release);
   }
-  a.counter += counter;
-  a.n_units = units;
-  const int grid = units < sms ? units : sms;
-  if (MODE == kDQ)
-    window_bwd_kernel<D, MODE><<<grid, kThreads, C::SMEM_ALLOC, st>>>(m.q, m.dout, m.k, m.v, a);
-  else
-    window_bwd_kernel<D, MODE><<<grid, kThreads, C::SMEM_ALLOC, st>>>(m.k, m.v, m.q, m.dout, a);
+  a.blocks_sink = (int)std::min<int64_t>(sink_units, sms);
+  a.blocks_dkv = std::min(a.units_dkv, sms);
+  const int grid = a.blocks_sink + a.blocks_dkv + std::min(a.units_dq, sms);
+  window_bwd_kernel<D><<<grid, kThreads, kBytes, st>>>(m.q, m.dout, m.k, m.v, a);
   return cudaGetLastError() == cudaSuccess ? JCA_OK : JCA_ERR_CUDA;
 }
 
 template <int D>
-int launch_bwd(const BwdArgs& a, const void* q, const void* k, const void* v, const void* out,
+int launch_bwd(BwdArgs a, const void* q, const void* k, const void* v, const void* out,
                const void* dout, const float* lse, const void* offsets, int64_t B, int64_t qs,
                int64_t ks, int64_t vs, int idx_bits, float* lse2, float* dsum, int4* sinks,
                int4* sink_users, int32_t* n_sinks, int64_t slots, int dev, int sms,
@@ -931,14 +952,10 @@ int launch_bwd(const BwdArgs& a, const void* q, const void* k, const void* v, co
         sinks, sink_users, n_sinks, n_sinks + 1, a.status);
   if (cudaGetLastError() != cudaSuccess) return JCA_ERR_CUDA;
   const int tiles = (a.T + kTileM - 1) / kTileM;
-  int rc = launch_pass<D, kDQ>(a, m, 0, tiles * a.H, dev, sms, st);
-  if (rc) return rc;
-  if (sinks) {
-    const int64_t most = slots * a.Hkv;   // the list's length is known on the device only
-    rc = launch_pass<D, kSink>(a, m, 1, (int)(most < sms ? most : sms), dev, sms, st);
-    if (rc) return rc;
-  }
-  rc = launch_pass<D, kDKV>(a, m, 2, tiles * a.Hkv, dev, sms, st);
+  a.units_dq = tiles * a.H;
+  a.units_dkv = tiles * a.Hkv;
+  // The list of kSink units is counted on the device; no more than this.
+  const int rc = launch_parts<D>(a, m, sinks ? slots * a.Hkv : 0, dev, sms, st);
   if (rc || !sinks) return rc;
   const int64_t most = B * a.Hkv;
   window_join_kernel<D><<<(int)(most < (int64_t)sms * 64 ? most : sms * 64), 256, 0, st>>>(a);
