@@ -34,11 +34,13 @@
 // is 350 us here).
 //
 // What bounds it (256 users, window 256, d = 128: 350 us, 0.49 of the copy bandwidth; 12 long users,
-// window 1024, d = 64: 510 us): the chain QK -> softmax -> PV of each query tile. A tile's softmax takes
-// about 1700 cycles alone, of which 1024 are its 16,384 exponentials, and TMEM holds the scores of
-// two tiles. Eight warps on one tile at a time (64 columns a thread) measured 350 and 657 us,
-// one thread issuing both tiles' MMAs 350 and 562 us. Without padding the kernel reads and writes
-// each tensor about once; exponentials and tensor core are each busy less than half of the time.
+// window 1024, d = 64: 515 us): the chain QK -> softmax -> PV of each query tile. At d = 64 a tile takes
+// a softmax group about 4100 cycles: 1600 to 2400 for its 16,384 exponentials (1024 at the unit's full
+// rate), 770 for the maximum, 250 to read the scores, the rest in waits that are short but many; TMEM
+// holds the scores of two tiles only. Exponential unit busy 0.42, tensor core 0.23. What did not help:
+// eight warps on one tile at a time (64 columns a thread; 350 and 657 us), sixteen with two threads to a
+// row that exchange their maxima (460 and 745 us), one thread issuing both tiles' MMAs (350 and
+// 562 us), the two groups taking turns at their exponentials (363 and 540 us).
 #include <atomic>
 #include <climits>
 #include <cmath>
@@ -460,7 +462,7 @@ __device__ __forceinline__ uint32_t range_bits(int a, int b) {
 // Weights p = 2^(scale_log2 s - m) of 32 scores, their sum added to (acc0, acc1), and the weights
 // rounded to bf16 pairs, the operand type of the PV product.
 __device__ __forceinline__ void weights32(const uint32_t* x, float2 sl2v, float2 negv, float2& acc0,
-                                          float2& acc1, uint32_t (&pk)[16]) {
+                                          float2& acc1, uint32_t* pk) {
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
     const float2 xs = __ffma2_rn(
@@ -587,24 +589,29 @@ __device__ void softmax_role(const FwdArgs& a, uint32_t bars, uint32_t tmem,
       const float neg_m = (m_use == -INFINITY) ? 0.f : -m_use;
       const float alpha = (rescale && m != -INFINITY) ? fast_exp2(m - m_use) : 1.f;
       const float2 sl2v = make_float2(sl2, sl2), negv = make_float2(neg_m, neg_m);
-      if (C::SEP_P && lt > 1) {
-        // The PV before has read the weights that these replace, and O is stable.
-        ok = __all_sync(0xffffffffu, mbar_wait_long(bars + 8 * (C::B_PVDONE + grp), lt & 1, abort_flag,
-                                               a.status));
-        if (!ok) break;
-        tc_fence_after();
-      }
       float2 acc0 = make_float2(0.f, 0.f), acc1 = acc0;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
+        uint32_t* pk = x + 32 * c;   // in place: each pair goes where a pair before it was read
         if ((any >> c) & 1) {
           weights32(x + 32 * c, sl2v, negv, acc0, acc1, pk);
         } else {
 #pragma unroll
           for (int k = 0; k < 16; ++k) pk[k] = 0u;
         }
-        tmem_st_x16(t_p + 16 * c, pk);
+        if (!C::SEP_P) tmem_st_x16(t_p + 16 * c, pk);
+      }
+      if (C::SEP_P) {
+        if (lt > 1) {
+          // The PV before has read the weights that these replace, and O is stable.
+          ok = __all_sync(0xffffffffu, mbar_wait_long(bars + 8 * (C::B_PVDONE + grp), lt & 1, abort_flag,
+                                                 a.status));
+          if (!ok) break;
+          tc_fence_after();
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          tmem_st_x16(t_p + 16 * c, x + 32 * c);
       }
       // O is stable here: without SEP_P its last PV was issued before the QK that filled S, and a
       // commit fires only after every earlier MMA of its thread.
