@@ -647,8 +647,8 @@ int jagged_window_attn_bwd(const void* q, const void* k, const void* v, const vo
  *     and lies in [0, R]. cache_len[b] = -1 marks an empty slot of the batch: out is 0 there and no
  *     row is written.
  *   window, n_sinks, scale as above, with any n_sinks >= 0.
- * Device errors, each for its own user, whose rows are then not written while the other users' may
- * be: cache_offsets that fall or leave [0, R] -> JCA_STATUS_BAD_OFFSETS; cache_len[b] < -1, or no room for
+ * Device errors, each for its own user, whose rows are then not written while those of other users
+ * (some of their heads, too) may be: cache_offsets that fall or leave [0, R] -> JCA_STATUS_BAD_OFFSETS; cache_len[b] < -1, or no room for
  * the new token -> JCA_STATUS_BAD_LENGTH. */
 int jagged_window_decode_fwd(const void* q, const void* k_new, const void* v_new, void* k_cache,
                              void* v_cache, void* out, const void* cache_offsets,
@@ -674,10 +674,10 @@ int jagged_window_decode_fwd(const void* q, const void* k_new, const void* v_new
  *   cand_offsets, hist_offsets [B+1], hist_len [B] in the idx_bits type, read; cand_offsets starts
  *     at 0 and ends at Nc, hist_offsets never falls and lies in [0, R].
  *   max_cand: no run is longer; 1 <= max_cand <= 1024. scale <= 0 selects 1/sqrt(d_head).
- * Device errors, each for its own user, whose rows are then not written while the other users' may
- * be: bad offsets -> JCA_STATUS_BAD_OFFSETS; hist_len[b] outside
- * its region -> JCA_STATUS_BAD_LENGTH; a bad parent or a run longer than max_cand ->
- * JCA_STATUS_BAD_TREE. No workspace.
+ * Device errors, each for its own user, whose rows are then not written while those of other users
+ * (some of their heads, too) may be: bad offsets -> JCA_STATUS_BAD_OFFSETS; hist_len[b] outside its
+ * region -> JCA_STATUS_BAD_LENGTH; a bad parent or a run longer than max_cand -> JCA_STATUS_BAD_TREE.
+ * No workspace. The outputs overlap no input.
  * ------------------------------------------------------------------------------------------- */
 int cand_tree_attn_fwd(const void* cand_q, const void* own_k, const void* own_v,
                        const void* cand_offsets, const int32_t* parent, const void* hist_k,
