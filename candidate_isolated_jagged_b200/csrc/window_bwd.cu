@@ -30,7 +30,8 @@
 //   warps 12..15 write a unit's accumulators out while the others are at the next unit.
 //
 // What bounds it (256 users, window 256, d = 128: dKV 437 us, dQ 373, first tokens 118; 0.33 of the copy
-// bandwidth with the statistics before and the joining behind): the tensor core's part of the
+// bandwidth with the statistics before and the joining behind; a tenth longer under the power limit of
+// a long run): the tensor core's part of the
 // chain S, dP -> dS -> products. Seven products are formed per pair instead of five (S and dP in both
 // passes), and those of 64 columns take nearly as long as those of 128 (about 60 cycles for 16 of
 // the head) but leave room for three score buffers, which overlap the exponentials and conversions
@@ -781,6 +782,7 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& tmO1, const CUtenso
 // by side (16 users 16 us; three launches 38 us), and a large one's blocks of the next part start
 // where blocks of the one before end (256 users 919 us, one after the other 928 us). First tokens
 // come first: behind the others a few blocks would take all their units in a row (16 users 43 us).
+// Blocks of dKV and dQ in turn, to share tiles in L2, took 25 and 958 us.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     window_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmDO,
