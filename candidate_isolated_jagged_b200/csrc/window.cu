@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(128)
                        int32_t* __restrict__ row_start, int32_t* __restrict__ row_end,
                        int32_t* __restrict__ row_user, int32_t* counters, int n_counters,
                        int32_t* status) {
+  grid_dep_launch();
   if (blockIdx.x == 0 && blockIdx.y == 0 && (int)threadIdx.x < n_counters) counters[threadIdx.x] = 0;
   if (*status != 0) return;
   for (int64_t b = blockIdx.x; b < B; b += gridDim.x) {
@@ -680,7 +681,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* skip = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    *skip = *a.status != 0;   // an error recorded earlier makes the launch a no-op
     for (int i = 0; i < C::NUM_BARS; ++i) {
       uint32_t n = 1;
       if (i >= C::B_KEMPTY && i < C::B_KEMPTY + C::KVS) n = 2;   // both MMA threads
@@ -708,6 +708,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
     tc_fence_before();
   }
+  grid_dep_wait();
+  if (threadIdx.x == 0) *skip = *a.status != 0;   // an error recorded earlier makes the launch a no-op
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -757,8 +759,7 @@ int launch_fwd(FwdArgs a, const void* q, const void* k, const void* v, int Hkv, 
       !make_strided_map_bf16(&tmV, v, a.T, Hkv, D, vs, C::BN))
     return JCA_ERR_CUDA;
   const int grid = a.n_items < sms ? a.n_items : sms;
-  window_fwd_kernel<D><<<grid, kThreads, C::SMEM_ALLOC, st>>>(tmQ, tmK, tmV, a);
-  return cudaGetLastError() == cudaSuccess ? JCA_OK : JCA_ERR_CUDA;
+  return launch_dependent(window_fwd_kernel<D>, grid, kThreads, C::SMEM_ALLOC, st, tmQ, tmK, tmV, a);
 }
 
 struct FwdLayout {

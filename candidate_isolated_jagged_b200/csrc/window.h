@@ -4,6 +4,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "jca.h"
+
 namespace jca {
 
 constexpr int kWindowMaxSinks = 128;   // the visible first tokens of a user fit one key tile
@@ -19,5 +21,35 @@ int window_check(int64_t B, int64_t T, int H, int Hkv, int d, int64_t window, in
 int window_plan(const void* offsets, int64_t B, int64_t T, int idx_bits, int32_t* row_start,
                 int32_t* row_end, int32_t* row_user, int32_t* counters, int n_counters,
                 int32_t* status, cudaStream_t st);
+
+// The kernels of a call follow one another by programmatic dependent launch: a kernel's blocks may be
+// placed, and its barriers and TMEM set up, while the kernel before still runs. Every thread of a
+// dependent kernel waits (grid_dep_wait) before its first access to global memory, until the kernel
+// before is complete and its writes are visible; since that kernel waited for its own predecessor,
+// the whole chain is then complete. A call's first kernel is launched in the ordinary way, behind
+// everything that the stream held.
+__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the dependent kernel's blocks be placed once every block here has got this far.
+__device__ __forceinline__ void grid_dep_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <typename... Params, typename... Args>
+int launch_dependent(void (*kernel)(Params...), int grid, int threads, size_t smem, cudaStream_t st,
+                     const Args&... args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, Params(args)...) == cudaSuccess) return JCA_OK;
+  cudaGetLastError();
+  return JCA_ERR_CUDA;
+}
 
 }  // namespace jca

@@ -715,7 +715,6 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& tmO1, const CUtenso
   volatile int* skip = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    *skip = *a.status != 0;   // an error recorded earlier makes the launch a no-op
     for (int i = 0; i < C::NUM_BARS; ++i) {
       uint32_t n = 1;
       if (i >= C::B_DSFULL && i < C::B_DSFULL + C::BUFS) n = kCompute;
@@ -741,6 +740,8 @@ __device__ __forceinline__ void bwd_block(const CUtensorMap& tmO1, const CUtenso
     tmem_relinquish();
     tc_fence_before();
   }
+  grid_dep_wait();
+  if (threadIdx.x == 0) *skip = *a.status != 0;   // an error recorded earlier makes the launch a no-op
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -805,6 +806,8 @@ __global__ void __launch_bounds__(256)
                        const IdxT* __restrict__ off, int64_t B, int window, int4* sinks,
                        int4* sink_users, int32_t* n_sink_units, int32_t* n_sink_users,
                        const int32_t* status) {
+  grid_dep_launch();
+  grid_dep_wait();
   if (*status != 0) return;
   constexpr int L = D / 8;
   const int64_t n = (int64_t)T * H;
@@ -848,6 +851,7 @@ __global__ void __launch_bounds__(256)
 // order. One block per user and key head, four elements a thread.
 template <int D>
 __global__ void __launch_bounds__(256) window_join_kernel(const BwdArgs a) {
+  grid_dep_wait();
   if (*a.status != 0) return;
   const int64_t n = *a.n_sink_users;
   for (int64_t x = blockIdx.x; x < n * a.Hkv; x += gridDim.x) {
@@ -925,8 +929,7 @@ int launch_parts(BwdArgs a, const Maps& m, int64_t sink_units, int dev, int sms,
   a.blocks_sink = (int)std::min<int64_t>(sink_units, sms);
   a.blocks_dkv = std::min(a.units_dkv, sms);
   const int grid = a.blocks_sink + a.blocks_dkv + std::min(a.units_dq, sms);
-  window_bwd_kernel<D><<<grid, kThreads, kBytes, st>>>(m.q, m.dout, m.k, m.v, a);
-  return cudaGetLastError() == cudaSuccess ? JCA_OK : JCA_ERR_CUDA;
+  return launch_dependent(window_bwd_kernel<D>, grid, kThreads, kBytes, st, m.q, m.dout, m.k, m.v, a);
 }
 
 template <int D>
@@ -944,24 +947,25 @@ int launch_bwd(BwdArgs a, const void* q, const void* k, const void* v, const voi
   const int64_t want = ((int64_t)a.T * a.H * (D / 8) + 255) / 256;
   const int grid = (int)(want < (int64_t)sms * 16 ? want : (int64_t)sms * 16);
   const bf16 *o = static_cast<const bf16*>(out), *g = static_cast<const bf16*>(dout);
+  int rc;
   if (idx_bits == 32)
-    window_prep_kernel<D, int32_t><<<grid, 256, 0, st>>>(
-        o, g, lse, a.valid, a.T, a.H, lse2, dsum, static_cast<const int32_t*>(offsets), B, a.window,
-        sinks, sink_users, n_sinks, n_sinks + 1, a.status);
+    rc = launch_dependent(window_prep_kernel<D, int32_t>, grid, 256, 0, st, o, g, lse, a.valid, a.T,
+                          a.H, lse2, dsum, static_cast<const int32_t*>(offsets), B, a.window, sinks,
+                          sink_users, n_sinks, n_sinks + 1, a.status);
   else
-    window_prep_kernel<D, int64_t><<<grid, 256, 0, st>>>(
-        o, g, lse, a.valid, a.T, a.H, lse2, dsum, static_cast<const int64_t*>(offsets), B, a.window,
-        sinks, sink_users, n_sinks, n_sinks + 1, a.status);
-  if (cudaGetLastError() != cudaSuccess) return JCA_ERR_CUDA;
+    rc = launch_dependent(window_prep_kernel<D, int64_t>, grid, 256, 0, st, o, g, lse, a.valid, a.T,
+                          a.H, lse2, dsum, static_cast<const int64_t*>(offsets), B, a.window, sinks,
+                          sink_users, n_sinks, n_sinks + 1, a.status);
+  if (rc) return rc;
   const int tiles = (a.T + kTileM - 1) / kTileM;
   a.units_dq = tiles * a.H;
   a.units_dkv = tiles * a.Hkv;
   // The list of kSink units is counted on the device; no more than this.
-  const int rc = launch_parts<D>(a, m, sinks ? slots * a.Hkv : 0, dev, sms, st);
+  rc = launch_parts<D>(a, m, sinks ? slots * a.Hkv : 0, dev, sms, st);
   if (rc || !sinks) return rc;
   const int64_t most = B * a.Hkv;
-  window_join_kernel<D><<<(int)(most < (int64_t)sms * 64 ? most : sms * 64), 256, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? JCA_OK : JCA_ERR_CUDA;
+  return launch_dependent(window_join_kernel<D>, (int)(most < (int64_t)sms * 64 ? most : sms * 64), 256,
+                          0, st, a);
 }
 
 }  // namespace
