@@ -16,8 +16,8 @@
 // Angles are counted in turns, in 64-bit fixed point: theta / 2 pi is an integer multiple of 2^-64 (the
 // host rounds it from extended precision), and the position times that integer, wrapped to 64 bits,
 // is the fraction of the turn, whatever the position: one integer product in place of a chain of fp64
-// operations and their reduction (a third of the time on the 256-user batch), off by at most 2^-65
-// of a turn per unit of position, 2^-34 at a position of 2^31 (seconds since an epoch), where an
+// operations and their reduction (a third of the time on the 256-user batch), off by at most 2^-61
+// of a turn per unit of position, 2^-30 at a position of 2^31 (seconds since an epoch), where an
 // fp64 product would be off by 2^-22 of a radian. The nearest quarter turn is split off and the
 // remainder in [-1/8, 1/8] turns goes to fp32 series for sine and cosine: its rounding there is at
 // most 2^-24, where that of a whole half turn would be four times as much. The rotation is fp32, rounded once to the element type; pairs past the sections keep their bits.
@@ -316,13 +316,25 @@ int rope_axes(const void* q, const void* k, void* q_out, void* k_out, const void
   a.sign = sign;
   const long double log2_base = log2l((long double)base);
   const long double inv_2pi = 0.159154943091895335768883763372514362L;
+  // Frequency i of n is base^(-i / n): the product of those of i's bits, so that a call pays for a few
+  // exponentials instead of one per pair (they were half of its time on the host). Six factors
+  // and products, each off by at most 2^-63 of its value, and a first frequency of 1 / 2 pi turns.
+  long double freq[64], power[6];
+  auto frequencies = [&](int n, int count) {
+    for (int b = 0; b < 6 && (1 << b) < count; ++b)
+      power[b] = exp2l(-log2_base * (1 << b) / n);
+    freq[0] = ldexpl(inv_2pi, 64);
+    for (int i = 1; i < count; ++i) freq[i] = freq[i & (i - 1)] * power[__builtin_ctz(i)];
+  };
+  if (!per_axis) frequencies(half, (int)sum);
   int j = 0;
-  for (int ax = 0; ax < n_axes; ++ax)
+  for (int ax = 0; ax < n_axes; ++ax) {
+    if (per_axis) frequencies(sections[ax], sections[ax]);
     for (int i = 0; i < sections[ax]; ++i, ++j) {
-      const long double e = per_axis ? (long double)i / sections[ax] : (long double)j / half;
-      a.turns[j] = (uint64_t)roundl(ldexpl(exp2l(-e * log2_base) * inv_2pi, 64));
+      a.turns[j] = (uint64_t)(freq[per_axis ? i : j] + 0.5L);
       a.axis[j] = (uint8_t)ax;
     }
+  }
   a.n_turned = j;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (idx_bits == 32) {

@@ -550,7 +550,7 @@ int jca_stack_fwd(const void* x, void* x_out, const void* weights, int n_layers,
  * turns by the angle positions[t, axis] * theta:
  *   per_axis = 0:  theta = base^(-2 j / d_head), one row of frequencies over the whole head;
  *   per_axis = 1:  theta = base^(-i / sections[axis]) for the i-th pair of its axis.
- * (a, b) -> (a cos - b sin, a sin + b cos). Angles are formed in fixed point (off by at most 2^-65 of a
+ * (a, b) -> (a cos - b sin, a sin + b cos). Angles are formed in fixed point (off by at most 2^-61 of a
  * turn per unit of position), the rotation is fp32 and each result is rounded once to the element
  * type.
  *   q [T, H, d_head] and k [T, Hkv, d_head] of `dtype` (JCA_BF16, JCA_FP16, JCA_FP32), read; k may
