@@ -667,6 +667,12 @@ def _call(fn: str, device, stream, *args) -> int:
     return code if code >= 0 else _check(code, fn)
 
 
+def _clip(x: int, bits: int) -> int:
+    """x, or the nearest integer of that many bits: ctypes would drop the upper ones."""
+    top = 2 ** (bits - 1)
+    return max(-top, min(int(x), top - 1))
+
+
 def _at(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -754,11 +760,11 @@ def jagged_window_attn_fwd(q, k, v, out, offsets, window: int, n_sinks: int = 0,
     _vector("valid", valid, T, torch.uint8, dev)
     _vector("lse", lse, T * H, torch.float32, dev)
     workspace, status = _window_scratch(
-        workspace, status, lambda: jca_window_workspace_bytes(B, T, H, Hkv, d, n_sinks), dev,
-        stream)
+        workspace, status, lambda: jca_window_workspace_bytes(
+            B, T, H, Hkv, d, _clip(n_sinks, 32)), dev, stream)
     return _call("jagged_window_attn_fwd", dev, stream, _at(q), _at(k), _at(v), _at(out), _at(lse),
-                 _at(offsets), _at(valid), B, T, H, Hkv, d, int(window), int(n_sinks), qs, ks, vs,
-                 float(scale), _idx_bits(offsets), _at(workspace),
+                 _at(offsets), _at(valid), B, T, H, Hkv, d, _clip(window, 64), _clip(n_sinks, 32), qs,
+                 ks, vs, float(scale), _idx_bits(offsets), _at(workspace),
                  workspace.numel() * workspace.element_size(), _at(status))
 
 
@@ -780,11 +786,11 @@ def jagged_window_attn_bwd(q, k, v, out, dout, lse, dq, dk, dv, offsets, window:
     _vector("valid", valid, T, torch.uint8, dev)
     _vector("lse", lse, T * H, torch.float32, dev)
     workspace, status = _window_scratch(
-        workspace, status, lambda: jca_window_bwd_workspace_bytes(B, T, H, Hkv, d, n_sinks),
-        dev, stream)
+        workspace, status, lambda: jca_window_bwd_workspace_bytes(
+            B, T, H, Hkv, d, _clip(n_sinks, 32)), dev, stream)
     return _call("jagged_window_attn_bwd", dev, stream, _at(q), _at(k), _at(v), _at(out), _at(dout),
                  _at(lse), _at(dq), _at(dk), _at(dv), _at(offsets), _at(valid), B, T, H, Hkv, d,
-                 int(window), int(n_sinks), qs, ks, vs, float(scale), _idx_bits(offsets),
+                 _clip(window, 64), _clip(n_sinks, 32), qs, ks, vs, float(scale), _idx_bits(offsets),
                  _at(workspace), workspace.numel() * workspace.element_size(), _at(status))
 
 
@@ -808,7 +814,7 @@ def jagged_window_decode_fwd(q, k_new, v_new, k_cache, v_cache, out, cache_offse
     status = _status_on(status, dev, stream)
     return _call("jagged_window_decode_fwd", dev, stream, _at(q), _at(k_new), _at(v_new),
                  _at(k_cache), _at(v_cache), _at(out), _at(cache_offsets), _at(cache_len), B, R, H,
-                 Hkv, d, int(window), int(n_sinks), qs, ks, vs, float(scale),
+                 Hkv, d, _clip(window, 64), _clip(n_sinks, 64), qs, ks, vs, float(scale),
                  _idx_bits(cache_offsets), _at(status))
 
 
@@ -835,7 +841,7 @@ def cand_tree_attn_fwd(cand_q, own_k, own_v, cand_offsets, parent, hist_k, hist_
     status = _status_on(status, dev, stream)
     return _call("cand_tree_attn_fwd", dev, stream, _at(cand_q), _at(own_k), _at(own_v),
                  _at(cand_offsets), _at(parent), _at(hist_k), _at(hist_v), _at(hist_offsets),
-                 _at(hist_len), _at(out), B, N, R, H, Hkv, d, int(max_cand), qs, ks, vs,
+                 _at(hist_len), _at(out), B, N, R, H, Hkv, d, _clip(max_cand, 32), qs, ks, vs,
                  float(scale), _idx_bits(cand_offsets), _at(status))
 
 

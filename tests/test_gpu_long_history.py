@@ -276,6 +276,20 @@ def test_window_captured_and_replayed_with_an_eager_call_between():
     other.check_forward(60, 2)
 
 
+def test_window_numbers_past_the_c_types():
+    b = Window([70, 40], 2, 2, 16, seed=16)
+    b.forward(1 << 70, 0)
+    b.check_forward(1 << 40, 0)
+    with pytest.raises(jca.JcaError):
+        b.forward(20, (1 << 32) + 1)
+    d = Decode([5], [8], 2, 2, 16, seed=16)
+    d.run(1 << 70, 1 << 70)
+    d.check(1 << 40, 1 << 40)
+    t = Tree([3], [9], 2, 2, 16, seed=16)
+    with pytest.raises(jca.JcaError):
+        t.run((1 << 32) + 3)
+
+
 def test_window_two_streams():
     batches = [Window([150, 420, 64], 4, 4, 64, seed=s) for s in (11, 12)]
     torch.cuda.synchronize()

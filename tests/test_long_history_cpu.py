@@ -196,3 +196,8 @@ def test_wrappers_refuse_scratch_of_another_kind(L):
     with pytest.raises(ValueError, match="workspace"):
         jca._window_scratch(torch.zeros(8, 2, dtype=torch.uint8)[:, 0], status, lambda: 0, dev, None)
     assert jca._status_on(status, dev, None) is status
+
+
+def test_integers_past_the_c_types_stay_large(L):
+    assert jca._clip(1 << 70, 64) == 2**63 - 1 and jca._clip((1 << 32) + 1, 32) == 2**31 - 1
+    assert jca._clip(-(1 << 40), 32) == -2**31 and jca._clip(128, 32) == 128
