@@ -836,3 +836,89 @@ def test_layer_of_a_training_step_and_its_serving():
     t.cache[0][: b.T], t.cache[1][: b.T] = kc.cpu(), vc.cpu()
     t.run()
     t.check()
+
+
+# ------------------------------------------------------------------------------------------------
+# Large offsets, threads
+# ------------------------------------------------------------------------------------------------
+
+def test_caches_beyond_32_bit_offsets():
+    """Users at both ends of a cache of more than 2^31 elements, for one token and for trees."""
+    H, d, n, last = 8, 128, 300, 2**21 + 5000
+    R = last + n + 1
+    assert last * H * d > 2**31
+    g = torch.Generator().manual_seed(1)
+    kc, vc = (torch.empty(R, H, d, dtype=torch.bfloat16, device=dev()) for _ in range(2))
+    kh, vh = (torch.randn(2, n, H, d, generator=g).to(torch.bfloat16) for _ in range(2))
+    for c, x in ((kc, kh), (vc, vh)):
+        c[:n], c[last:last + n] = x[0].to(dev()), x[1].to(dev())
+    q, k, v = (torch.randn(6, H, d, generator=g).to(torch.bfloat16) for _ in range(3))
+    st = jca.new_status(dev())
+    off = torch.tensor([0, last, R], device=dev())
+    used = torch.tensor([n, n], device=dev())
+    parent = torch.tensor([-1, 0, 0, -1, 0, 1], dtype=torch.int32, device=dev())
+    out = torch.empty(6, H, d, dtype=torch.bfloat16, device=dev())
+    jca.cand_tree_attn_fwd(q.to(dev()), k.to(dev()), v.to(dev()), torch.tensor([0, 3, 6], device=dev()), parent, kc, vc,
+                           off, out, 3, hist_len=used, status=st)
+    jca.check_status(st)
+    for b, par in enumerate(([-1, 0, 0], [-1, 0, 1])):
+        t = slice(3 * b, 3 * b + 3)
+        ref, _, _, A = lh.masked(q[t], torch.cat([kh[b], k[t]]), torch.cat([vh[b], v[t]]), lh.tree_mask(par, n), d**-0.5)
+        near(out[t], ref, (2.0**-8 + 2.0**-11) * A + 2.0**-8 * np.abs(ref), f"tree {b}")
+    one = torch.empty(2, H, d, dtype=torch.bfloat16, device=dev())
+    jca.jagged_window_decode_fwd(q[:2].to(dev()), k[:2].to(dev()), v[:2].to(dev()), kc, vc, one, off, used, 100, 5,
+                                 status=st)
+    jca.check_status(st)
+    mask = lh.window_mask(n + 1, 100, 5)[-1:]
+    for b, at in enumerate((n, last + n)):
+        assert torch.equal(kc[at].cpu(), k[b]) and torch.equal(vc[at].cpu(), v[b])
+        ref, _, _, A = lh.masked(q[b:b + 1], torch.cat([kh[b], k[b:b + 1]]), torch.cat([vh[b], v[b:b + 1]]), mask, d**-0.5)
+        near(one[b:b + 1], ref, (2.0**-8 + 2.0**-11) * A + 2.0**-8 * np.abs(ref), f"token {b}")
+
+
+def test_rope_rows_beyond_32_bit_offsets():
+    T, H, d = 2**21 + 1001, 8, 128
+    g = torch.Generator(device=dev()).manual_seed(2)
+    q = torch.empty(T, H, d, dtype=torch.bfloat16, device=dev()).normal_(generator=g)
+    pos = torch.randint(-1000, 1 << 40, (T, 2), generator=g, device=dev())
+    ends = [slice(0, 40), slice(T - 40, T)]
+    kept = [q[r].cpu() for r in ends]
+    jca.jca_rope_axes_fwd(q, None, q, None, pos, [40, 24])
+    for r, x in zip(ends, kept):
+        ref = lh.rope_axes(x, pos[r].cpu(), [40, 24])
+        a = np.abs(lh.f64(x))
+        both = np.concatenate([a[..., :64] + a[..., 64:]] * 2, -1)
+        # The angle is off by 2^40 2^-61 turns at most, 2^-18 of a radian.
+        near(q[r], ref, 2.0**-8 * np.abs(ref) + (2.0**-22 + 2.0**-18) * both, f"rows {r}")
+
+
+def test_calls_from_two_threads():
+    """Each thread its own stream, batch and buffers; every operator, first calls included."""
+    import threading
+    wrong = []
+
+    def work(seed):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                w = Window([90, 200 + seed], 4, 2, 32, seed=seed)
+                d = Decode([50, 7], [60, 9], 4, 2, 32, seed=seed)
+                t = Tree([4, 9], [30, 70], 4, 2, 32, seed=seed)
+                for _ in range(4):
+                    w.forward(40, 2)
+                    d.run(30, 2)
+                    t.run()
+                    w.check_forward(40, 2)
+                    w.backward(40, 2)
+                    w.check_backward(40, 2)
+                    d.check(30, 2)
+                    t.check()
+        except BaseException as e:                                  # noqa: BLE001
+            wrong.append(e)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(s,)) for s in (21, 22)]
+    for x in threads:
+        x.start()
+    for x in threads:
+        x.join()
+    assert not wrong, wrong
