@@ -45,7 +45,8 @@ using bf16 = __nv_bfloat16;
 constexpr int kMaxTree = 1024;
 constexpr int kThr = 128;          // threads of a block
 constexpr int kBK = 64;            // keys of a tile
-constexpr int kMaxSplit = 8;       // blocks of a cluster (16: one token 10.8 us too, 4 users with trees 10.9)
+// Blocks of a cluster. (Sixteen: one user's token 10.8 us too, 4 users with trees 10.9 us, not 9.7.)
+constexpr int kMaxSplit = 8;
 constexpr int kTreeWords = kMaxTree / 32;
 constexpr int kGroup = 256;        // users that are put in order together
 
@@ -147,10 +148,11 @@ struct Keys {
 
 // The user that takes place b when the users of each group of 256 go by the length of their history,
 // longest first. Blocks start in the order of their index, so a long history that starts late runs
-// on alone after the others (256 users with trees of 64 tokens, two blocks to an SM: 222 us in the order of the batch, 165 us so).
+// on alone after the others (256 users with trees of 64 tokens, two blocks to an SM: 222 us in the
+// order of the batch, 165 us so).
 // A sort by quarter octaves is close enough and cheap: counts, a scan, the bucket that holds the
 // place, the place's bit among its members. It depends on the lengths only, so all blocks agree
-// whatever the lengths hold. `w`: 128 + 16 words of shared memory.
+// whatever the lengths hold. `w`: 128 + 10 words of shared memory.
 template <typename IdxT>
 __device__ int64_t longest_first(const CacheArgs& a, int64_t b, uint32_t* w) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -195,26 +197,22 @@ __device__ int64_t longest_first(const CacheArgs& a, int64_t b, uint32_t* w) {
     }
   }
   __syncthreads();
-  const int want = (int)w[128];
-  int k = (int)w[129];
+  const int want = (int)w[128], k = (int)w[129];
+  uint32_t mine[kGroup / kThr];   // members of the bucket in this warp's 32 users
 #pragma unroll
   for (int i = 0; i < kGroup / kThr; ++i) {
-    const uint32_t m = __ballot_sync(0xffffffffu, bucket[i] == want);
-    if (lane == 0) w[130 + i * (kThr / 32) + warp] = m;
+    mine[i] = __ballot_sync(0xffffffffu, bucket[i] == want);
+    if (lane == 0) w[130 + i * (kThr / 32) + warp] = __popc(mine[i]);
   }
   __syncthreads();
-  int64_t user = g0;
-  bool found = false;
 #pragma unroll
-  for (int i = 0; i < kGroup / 32; ++i) {
-    const uint32_t m = w[130 + i];
-    const int c = __popc(m);
-    if (!found && k < c) {
-      user = g0 + i * 32 + __fns(m, 0, k + 1);
-      found = true;
-    }
-    k -= c;
+  for (int i = 0; i < kGroup / kThr; ++i) {
+    int before = __popc(mine[i] & ((1u << lane) - 1u));
+    for (int x = 0; x < i * (kThr / 32) + warp; ++x) before += (int)w[130 + x];
+    if (bucket[i] == want && before == k) w[0] = i * kThr + tid;
   }
+  __syncthreads();
+  const int64_t user = g0 + w[0];
   __syncthreads();
   return user;
 }
@@ -646,7 +644,8 @@ __global__ void __launch_bounds__(kThr, CCfg<D, RW, TREE>::BPS) cache_attn_kerne
   }
   const int n4 = rows * D / 4;
   auto store = [&](int i, float4 x) {
-    *reinterpret_cast<uint2*>(out_row(i / (D / 4)) + i % (D / 4) * 4) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+    *reinterpret_cast<uint2*>(out_row(i / (D / 4)) + i % (D / 4) * 4) =
+        make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
   };
   if (a.split == 1) {
     for (int i = tid; i < n4; i += kThr) {

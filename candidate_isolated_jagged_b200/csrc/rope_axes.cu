@@ -20,7 +20,8 @@
 // of a turn per unit of position, 2^-30 at a position of 2^31 (seconds since an epoch), where an
 // fp64 product would be off by 2^-22 of a radian. The nearest quarter turn is split off and the
 // remainder in [-1/8, 1/8] turns goes to fp32 series for sine and cosine: its rounding there is at
-// most 2^-24, where that of a whole half turn would be four times as much. The rotation is fp32, rounded once to the element type; pairs past the sections keep their bits.
+// most 2^-24, where that of a whole half turn would be four times as much. The rotation is fp32,
+// rounded once to the element type; pairs past the sections keep their bits.
 #include <climits>
 #include <cmath>
 #include <cstdint>
