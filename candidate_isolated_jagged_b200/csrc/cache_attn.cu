@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kThr, CCfg<D, RW, TREE>::BPS) cache_attn_kerne
     k.base2 = s + lo;
     k.own = b;
     k.n_own = 1;
-    nt = (k.n1 + k.n2 + 1 + kBK - 1) / kBK;
+    nt = (k.n1 + k.n2) / kBK + 1;   // of n1 + n2 + 1 keys; rounding up would pass 2^31 on the longest
     // The new token's key and value go behind the cached ones; no block reads them from there.
     if (rank == 0 && rb == 0 && !skip && tid < 2 * C::CH) {
       const int c = tid % C::CH;
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kThr, CCfg<D, RW, TREE>::BPS) cache_attn_kerne
       }
     } else {
       const int x0 = t * kBK, cached = k.n1 + k.n2;
-      if (x0 >= k.n1 && x0 + kBK <= cached) {
+      if (x0 >= k.n1 && cached - x0 >= kBK) {
         load_run(st, k.base2 + (x0 - k.n1), kBK);
         return;
       }

@@ -922,3 +922,40 @@ def test_calls_from_two_threads():
     for x in threads:
         x.join()
     assert not wrong, wrong
+
+
+def test_longest_list_of_keys():
+    """A list of 2^31 - 2 keys, the longest that is accepted: one token and one draft over a history of
+    which four rows, the first and the last of the cache among them, hold nearly all the weight."""
+    d, R = 16, 2**31 - 2
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 4 * R * d + (4 << 30):
+        pytest.skip("two caches of 2^35 elements need 138 GB")
+    kc, vc = (torch.zeros(R, 1, d, dtype=torch.bfloat16, device=dev()) for _ in range(2))
+    g = torch.Generator().manual_seed(3)
+    rows = [0, 2**30 + 17, R - 2]
+    v = torch.randn(5, 1, d, generator=g).to(torch.bfloat16)
+    for i, r in enumerate(rows):
+        kc[r], vc[r] = 10.0, v[i].to(dev())
+    q = torch.ones(1, 1, d, dtype=torch.bfloat16, device=dev())
+    kn, out, st = 10.0 * q, torch.full_like(q, float("nan")), jca.new_status(dev())
+    off, n = torch.tensor([0, R], device=dev()), torch.tensor([R - 1], device=dev())
+    # Scores 40 for the four, 0 for the rest, whose values are 0.
+    heavy = np.exp(40.0)
+
+    def check(x):
+        want = heavy * lh.f64(x).sum(0) / (len(x) * heavy + R - len(x))
+        A = heavy * np.abs(lh.f64(x)).sum(0) / (len(x) * heavy)
+        near(out[0], want, (2.0**-8 + 2.0**-11) * A + 2.0**-8 * np.abs(want), f"{len(x)} rows")
+
+    jca.jagged_window_decode_fwd(q, kn, v[3:4].to(dev()), kc, vc, out, off, n, 1 << 40, 0, status=st)
+    jca.check_status(st)
+    check(v[:4])
+    assert bool((kc[R - 1] == 10.0).all()) and torch.equal(vc[R - 1].cpu(), v[3])
+    out.fill_(float("nan"))
+    jca.cand_tree_attn_fwd(q, kn, v[4:].to(dev()), torch.tensor([0, 1], device=dev()),
+                           torch.tensor([-1], dtype=torch.int32, device=dev()), kc, vc, off, out, 1, status=st)
+    jca.check_status(st)
+    check(v)                                       # the new row of the cache among them
+    del kc, vc
+    torch.cuda.empty_cache()
