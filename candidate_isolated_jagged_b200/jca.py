@@ -11,6 +11,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
+import operator
 import os
 import re
 from typing import Optional
@@ -678,8 +679,12 @@ def _at(t: Optional[torch.Tensor]):
 
 
 @functools.lru_cache(maxsize=64)
+def _section_array(sections):
+    return (c_i32 * len(sections))(*(_clip(x, 32) for x in sections))
+
+
 def _sections(sections):
-    return (c_i32 * len(sections))(*sections)
+    return _section_array(tuple(map(operator.index, sections)))
 
 
 def _rope_axes(fn, q, k, q_out, k_out, positions, sections, base, per_axis, stream) -> int:
@@ -702,7 +707,7 @@ def _rope_axes(fn, q, k, q_out, k_out, positions, sections, base, per_axis, stre
                          f"{list(positions.shape)}")
     if positions.device != dev:
         raise ValueError(f"positions is on {positions.device}, not on {dev}")
-    sec = _sections(tuple(sections))
+    sec = _sections(sections)
     return _call(fn, dev, stream, _at(q), _at(k), _at(q_out), _at(k_out), _at(positions), sec,
                  n_axes, int(bool(per_axis)), T, H, Hkv, d, qs, ks, qo, ko, float(base),
                  _ROPE_TYPES[dtype], _idx_bits(positions))

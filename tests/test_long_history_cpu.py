@@ -201,3 +201,19 @@ def test_wrappers_refuse_scratch_of_another_kind(L):
 def test_integers_past_the_c_types_stay_large(L):
     assert jca._clip(1 << 70, 64) == 2**63 - 1 and jca._clip((1 << 32) + 1, 32) == 2**31 - 1
     assert jca._clip(-(1 << 40), 32) == -2**31 and jca._clip(128, 32) == 128
+
+
+def test_section_counts_past_32_bits_are_refused(L):
+    """ctypes alone would drop the upper bits and rotate by other sections."""
+    for given, kept in (((2**32 + 4, 3), (2**31 - 1, 3)), ((-(2**32) + 4,), (-2**31,)),
+                        ((1 << 70, 1), (2**31 - 1, 1)), ((3, 2, 2), (3, 2, 2))):
+        assert tuple(jca._sections(given)) == kept
+    call = _caller(L.jca_rope_axes_fwd, q=P, k=None, qo=P, ko=None, pos=P, sec=None, n_axes=2, per_axis=0,
+                   T=5, H=4, Hkv=0, d=16, qs=64, ks=0, qos=64, kos=0, base=10000.0, dtype=0, idx_bits=64,
+                   stream=None)
+    assert call(sec=jca._sections((2**32 + 4, 3))) == -2
+    assert call(sec=jca._sections((4, -(2**32) + 3))) == -2
+    assert tuple(jca._sections([8])) == (8,)
+    for bad in (2.5, 8.0, "8", None):   # 8.0 too, although it equals an accepted number
+        with pytest.raises(TypeError):
+            jca._sections((bad,))
