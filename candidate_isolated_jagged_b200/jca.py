@@ -730,13 +730,17 @@ def jca_rope_axes_bwd(dq_out, dk_out, dq, dk, positions, sections, base: float =
                       per_axis, stream)
 
 
+def _window_sizes(B, T, H, Hkv, d_head, n_sinks):
+    return (_clip(B, 64), _clip(T, 64), *(_clip(x, 32) for x in (H, Hkv, d_head, n_sinks)))
+
+
 def jca_window_workspace_bytes(B: int, T: int, H: int, Hkv: int, d_head: int, n_sinks: int) -> int:
-    return int(lib().jca_window_workspace_bytes(B, T, H, Hkv, d_head, n_sinks))
+    return int(lib().jca_window_workspace_bytes(*_window_sizes(B, T, H, Hkv, d_head, n_sinks)))
 
 
 def jca_window_bwd_workspace_bytes(B: int, T: int, H: int, Hkv: int, d_head: int,
                                    n_sinks: int) -> int:
-    return int(lib().jca_window_bwd_workspace_bytes(B, T, H, Hkv, d_head, n_sinks))
+    return int(lib().jca_window_bwd_workspace_bytes(*_window_sizes(B, T, H, Hkv, d_head, n_sinks)))
 
 
 def _window_scratch(workspace, status, nbytes, dev, stream):
@@ -766,7 +770,7 @@ def jagged_window_attn_fwd(q, k, v, out, offsets, window: int, n_sinks: int = 0,
     _vector("lse", lse, T * H, torch.float32, dev)
     workspace, status = _window_scratch(
         workspace, status, lambda: jca_window_workspace_bytes(
-            B, T, H, Hkv, d, _clip(n_sinks, 32)), dev, stream)
+            B, T, H, Hkv, d, n_sinks), dev, stream)
     return _call("jagged_window_attn_fwd", dev, stream, _at(q), _at(k), _at(v), _at(out), _at(lse),
                  _at(offsets), _at(valid), B, T, H, Hkv, d, _clip(window, 64), _clip(n_sinks, 32), qs,
                  ks, vs, float(scale), _idx_bits(offsets), _at(workspace),
@@ -792,7 +796,7 @@ def jagged_window_attn_bwd(q, k, v, out, dout, lse, dq, dk, dv, offsets, window:
     _vector("lse", lse, T * H, torch.float32, dev)
     workspace, status = _window_scratch(
         workspace, status, lambda: jca_window_bwd_workspace_bytes(
-            B, T, H, Hkv, d, _clip(n_sinks, 32)), dev, stream)
+            B, T, H, Hkv, d, n_sinks), dev, stream)
     return _call("jagged_window_attn_bwd", dev, stream, _at(q), _at(k), _at(v), _at(out), _at(dout),
                  _at(lse), _at(dq), _at(dk), _at(dv), _at(offsets), _at(valid), B, T, H, Hkv, d,
                  _clip(window, 64), _clip(n_sinks, 32), qs, ks, vs, float(scale), _idx_bits(offsets),

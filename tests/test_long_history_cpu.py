@@ -217,3 +217,14 @@ def test_section_counts_past_32_bits_are_refused(L):
     for bad in (2.5, 8.0, "8", None):   # 8.0 too, although it equals an accepted number
         with pytest.raises(TypeError):
             jca._sections((bad,))
+
+
+def test_workspace_sizes_of_numbers_past_the_c_types(L):
+    """0, as for other sizes that the calls refuse, and not the size of what the lower bits hold."""
+    for f in (jca.jca_window_workspace_bytes, jca.jca_window_bwd_workspace_bytes):
+        assert f(3, 20, 4, 2, 16, 2) > 0
+        wide = 1 << 32
+        for args in ((3 + (1 << 64), 20, 4, 2, 16, 2), (3, 20 + (1 << 64), 4, 2, 16, 2), (3, 20, 4 + wide, 2, 16, 2),
+                     (3, 20, 4, 2 + wide, 16, 2), (3, 20, 4, 2, 16 + wide, 2), (3, 20, 4, 2, 16, 2 + wide),
+                     (3, 20, 4, 2, 16, 2 - wide)):
+            assert f(*args) == 0, args
