@@ -600,8 +600,14 @@ int jca_rope_axes_bwd(const void* dq_out, const void* dk_out, void* dq, void* dk
  *   scale    <= 0 selects 1/sqrt(d_head). H a multiple of Hkv.
  *   workspace >= jca_window_workspace_bytes(...) bytes, 256-byte aligned, no part of it needs to
  *            start at zero. Calls that may overlap on the GPU need a workspace each.
- * The outputs overlap no input. A real token's q, k and v are finite: an Inf or NaN there may reach
- * other rows of its tile of 128 rows, those of a neighbouring user among them.
+ * The outputs overlap no input.
+ * A real token's q, k and v are finite. An Inf or NaN in q stays in its own row and one in k in the
+ * rows that see it, but one in v may also reach rows that do not see it, those of other users
+ * included, since a weight of 0 times Inf or NaN is NaN: every row of a tile that reads it. Tile n is
+ * packed rows [a, a + 128), a = 128 n; with s the first row of row a's user it reads the rows from
+ * max(s, a - window + 1) to a + 127 and the first tokens [s, s + n_sinks), each with up to 127 rows
+ * before and behind. A token thus reaches rows from 127 before it to window + 253 behind it, and near a
+ * user's first tokens (up to 127 rows away) every tile that starts inside that user.
  * Device errors: bad offsets -> JCA_STATUS_BAD_OFFSETS (nothing is written then);
  * JCA_STATUS_TIMEOUT.
  * ------------------------------------------------------------------------------------------- */
@@ -622,6 +628,12 @@ int jagged_window_attn_fwd(const void* q, const void* k, const void* v, void* ou
  *   padding may hold anything in out, dout and lse too).
  *   dq [T, H, d_head], dk and dv [T, Hkv, d_head] bf16, packed, written: every row, 0 for padding.
  *   workspace >= jca_window_bwd_workspace_bytes(...) bytes, 256-byte aligned.
+ * Real tokens are finite here too. An Inf or NaN in v stays in the gradients that it enters; one in k
+ * may reach dq of all rows of the tiles that read it as above; one in q, dout, out or lse may reach dk
+ * and dv of all rows of the tiles among whose query rows it is: those of tile [a, a + 128), whose last
+ * row's user ends before row e, are the rows from a on before min(e, a + 127 + window), and up to 63
+ * behind; those of the first tokens of a user [s, e) longer than the window are the rows [s + window,
+ * e), and up to 63 before and behind.
  * Other arguments and errors as the forward. */
 size_t jca_window_bwd_workspace_bytes(int64_t B, int64_t T, int H, int Hkv, int d_head, int n_sinks);
 

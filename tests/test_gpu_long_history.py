@@ -959,3 +959,81 @@ def test_longest_list_of_keys():
     check(v)                                       # the new row of the cache among them
     del kc, vc
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------------------------------------
+# Reach of a real token that is not finite
+# ------------------------------------------------------------------------------------------------
+
+def _tile_reads(off, window, sinks):
+    """[T, T]: row i lies in a query tile that reads row r, by include/jca.h."""
+    T = int(off[-1])
+    start = np.repeat(off[:-1], np.diff(off))
+    r, got = np.arange(T), np.zeros((T, T), bool)
+    for a in range(0, T, 128):
+        s = int(start[a])
+        got[a:a + 128] = (r >= max(s, a - window + 1) - 127) & (r < a + 128)
+        if sinks:
+            got[a:a + 128] |= (r >= s - 127) & (r < s + sinks + 127)
+    return got
+
+
+def _tile_queries(off, window, sinks):
+    """[T, T]: query row r is among those that key row j's gradients are formed with."""
+    T = int(off[-1])
+    end = np.repeat(off[1:], np.diff(off))
+    r, got = np.arange(T), np.zeros((T, T), bool)
+    for a in range(0, T, 128):
+        last = min(a + 128, T) - 1
+        got[a:a + 128] = (r >= a) & (r < min(int(end[last]), a + 127 + window) + 63)
+    for s, e in zip(off[:-1], off[1:]):
+        if e - s > window:
+            got[s:min(s + sinks, e)] |= (r >= s + window - 63) & (r < e + 63)
+    return got
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(1024, 0), (1024, 3), (70, 0), (1, 5), (130, 100)])
+def test_window_reach_of_a_token_that_is_not_finite(window, sinks, d):
+    """One row of one user holds NaN or Inf. All rows beyond the stated reach are as without it, bit for
+    bit, and the rows that see it are not finite."""
+    b = Window([100, 1000, 60, 7, 300], 2, 1, d, seed=30)
+    sees = np.zeros((b.T, b.T), bool)
+    for r, mask in b.users(window, sinks):
+        sees[r, r] = mask
+    reads, queries = _tile_reads(b.off_np, window, sinks), _tile_queries(b.off_np, window, sinks)
+    assert (reads | ~sees).all() and (queries | ~sees.T).all()
+    own = np.eye(b.T, dtype=bool)
+
+    def forward(**kw):
+        x = {**dict(q=b.q, k=b.k, v=b.v), **kw}
+        out, lse = torch.empty_like(b.q), torch.empty(b.T, 2, device=dev())
+        jca.jagged_window_attn_fwd(x["q"], x["k"], x["v"], out, b.off, window, sinks, lse=lse, status=b.st)
+        return out, lse
+
+    def backward(**kw):
+        x = {**dict(q=b.q, k=b.k, v=b.v, dout=b.dout), **kw}
+        grads = [torch.empty_like(t) for t in (b.q, b.k, b.v)]
+        jca.jagged_window_attn_bwd(x["q"], x["k"], x["v"], out, x["dout"], lse, *grads, b.off, window, sinks,
+                                   status=b.st)
+        return grads
+
+    out, lse = forward()
+    clean = [out, lse] + backward()
+    jca.check_status(b.st)
+    none = np.zeros_like(own)
+    # Row i of (out, lse, dq, dk, dv) may differ for a bad row r of the input.
+    reach = dict(q=(own, own, own, queries, queries), k=(sees, sees, reads, own, own),
+                 v=(reads, none, sees, own, none), dout=(none, none, own, queries, queries))
+    for name, spread in reach.items():
+        for r in (0, 50, 99, 100, 127, 128, 700, 1099, 1100, 1160, 1166, 1167, b.T - 1):
+            bad = getattr(b, name).clone()
+            bad[r] = float("nan") if r % 2 else float("inf")
+            got = list(forward(**{name: bad}) if name != "dout" else (out, lse)) + backward(**{name: bad})
+            jca.check_status(b.st)
+            for what, x, y, where in zip(("out", "lse", "dq", "dk", "dv"), got, clean, spread):
+                keep = torch.tensor(~where[:, r], device=dev())
+                assert torch.equal(x[keep], y[keep]), f"{name} {r}: {what}"
+            if name == "v":
+                seen = torch.tensor(sees[:, r], device=dev())
+                assert not bool(torch.isfinite(got[0][seen].float()).any())
