@@ -659,9 +659,11 @@ int jagged_window_attn_bwd(const void* q, const void* k, const void* v, const vo
  *     and lies in [0, R]. cache_len[b] = -1 marks an empty slot of the batch: out is 0 there and no
  *     row is written.
  *   window, n_sinks, scale as above, with any n_sinks >= 0.
+ * Rows that a user's token does not see may hold anything; an Inf or NaN in one that it sees reaches
+ * no other user.
  * Device errors, each for its own user, whose rows are then not written while those of other users
- * (some of their heads, too) may be: cache_offsets that fall or leave [0, R] -> JCA_STATUS_BAD_OFFSETS; cache_len[b] < -1, or no room for
- * the new token -> JCA_STATUS_BAD_LENGTH. */
+ * (some of their heads, too) may be: cache_offsets that fall or leave [0, R] ->
+ * JCA_STATUS_BAD_OFFSETS; cache_len[b] < -1, or no room for the new token -> JCA_STATUS_BAD_LENGTH. */
 int jagged_window_decode_fwd(const void* q, const void* k_new, const void* v_new, void* k_cache,
                              void* v_cache, void* out, const void* cache_offsets,
                              const void* cache_len, int64_t B, int64_t R, int H, int Hkv,
@@ -689,7 +691,9 @@ int jagged_window_decode_fwd(const void* q, const void* k_new, const void* v_new
  * Device errors, each for its own user, whose rows are then not written while those of other users
  * (some of their heads, too) may be: bad offsets -> JCA_STATUS_BAD_OFFSETS; hist_len[b] outside its
  * region -> JCA_STATUS_BAD_LENGTH; a bad parent or a run longer than max_cand -> JCA_STATUS_BAD_TREE.
- * No workspace. The outputs overlap no input.
+ * No workspace. The outputs overlap no input. Drafted tokens and history rows are finite: an Inf or NaN
+ * in a drafted token's q or k stays in the rows that see it, but one in its v may reach every token of
+ * its user's run, its descendants or not; it reaches no other user.
  * ------------------------------------------------------------------------------------------- */
 int cand_tree_attn_fwd(const void* cand_q, const void* own_k, const void* own_v,
                        const void* cand_offsets, const int32_t* parent, const void* hist_k,

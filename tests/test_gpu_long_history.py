@@ -1037,3 +1037,41 @@ def test_window_reach_of_a_token_that_is_not_finite(window, sinks, d):
             if name == "v":
                 seen = torch.tensor(sees[:, r], device=dev())
                 assert not bool(torch.isfinite(got[0][seen].float()).any())
+
+
+def test_cache_rows_that_are_not_finite_stay_with_their_user():
+    """Trees: a bad k or q of a drafted token only in the rows that see it, a bad v only in its run, a
+    bad history row only in its user. One token: rows it does not see hold NaN."""
+    for H, Hkv, d in ((2, 2, 64), (8, 2, 128), (40, 2, 32)):
+        b = Tree([5, 70, 9], [30, 130, 65], H, Hkv, d, seed=40)
+        b.run()
+        b.check()
+        clean = b.out.clone()
+        for name, at in (("q", 20), ("k", 20), ("v", 20), ("v", 74), ("hk", 100), ("hv", 31)):
+            x = getattr(b, name)
+            kept = x[at].clone()
+            x[at] = float("nan")
+            b.out.fill_(7.0)
+            b.run()
+            jca.check_status(b.st)
+            x[at] = kept
+            hit = np.zeros(84, bool)
+            if name in "qk":
+                hit[5:75] = lh.tree_mask(b.par[1], 0)[:, 15] if name == "k" else np.arange(70) == 15
+            else:
+                hit[5:75] = True
+            keep = torch.tensor(~hit, device=dev())
+            assert torch.equal(b.out[keep], clean[keep]), (name, at)
+        c = Decode([50, 90, 3], [60, 90 + 1, 9], H, Hkv, d, seed=41)
+        c.run(20, 4)
+        c.check(20, 4)
+        clean = c.out.clone()
+        for x in (c.kc, c.vc):
+            x[4:31] = float("nan")                 # behind user 0's first tokens, before its window
+        c.run(20, 4)
+        assert torch.equal(c.out, clean)
+        c.kc[60 + 80], c.vc[60 + 81] = float("nan"), float("inf")
+        c.run(20, 4)
+        jca.check_status(c.st)
+        assert torch.equal(c.out[[0, 2]], clean[[0, 2]])
+        assert not bool(torch.isfinite(c.out[1].float()).any())
