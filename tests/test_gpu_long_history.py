@@ -1075,3 +1075,109 @@ def test_cache_rows_that_are_not_finite_stay_with_their_user():
         jca.check_status(c.st)
         assert torch.equal(c.out[[0, 2]], clean[[0, 2]])
         assert not bool(torch.isfinite(c.out[1].float()).any())
+
+
+# ------------------------------------------------------------------------------------------------
+# Users with bad data beside good ones: nothing of theirs is written, nothing of the others is wrong
+# ------------------------------------------------------------------------------------------------
+
+def _right_or_unwritten(got, want, rows, fill, what):
+    """Head by head, since the blocks of a user see the status at different times."""
+    same = (got == want).all(2) | (got == fill).all(2)
+    assert bool(same[rows].all()), what
+
+
+def _bits(x):
+    return x.view(torch.int16)
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(2, 2, 16), (16, 2, 128), (40, 1, 64)])
+def test_decode_bad_users_write_nothing(H, Hkv, d):
+    """A cache_len that fills its region would append to the next user's first row."""
+    rng = np.random.default_rng(H)
+    for B in (3, 400):
+        lens = [int(x) for x in rng.integers(0, 90, B)]
+        lens[:3] = [5, 8, 7]
+        caps = [n + 1 + int(x) for n, x in zip(lens, rng.integers(0, 3, B))]
+        b = Decode(lens, caps, H, Hkv, d, seed=B)
+        kc, vc = b.kc.clone(), b.vc.clone()
+        for name, at, x, code in (("len", 1, caps[1], 1), ("len", 1, caps[1] + 3, 1), ("len", 0, -2, 1),
+                                  ("len", B - 1, 1 << 40, 1), ("off", 0, -8, 2), ("off", B, 1 << 40, 2),
+                                  ("off", B, 0, 2)):
+            bad = at if name == "len" else min(at, B - 1)
+            # The batch with an empty slot in the bad user's place.
+            b.len[bad], kept = -1, int(b.len[bad])
+            b.kc.copy_(kc)
+            b.vc.copy_(vc)
+            b.st.zero_()
+            b.run(30, 2)
+            jca.check_status(b.st)
+            want, wk, wv = b.out.clone(), b.kc.clone(), b.vc.clone()
+            b.len[bad] = kept
+            held = int(getattr(b, name)[at])
+            getattr(b, name)[at] = x
+            b.kc.copy_(kc)
+            b.vc.copy_(vc)
+            b.out.fill_(7.0)
+            b.run(30, 2)
+            torch.cuda.synchronize()
+            what = f"B={B} {name}[{at}]={x}"
+            assert int(b.st.item()) == code, what
+            assert bool((b.out[bad] == 7.0).all()), what
+            rest = torch.arange(B, device=dev()) != bad
+            _right_or_unwritten(b.out, want, rest, 7.0, what)
+            # Cache rows: as before, or with the new token of a good user, head by head.
+            for got, old, new in ((b.kc, kc, wk), (b.vc, vc, wv)):
+                same = (_bits(got) == _bits(old)).all(2) | (_bits(got) == _bits(new)).all(2)
+                assert bool(same.all()), what
+            getattr(b, name)[at] = held
+
+
+def test_decode_falling_offsets_write_nothing_of_their_user():
+    """Users 0 and 2 are good; the region of user 2 then starts inside that of user 0."""
+    b = Decode([5, 6, 7], [8, 8, 8], 2, 2, 16, seed=2)
+    b.off = torch.tensor([0, 8, 4, 24], device=dev())
+    kc, vc = b.kc.clone(), b.vc.clone()
+    b.out.fill_(7.0)
+    b.run(4, 1)
+    torch.cuda.synchronize()
+    assert int(b.st.item()) == 2 and bool((b.out[1] == 7.0).all())
+    for u, first in ((0, 0), (2, 4)):
+        p = b.lens[u]
+        k, v = (torch.cat([x[first:first + p], y[u:u + 1]]) for x, y in ((b.kc_cpu, b.kn_cpu), (b.vc_cpu, b.vn_cpu)))
+        mask = lh.window_mask(p + 1, 4, 1)[-1:]
+        ref, _, _, A = lh.masked(b.q_cpu[u:u + 1], k, v, mask, b.scale)
+        for h in range(2):
+            if bool((b.out[u, h] == 7.0).all()):
+                continue
+            near(b.out[u:u + 1, h], ref[:, h], (2.0**-8 + 2.0**-11) * A[:, h] + 2.0**-8 * np.abs(ref[:, h]) + 1e-30,
+                 f"user {u}")
+    for got, old, new in ((b.kc, kc, b.kn), (b.vc, vc, b.vn)):
+        want = old.clone()
+        want[5], want[11] = new[0], new[2]
+        same = (_bits(got) == _bits(old)).all(2) | (_bits(got) == _bits(want)).all(2)
+        assert bool(same.all())
+
+
+@pytest.mark.parametrize("H,Hkv,d", [(2, 2, 16), (8, 2, 128), (40, 1, 64)])
+def test_tree_bad_users_write_nothing(H, Hkv, d):
+    n = [4, 6, 3]
+    for name, at, x, bad, code in (("parent", 4, 0, [1], 8), ("parent", 6, 3, [1], 8), ("parent", 9, -2, [1], 8),
+                                   ("parent", 0, 1 << 30, [0], 8), ("hl", 1, 31, [1], 1), ("hl", 1, -1, [1], 1),
+                                   ("ho", 3, 1 << 40, [2], 2), ("ho", 0, -1, [0], 2), ("off", 1, 11, [0, 1], None),
+                                   ("off", 0, 1, [0], 2), ("off", 3, 14, [2], 2), ("off", 1, -5, [0, 1], 2)):
+        b = Tree(n, [20, 30, 10], H, Hkv, d, seed=5, hist_len=[20, 30, 10])
+        b.run(6)
+        b.check()
+        want = b.out.clone()
+        getattr(b, name)[at] = x
+        b.out.fill_(7.0)
+        b.run(6)
+        torch.cuda.synchronize()
+        what = f"{name}[{at}]={x}"
+        assert int(b.st.item()) in ((2, 8) if code is None else (code,)), what
+        rows = torch.zeros(13, dtype=torch.bool, device=dev())
+        for u in bad:
+            rows[b.coff[u]:b.coff[u + 1]] = True
+        assert bool((b.out[rows] == 7.0).all()), what
+        _right_or_unwritten(b.out, want, ~rows, 7.0, what)
