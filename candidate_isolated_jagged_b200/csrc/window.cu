@@ -66,8 +66,7 @@ template <typename IdxT>
 __global__ void __launch_bounds__(128)
     window_plan_kernel(const IdxT* __restrict__ off, int64_t B, int64_t T,
                        int32_t* __restrict__ row_start, int32_t* __restrict__ row_end,
-                       int32_t* __restrict__ row_user, int32_t* counters, int n_counters,
-                       int32_t* status) {
+                       int32_t* counters, int n_counters, int32_t* status) {
   grid_dep_launch();
   if (blockIdx.x == 0 && blockIdx.y == 0 && (int)threadIdx.x < n_counters) counters[threadIdx.x] = 0;
   if (*status != 0) return;
@@ -80,7 +79,6 @@ __global__ void __launch_bounds__(128)
     for (long long i = s + blockIdx.y * 128 + threadIdx.x; i < e; i += gridDim.y * 128) {
       row_start[i] = (int32_t)s;
       if (row_end) row_end[i] = (int32_t)e;
-      if (row_user) row_user[i] = (int32_t)b;
     }
   }
 }
@@ -796,19 +794,19 @@ int window_check(int64_t B, int64_t T, int H, int Hkv, int d, int64_t window, in
 }
 
 int window_plan(const void* offsets, int64_t B, int64_t T, int idx_bits, int32_t* row_start,
-                int32_t* row_end, int32_t* row_user, int32_t* counters, int n_counters,
-                int32_t* status, cudaStream_t st) {
+                int32_t* row_end, int32_t* counters, int n_counters, int32_t* status,
+                cudaStream_t st) {
   // About four rows a thread on average, so that a few long users do not wait for one block each.
   const int64_t x = B < (1 << 20) ? B : (1 << 20), share = T / (B * 512);
   const dim3 grid((unsigned)x, (unsigned)(share < 1 ? 1 : share < 256 ? share : 256));
   if (idx_bits == 32)
     window_plan_kernel<int32_t><<<grid, 128, 0, st>>>(static_cast<const int32_t*>(offsets), B, T,
-                                                      row_start, row_end, row_user, counters,
-                                                      n_counters, status);
+                                                      row_start, row_end, counters, n_counters,
+                                                      status);
   else
     window_plan_kernel<int64_t><<<grid, 128, 0, st>>>(static_cast<const int64_t*>(offsets), B, T,
-                                                      row_start, row_end, row_user, counters,
-                                                      n_counters, status);
+                                                      row_start, row_end, counters, n_counters,
+                                                      status);
   return cudaGetLastError() == cudaSuccess ? JCA_OK : JCA_ERR_CUDA;
 }
 
@@ -861,7 +859,7 @@ extern "C" int jagged_window_attn_fwd(const void* q, const void* k, const void* 
   a.out_v8 = aligned(out, 32) ? 1 : 0;
   a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)d_head)) * 1.4426950408889634f;
   rc = window_plan(offsets, B, T, idx_bits, reinterpret_cast<int32_t*>(ws + L.row_start), nullptr,
-                   nullptr, a.counter, 1, status, st);
+                   a.counter, 1, status, st);
   if (rc || T == 0) return rc;
   switch (d_head) {
     case 16: return launch_fwd<16>(a, q, k, v, Hkv, q_stride, k_stride, v_stride, dev, sms, st);

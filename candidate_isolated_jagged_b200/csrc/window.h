@@ -17,11 +17,10 @@ int window_check(int64_t B, int64_t T, int H, int Hkv, int d, int64_t window, in
                  int64_t q_stride, int64_t k_stride, int64_t v_stride, int idx_bits);
 
 // Checks the offsets (JCA_STATUS_BAD_OFFSETS), writes the first row of each row's user and, unless
-// null, one past its last and the user's index, and zeroes the counters. No other check: callers
-// validate first.
+// null, one past its last, and zeroes the counters. No other check: callers validate first.
 int window_plan(const void* offsets, int64_t B, int64_t T, int idx_bits, int32_t* row_start,
-                int32_t* row_end, int32_t* row_user, int32_t* counters, int n_counters,
-                int32_t* status, cudaStream_t st);
+                int32_t* row_end, int32_t* counters, int n_counters, int32_t* status,
+                cudaStream_t st);
 
 // The kernels of a call follow one another by programmatic dependent launch: a kernel's blocks may be
 // placed, and its barriers and TMEM set up, while the kernel before still runs. Every thread of a

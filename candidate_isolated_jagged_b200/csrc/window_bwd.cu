@@ -76,13 +76,14 @@ struct BwdArgs {
   const uint8_t* valid;       // [T] or null
   const int32_t* row_start;   // [T]
   const int32_t* row_end;     // [T]
-  const int32_t* row_user;    // [T], with first tokens
+  const int32_t* row_number;  // [T], for first tokens of users longer than the window: the user's
+                              // place in sink_users
   const float* lse2;          // [H][T] log2 units; +inf: the row sees no key
   const float* dsum;          // [H][T] D
   float* part;                // partials of first tokens [slot][Hkv][n_sinks][2][D]: dV, dK / scale
-  int window_slot;            // slot of the window's own sums: this + user
+  int window_slot;            // slot of the window's own sums: this + the user's place in sink_users
   const int4* sinks;          // kSink units {first row, end, chunk, slot}
-  const int4* sink_users;     // their users {first row, end, user, 0}
+  const int4* sink_users;     // their users {first row, end, slot of the first unit, 0}
   const int32_t* n_sink_units;
   const int32_t* n_sink_users;
   int32_t* counter;           // [3] next unit of each part
@@ -660,7 +661,7 @@ __device__ void epilogue_role(const BwdArgs& a, uint32_t bars, uint32_t tmem,
     } else if (MODE == kDKV && a.part && row_ok) {
       const int start = a.row_start[row];
       if (row - start < a.n_sinks && a.row_end[row] - start > a.window) {
-        const size_t slot = (size_t)a.window_slot + a.row_user[row];
+        const size_t slot = (size_t)a.window_slot + a.row_number[row];
         mine = a.part + ((slot * a.Hkv + u.oh) * a.n_sinks + (row - start)) * 2 * D;
       }
     }
@@ -803,9 +804,9 @@ __global__ void __launch_bounds__(256)
     window_prep_kernel(const bf16* __restrict__ out, const bf16* __restrict__ dout,
                        const float* __restrict__ lse, const uint8_t* __restrict__ valid, int T,
                        int H, float* __restrict__ lse2, float* __restrict__ dsum,
-                       const IdxT* __restrict__ off, int64_t B, int window, int4* sinks,
-                       int4* sink_users, int32_t* n_sink_units, int32_t* n_sink_users,
-                       const int32_t* status) {
+                       const IdxT* __restrict__ off, int64_t B, int window, int n_sinks,
+                       int4* sinks, int4* sink_users, int32_t* row_number, int32_t* n_sink_units,
+                       int32_t* n_sink_users, const int32_t* status) {
   grid_dep_launch();
   grid_dep_wait();
   if (*status != 0) return;
@@ -841,9 +842,11 @@ __global__ void __launch_bounds__(256)
        b += (int64_t)gridDim.x * 256) {
     const int s = (int)off[b], e = (int)off[b + 1];
     if (e - s <= window) continue;
-    sink_users[atomicAdd(n_sink_users, 1)] = make_int4(s, e, (int)b, 0);
-    for (int c = (s + window) / kChunk; c <= (e - 1) / kChunk; ++c)
-      sinks[atomicAdd(n_sink_units, 1)] = make_int4(s, e, c, c + (int)b);
+    const int first = (s + window) / kChunk, chunks = (e - 1) / kChunk - first + 1;
+    const int number = atomicAdd(n_sink_users, 1), slot = atomicAdd(n_sink_units, chunks);
+    sink_users[number] = make_int4(s, e, slot, 0);
+    for (int c = 0; c < chunks; ++c) sinks[slot + c] = make_int4(s, e, first + c, slot + c);
+    for (int i = 0; i < min(n_sinks, e - s); ++i) row_number[s + i] = number;
   }
 }
 
@@ -855,14 +858,15 @@ __global__ void __launch_bounds__(256) window_join_kernel(const BwdArgs a) {
   if (*a.status != 0) return;
   const int64_t n = *a.n_sink_users;
   for (int64_t x = blockIdx.x; x < n * a.Hkv; x += gridDim.x) {
-    const int4 user = a.sink_users[x / a.Hkv];   // {first row, end, user, -}
-    const int hk = (int)(x % a.Hkv), s = user.x, e = user.y, b = user.z;
+    const int64_t number = x / a.Hkv;
+    const int4 user = a.sink_users[number];      // {first row, end, slot of the first unit, -}
+    const int hk = (int)(x % a.Hkv), s = user.x, e = user.y;
     const int c0 = (s + a.window) / kChunk, chunks = (e - 1) / kChunk - c0 + 1;
     const size_t step = (size_t)a.Hkv * a.n_sinks * 2 * D / 4;
     const size_t head = (size_t)hk * a.n_sinks * 2 * D / 4;
     const float4* part = reinterpret_cast<const float4*>(a.part);
-    const float4* own = part + (size_t)(a.window_slot + b) * step + head;
-    part += (size_t)(c0 + b) * step + head;
+    const float4* own = part + (size_t)(a.window_slot + number) * step + head;
+    part += (size_t)user.z * step + head;
     const int keys = min(a.n_sinks, e - s);      // a user may be shorter than the first tokens
     for (int i = threadIdx.x; i < keys * 2 * D / 4; i += 256) {
       float4 v = own[i];
@@ -884,22 +888,23 @@ __global__ void __launch_bounds__(256) window_join_kernel(const BwdArgs a) {
 }
 
 struct BwdLayout {
-  size_t row_start = 0, row_end = 0, row_user = 0, lse2 = 0, dsum = 0, sinks = 0, users = 0,
+  size_t row_start = 0, row_end = 0, row_number = 0, lse2 = 0, dsum = 0, sinks = 0, users = 0,
          part = 0, counters = 0, total = 0;
   int64_t slots = 0, sink_users = 0;   // chunk partials, users that can have any
 };
 
-// Slots of partial sums: chunk index + user index is unique to a (user, chunk) pair, since both never
-// fall from pair to pair and one of them rises.
-BwdLayout bwd_layout(int64_t B, int64_t T, int H, int Hkv, int d, int n_sinks) {
+// Only users longer than the window leave partial sums: at most T / (window + 1) of them. Their rows
+// behind the window are disjoint runs, so that of their (user, chunk) pairs no more than one a user
+// share a chunk with a pair before.
+BwdLayout bwd_layout(int64_t B, int64_t T, int H, int Hkv, int d, int64_t window, int n_sinks) {
   BwdLayout L;
   const size_t t4 = align_up(4 * (size_t)T, 256);
-  if (n_sinks > 0) {
-    L.slots = T / kChunk + 1 + B;
-    L.sink_users = B;
+  if (n_sinks > 0 && window < T) {
+    L.sink_users = std::min(B, T / (window + 1));
+    L.slots = T / kChunk + 1 + L.sink_users;
   }
   L.row_end = t4;
-  L.row_user = 2 * t4;
+  L.row_number = 2 * t4;
   L.lse2 = 3 * t4;
   L.dsum = L.lse2 + align_up(4 * (size_t)T * H, 256);
   L.sinks = L.dsum + align_up(4 * (size_t)T * H, 256);
@@ -936,8 +941,8 @@ template <int D>
 int launch_bwd(BwdArgs a, const void* q, const void* k, const void* v, const void* out,
                const void* dout, const float* lse, const void* offsets, int64_t B, int64_t qs,
                int64_t ks, int64_t vs, int idx_bits, float* lse2, float* dsum, int4* sinks,
-               int4* sink_users, int32_t* n_sinks, int64_t slots, int dev, int sms,
-               cudaStream_t st) {
+               int4* sink_users, int32_t* row_number, int32_t* n_listed, const BwdLayout& L, int dev,
+               int sms, cudaStream_t st) {
   Maps m;
   if (!make_strided_map_bf16(&m.q, q, a.T, a.H, D, qs, kStep) ||
       !make_strided_map_bf16(&m.k, k, a.T, a.Hkv, D, ks, kStep) ||
@@ -950,20 +955,20 @@ int launch_bwd(BwdArgs a, const void* q, const void* k, const void* v, const voi
   int rc;
   if (idx_bits == 32)
     rc = launch_dependent(window_prep_kernel<D, int32_t>, grid, 256, 0, st, o, g, lse, a.valid, a.T,
-                          a.H, lse2, dsum, static_cast<const int32_t*>(offsets), B, a.window, sinks,
-                          sink_users, n_sinks, n_sinks + 1, a.status);
+                          a.H, lse2, dsum, static_cast<const int32_t*>(offsets), B, a.window,
+                          a.n_sinks, sinks, sink_users, row_number, n_listed, n_listed + 1, a.status);
   else
     rc = launch_dependent(window_prep_kernel<D, int64_t>, grid, 256, 0, st, o, g, lse, a.valid, a.T,
-                          a.H, lse2, dsum, static_cast<const int64_t*>(offsets), B, a.window, sinks,
-                          sink_users, n_sinks, n_sinks + 1, a.status);
+                          a.H, lse2, dsum, static_cast<const int64_t*>(offsets), B, a.window,
+                          a.n_sinks, sinks, sink_users, row_number, n_listed, n_listed + 1, a.status);
   if (rc) return rc;
   const int tiles = (a.T + kTileM - 1) / kTileM;
   a.units_dq = tiles * a.H;
   a.units_dkv = tiles * a.Hkv;
   // The list of kSink units is counted on the device; no more than this.
-  rc = launch_parts<D>(a, m, sinks ? slots * a.Hkv : 0, dev, sms, st);
+  rc = launch_parts<D>(a, m, sinks ? L.slots * a.Hkv : 0, dev, sms, st);
   if (rc || !sinks) return rc;
-  const int64_t most = B * a.Hkv;
+  const int64_t most = L.sink_users * a.Hkv;
   return launch_dependent(window_join_kernel<D>, (int)(most < (int64_t)sms * 64 ? most : sms * 64), 256,
                           0, st, a);
 }
@@ -975,8 +980,13 @@ using namespace jca;
 
 extern "C" size_t jca_window_bwd_workspace_bytes(int64_t B, int64_t T, int H, int Hkv, int d_head,
                                                  int n_sinks) {
-  if (!window_sizes_ok(B, T, H, Hkv, n_sinks) || !head_dim_ok(d_head)) return 0;
-  return bwd_layout(B, T, H, Hkv, d_head, n_sinks).total;
+  return jca_window_bwd_workspace_bytes_for(B, T, H, Hkv, d_head, n_sinks, 1);
+}
+
+extern "C" size_t jca_window_bwd_workspace_bytes_for(int64_t B, int64_t T, int H, int Hkv,
+                                                     int d_head, int n_sinks, int64_t window) {
+  if (!window_sizes_ok(B, T, H, Hkv, n_sinks) || !head_dim_ok(d_head) || window < 1) return 0;
+  return bwd_layout(B, T, H, Hkv, d_head, window, n_sinks).total;
 }
 
 extern "C" int jagged_window_attn_bwd(const void* q, const void* k, const void* v, const void* out,
@@ -996,7 +1006,7 @@ extern "C" int jagged_window_attn_bwd(const void* q, const void* k, const void* 
       !aligned(dout, 16) || !aligned(lse, 4) || !aligned(dq, 16) || !aligned(dk, 16) ||
       !aligned(dv, 16) || !aligned(workspace, 256))
     return JCA_ERR_ALIGN;
-  const BwdLayout L = bwd_layout(B, T, H, Hkv, d_head, n_sinks);
+  const BwdLayout L = bwd_layout(B, T, H, Hkv, d_head, window, n_sinks);
   if (workspace_bytes < L.total) return JCA_ERR_WORKSPACE;
   if (B == 0) return JCA_OK;
   int dev = 0, sms = 0;
@@ -1005,7 +1015,7 @@ extern "C" int jagged_window_attn_bwd(const void* q, const void* k, const void* 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
   // A window as long as the batch leaves no row behind it.
-  const bool sinks = n_sinks > 0 && window < T;
+  const bool sinks = L.sink_users > 0;
   BwdArgs a = {};
   a.dq = static_cast<bf16*>(dq);
   a.dk = static_cast<bf16*>(dk);
@@ -1013,7 +1023,8 @@ extern "C" int jagged_window_attn_bwd(const void* q, const void* k, const void* 
   a.valid = valid;
   a.row_start = reinterpret_cast<int32_t*>(ws + L.row_start);
   a.row_end = reinterpret_cast<int32_t*>(ws + L.row_end);
-  a.row_user = reinterpret_cast<int32_t*>(ws + L.row_user);
+  int32_t* row_number = reinterpret_cast<int32_t*>(ws + L.row_number);
+  a.row_number = row_number;
   a.lse2 = reinterpret_cast<float*>(ws + L.lse2);
   a.dsum = reinterpret_cast<float*>(ws + L.dsum);
   a.part = sinks ? reinterpret_cast<float*>(ws + L.part) : nullptr;
@@ -1034,17 +1045,15 @@ extern "C" int jagged_window_attn_bwd(const void* q, const void* k, const void* 
   a.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)d_head);
   a.scale_log2 = a.scale * 1.4426950408889634f;
   rc = window_plan(offsets, B, T, idx_bits, reinterpret_cast<int32_t*>(ws + L.row_start),
-                   reinterpret_cast<int32_t*>(ws + L.row_end),
-                   sinks ? reinterpret_cast<int32_t*>(ws + L.row_user) : nullptr, a.counter, 5,
-                   status, st);
+                   reinterpret_cast<int32_t*>(ws + L.row_end), a.counter, 5, status, st);
   if (rc || T == 0) return rc;
   float* lse2 = reinterpret_cast<float*>(ws + L.lse2);
   float* dsum = reinterpret_cast<float*>(ws + L.dsum);
   int4* list = sinks ? reinterpret_cast<int4*>(ws + L.sinks) : nullptr;
   auto run = [&](auto fn) {
     return fn(a, q, k, v, out, dout, lse, offsets, B, q_stride, k_stride, v_stride, idx_bits, lse2,
-              dsum, list, reinterpret_cast<int4*>(ws + L.users), a.counter + 3, L.slots, dev, sms,
-              st);
+              dsum, list, reinterpret_cast<int4*>(ws + L.users), row_number, a.counter + 3, L, dev,
+              sms, st);
   };
   switch (d_head) {
     case 16: return run(launch_bwd<16>);

@@ -86,6 +86,7 @@ _SIGNATURES = {
                           [c_i64] * 4 + [c_f32, c_i32, c_i32, c_vp]),
     "jca_window_workspace_bytes": (c_sz, [c_i64, c_i64, c_i32, c_i32, c_i32, c_i32]),
     "jca_window_bwd_workspace_bytes": (c_sz, [c_i64, c_i64, c_i32, c_i32, c_i32, c_i32]),
+    "jca_window_bwd_workspace_bytes_for": (c_sz, [c_i64, c_i64, c_i32, c_i32, c_i32, c_i32, c_i64]),
     "jagged_window_attn_fwd": (c_i32, [c_vp] * 7 + [c_i64, c_i64, c_i32, c_i32, c_i32, c_i64, c_i32,
                                                     c_i64, c_i64, c_i64, c_f32, c_i32, c_vp, c_sz,
                                                     c_vp, c_vp]),
@@ -738,9 +739,12 @@ def jca_window_workspace_bytes(B: int, T: int, H: int, Hkv: int, d_head: int, n_
     return int(lib().jca_window_workspace_bytes(*_window_sizes(B, T, H, Hkv, d_head, n_sinks)))
 
 
-def jca_window_bwd_workspace_bytes(B: int, T: int, H: int, Hkv: int, d_head: int,
-                                   n_sinks: int) -> int:
-    return int(lib().jca_window_bwd_workspace_bytes(*_window_sizes(B, T, H, Hkv, d_head, n_sinks)))
+def jca_window_bwd_workspace_bytes(B: int, T: int, H: int, Hkv: int, d_head: int, n_sinks: int,
+                                   window: int = 1) -> int:
+    """Enough for `window` and every longer one; without it for all of them. Many users with many
+    first tokens need far less under a window that few of them exceed."""
+    return int(lib().jca_window_bwd_workspace_bytes_for(
+        *_window_sizes(B, T, H, Hkv, d_head, n_sinks), _clip(window, 64)))
 
 
 def _window_scratch(workspace, status, nbytes, dev, stream):
@@ -796,7 +800,7 @@ def jagged_window_attn_bwd(q, k, v, out, dout, lse, dq, dk, dv, offsets, window:
     _vector("lse", lse, T * H, torch.float32, dev)
     workspace, status = _window_scratch(
         workspace, status, lambda: jca_window_bwd_workspace_bytes(
-            B, T, H, Hkv, d, n_sinks), dev, stream)
+            B, T, H, Hkv, d, n_sinks, window), dev, stream)
     return _call("jagged_window_attn_bwd", dev, stream, _at(q), _at(k), _at(v), _at(out), _at(dout),
                  _at(lse), _at(dq), _at(dk), _at(dv), _at(offsets), _at(valid), B, T, H, Hkv, d,
                  _clip(window, 64), _clip(n_sinks, 32), qs, ks, vs, float(scale), _idx_bits(offsets),

@@ -627,7 +627,9 @@ int jagged_window_attn_fwd(const void* q, const void* k, const void* v, void* ou
  *   out, lse from the forward on the same inputs; dout [T, H, d_head] bf16, packed, read (rows of
  *   padding may hold anything in out, dout and lse too).
  *   dq [T, H, d_head], dk and dv [T, Hkv, d_head] bf16, packed, written: every row, 0 for padding.
- *   workspace >= jca_window_bwd_workspace_bytes(...) bytes, 256-byte aligned.
+ *   workspace >= jca_window_bwd_workspace_bytes_for(..., window) bytes, 256-byte aligned. Users longer
+ *   than the window leave fp32 partial sums of their first tokens there, so a longer window needs
+ *   less; jca_window_bwd_workspace_bytes(...) is enough for every window.
  * Real tokens are finite here too. An Inf or NaN in v stays in the gradients that it enters; one in k
  * may reach dq of all rows of the tiles that read it as above; one in q, dout, out or lse may reach dk
  * and dv of all rows of the tiles among whose query rows it is: those of tile [a, a + 128), whose last
@@ -636,6 +638,9 @@ int jagged_window_attn_fwd(const void* q, const void* k, const void* v, void* ou
  * e), and up to 63 before and behind.
  * Other arguments and errors as the forward. */
 size_t jca_window_bwd_workspace_bytes(int64_t B, int64_t T, int H, int Hkv, int d_head, int n_sinks);
+
+size_t jca_window_bwd_workspace_bytes_for(int64_t B, int64_t T, int H, int Hkv, int d_head,
+                                          int n_sinks, int64_t window);
 
 int jagged_window_attn_bwd(const void* q, const void* k, const void* v, const void* out,
                            const void* dout, const float* lse, void* dq, void* dk, void* dv,

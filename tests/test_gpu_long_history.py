@@ -1181,3 +1181,31 @@ def test_tree_bad_users_write_nothing(H, Hkv, d):
             rows[b.coff[u]:b.coff[u + 1]] = True
         assert bool((b.out[rows] == 7.0).all()), what
         _right_or_unwritten(b.out, want, ~rows, 7.0, what)
+
+
+# ------------------------------------------------------------------------------------------------
+# Workspace of the gradients
+# ------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("lengths,window,sinks", [
+    ([41] * 120, 40, 3),                 # every user one row longer than the window
+    ([2] * 1500, 1, 2), ([1, 2] * 400, 1, 128), ([40, 41] * 60, 40, 5), ([3000], 1, 4),
+    ([300, 0, 513, 2, 256, 257, 90], 256, 7), ([255, 258, 511, 514] * 3, 1, 1), ([20] * 50, 20, 9),
+    ([5, 900, 5], 904, 3), ([5, 900, 5], 910, 3), ([257] * 40, 255, 128)])
+def test_window_gradient_in_the_workspace_of_its_window(lengths, window, sinks):
+    """The size for the window is enough: memory behind it stays as it was, and the gradients equal
+    those with the size for every window."""
+    b = Window(lengths, 4, 2, 32, seed=50)
+    sizes = [jca.jca_window_bwd_workspace_bytes(len(lengths), b.T, 4, 2, 32, sinks, *w) for w in ((window,), ())]
+    assert sizes[0] <= sizes[1]
+    grads = []
+    for n in sizes:
+        ws = torch.full((n + 65536,), 93, dtype=torch.uint8, device=dev())
+        grads.append([x.clone() for x in b.backward(window, sinks, workspace=ws[:n])])
+        torch.cuda.synchronize()
+        assert bool((ws[n:] == 93).all())
+    b.check_backward(window, sinks)
+    for x, y in zip(*grads):
+        assert torch.equal(x, y)
+    with pytest.raises(jca.JcaError):
+        b.backward(window, sinks, workspace=torch.empty(sizes[0] - 1, dtype=torch.uint8, device=dev()))

@@ -228,3 +228,30 @@ def test_workspace_sizes_of_numbers_past_the_c_types(L):
                      (3, 20, 4, 2 + wide, 16, 2), (3, 20, 4, 2, 16 + wide, 2), (3, 20, 4, 2, 16, 2 + wide),
                      (3, 20, 4, 2, 16, 2 - wide)):
             assert f(*args) == 0, args
+
+
+def test_gradient_workspace_is_for_users_longer_than_the_window(L):
+    """Partial sums of first tokens are kept only for users that can be longer than the window."""
+    f = jca.jca_window_bwd_workspace_bytes
+    rows, heads = 10000 * 50, (8, 8, 128)
+    stats = f(10000, rows, *heads, 0)                      # without first tokens
+    part = 8 * 8 * 64 * 128                                # bytes of one user's, or one chunk's, sums
+    assert f(10000, rows, *heads, 64) == L.jca_window_bwd_workspace_bytes(10000, rows, *heads, 64)
+    assert f(10000, rows, *heads, 64) >= stats + 2 * 10000 * part
+    for window, users in ((49, 10000), (99, 5000), (1023, 488), (rows // 2, 1), (rows - 1, 1)):
+        extra = f(10000, rows, *heads, 64, window) - stats
+        slots = 2 * users + rows // 256 + 1
+        assert slots * part <= extra <= slots * (part + 32) + 1024, window
+    for window in (rows, rows + 1, 1 << 62, 1 << 70):
+        assert f(10000, rows, *heads, 64, window) == stats
+    for window in (0, -1, -(1 << 70)):
+        assert f(10000, rows, *heads, 64, window) == 0
+    sizes = [f(700, 40000, 4, 2, 64, 8, w) for w in range(1, 40100, 37)]
+    assert sizes == sorted(sizes, reverse=True)
+
+
+@pytest.mark.parametrize("window", [1, 7, 40])
+def test_gradient_call_refuses_less_than_the_size_for_its_window(L, window):
+    call = _window(L, "bwd")
+    n = jca.jca_window_bwd_workspace_bytes(3, 20, 4, 2, 16, 2, window)
+    assert call(window=window, ws_bytes=n - 1) == -6
