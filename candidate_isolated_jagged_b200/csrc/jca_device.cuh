@@ -60,15 +60,16 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 }
 
 // Wait for the phase of parity `parity` to complete. Returns false, without waiting further,
-// when the CTA is aborting; on a timeout it starts the abort itself and records the status.
+// when the CTA is aborting; on a timeout it starts the abort itself and records the status. A wait
+// that covers more than a pipeline step has a limit of its own.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                          int32_t* status) {
+                                          int32_t* status, uint64_t limit_ns = kWaitTimeoutNs) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
-    if (global_timer_ns() - t0 > kWaitTimeoutNs) {
+    if (global_timer_ns() - t0 > limit_ns) {
       *abort_flag = 1;
       atomicCAS(status, 0, (int32_t)JCA_STATUS_TIMEOUT);
       return false;
@@ -92,13 +93,14 @@ __device__ __forceinline__ bool mbar_try_wait_long(uint32_t bar, uint32_t parity
 }
 
 __device__ __forceinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity,
-                                               volatile int* abort_flag, int32_t* status) {
+                                               volatile int* abort_flag, int32_t* status,
+                                               uint64_t limit_ns = kWaitTimeoutNs) {
   if (mbar_try_wait_long(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
   while (true) {
     if (mbar_try_wait_long(bar, parity)) return true;
     if (*abort_flag) return false;
-    if (global_timer_ns() - t0 > kWaitTimeoutNs) {
+    if (global_timer_ns() - t0 > limit_ns) {
       *abort_flag = 1;
       atomicCAS(status, 0, (int32_t)JCA_STATUS_TIMEOUT);
       return false;

@@ -90,6 +90,7 @@ struct FwdArgs {
   const int32_t* row_start;   // [T]
   int32_t* counter;           // next block to claim
   int32_t* status;
+  uint64_t item_ns;           // limit of the wait for room in the ring, which a block's work frees
   int T, H, group, window, n_sinks, n_items;
   int out_v8;                 // rows can be written with 32-byte stores
   float scale_log2;
@@ -235,7 +236,8 @@ __device__ void claim_role(const FwdArgs& a, Ring r, volatile int* abort_flag, i
         start[i] = a.row_start[min(q0 + 32 * i + lane, a.T - 1)];
     }
     const int s = (int)(r.k % kRing);
-    const bool ok = mbar_wait_long(r.empty + 8 * s, ((r.k / kRing) & 1) ^ 1, abort_flag, a.status);
+    const bool ok = mbar_wait_long(r.empty + 8 * s, ((r.k / kRing) & 1) ^ 1, abort_flag, a.status,
+                                   a.item_ns);
     if (!__all_sync(0xffffffffu, ok)) return;
     volatile int* e = r.slot + kEntry * s;
     if (lane == 0) e[0] = q0;
@@ -855,6 +857,7 @@ extern "C" int jagged_window_attn_fwd(const void* q, const void* k, const void* 
   a.group = H / Hkv;
   a.window = (int)(window < T ? window : (T > 0 ? T : 1));
   a.n_sinks = n_sinks;
+  a.item_ns = kWaitTimeoutNs + 20000ull * (uint64_t)(T / kTileN + 3);   // a key tile takes 2 us
   a.n_items = (int)((T + kItemRows - 1) / kItemRows) * H;
   a.out_v8 = aligned(out, 32) ? 1 : 0;
   a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)d_head)) * 1.4426950408889634f;

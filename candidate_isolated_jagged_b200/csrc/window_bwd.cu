@@ -88,6 +88,10 @@ struct BwdArgs {
   const int32_t* n_sink_users;
   int32_t* counter;           // [3] next unit of each part
   int32_t* status;
+  // Limit of the waits for a whole unit (the epilogue's, and that for room in the ring): the other
+  // waits are for one step, and an abort there ends these too. 10 us a step of the longest unit; a
+  // step takes 0.8 to 1.
+  uint64_t unit_ns;
   int T, H, Hkv, group, window, n_sinks;
   int units_dq, units_dkv;
   int blocks_sink, blocks_dkv;   // the launch's blocks in this order, those of kDQ last
@@ -263,7 +267,7 @@ __device__ void claim_role(const BwdArgs& a, Ring r, volatile int* abort_flag) {
       }
     }
     const int s = (int)(r.k % kRing);
-    if (!mbar_wait(r.empty + 8 * s, ((r.k / kRing) & 1) ^ 1, abort_flag, a.status)) return;
+    if (!mbar_wait(r.empty + 8 * s, ((r.k / kRing) & 1) ^ 1, abort_flag, a.status, a.unit_ns)) return;
 #pragma unroll
     for (int i = 0; i < kEntry; ++i) r.slot[kEntry * s + i] = e[i];
     mbar_arrive(r.full + 8 * s);
@@ -667,7 +671,8 @@ __device__ void epilogue_role(const BwdArgs& a, uint32_t bars, uint32_t tmem,
     }
     const size_t base = ((size_t)row * (MODE == kDQ ? a.H : a.Hkv) + u.oh) * D;
     ok = __all_sync(0xffffffffu,
-                    mbar_wait_long(bars + 8 * C::B_ACCFULL, seen & 1, abort_flag, a.status));
+                    mbar_wait_long(bars + 8 * C::B_ACCFULL, seen & 1, abort_flag, a.status,
+                                   a.unit_ns));
     if (!ok) break;
     ++seen;
     tc_fence_after();
@@ -1041,6 +1046,7 @@ extern "C" int jagged_window_attn_bwd(const void* q, const void* k, const void* 
   a.group = H / Hkv;
   a.window = (int)(window < T ? window : (T > 0 ? T : 1));
   a.n_sinks = n_sinks;
+  a.unit_ns = kWaitTimeoutNs + 10000ull * (uint64_t)(T / kStep + 3) * (uint64_t)a.group;
   a.v8 = aligned(dq, 32) && aligned(dk, 32) && aligned(dv, 32);
   a.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)d_head);
   a.scale_log2 = a.scale * 1.4426950408889634f;

@@ -1209,3 +1209,37 @@ def test_window_gradient_in_the_workspace_of_its_window(lengths, window, sinks):
         assert torch.equal(x, y)
     with pytest.raises(jca.JcaError):
         b.backward(window, sinks, workspace=torch.empty(sizes[0] - 1, dtype=torch.uint8, device=dev()))
+
+
+def test_window_gradient_of_a_key_that_very_many_rows_see():
+    """A key tile's work of 2.9 million steps, over 2 s: no wait for it gives up. Every query head holds the
+    same query, so that the gradients are those of one head for the heads' summed dO."""
+    T, H, d = 4096, 45000, 16
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 6 * 2 * T * H * d + 3 * 4 * T * H + (8 << 30):
+        pytest.skip("needs 45 GB")
+    g = torch.Generator(device=dev()).manual_seed(9)
+    one, k, v = (torch.randn(T, 1, d, generator=g, device=dev()).to(torch.bfloat16) for _ in range(3))
+    off, st = torch.tensor([0, T], device=dev()), jca.new_status(dev())
+    out1, lse1 = torch.empty_like(one), torch.empty(T, 1, device=dev())
+    jca.jagged_window_attn_fwd(one, k, v, out1, off, T, 0, lse=lse1, status=st)
+    q, out, lse = (x.expand(T, H, *x.shape[2:]).contiguous() for x in (one, out1, lse1))
+    dout = torch.empty_like(q).normal_(generator=g)
+    dq, dk, dv = (torch.full_like(x, float("nan")) for x in (q, k, v))
+    jca.jagged_window_attn_bwd(q, k, v, out, dout, lse, dq, dk, dv, off, T, 0, status=st)
+    jca.check_status(st)
+    assert bool(torch.isfinite(dq.sum(1, dtype=torch.float32)).all())
+    q1, k1, v1, o1 = (x[:, 0].double() for x in (one, k, v, out1))
+    P = torch.exp(d**-0.5 * q1 @ k1.T - lse1.double()).tril()
+    total, spread = dout.sum(1, dtype=torch.float64), dout.abs().sum(1, dtype=torch.float64)
+    dS = P * (total @ v1.T - (total * o1).sum(1, keepdim=True))
+    # |dS| of a head is at most P (|dO| |v| + |dO| |O|); the factors are those of the other gradients.
+    most = P * (spread @ v1.abs().T + (spread * o1.abs()).sum(1, keepdim=True))
+    for name, got, ref, terms in (("dv", dv, P.T @ total, P.T @ spread),
+                                  ("dk", dk, d**-0.5 * dS.T @ q1, d**-0.5 * most.T @ q1.abs())):
+        tol = (2.0**-8 + 2.0**-11) * terms + 2.0**-8 * ref.abs()
+        near(got[:, 0], ref.cpu().numpy(), tol.cpu().numpy(), name)
+    mask = lh.window_mask(T, T, 0)
+    for h in (0, H - 1):
+        (x, _, _), (tq, _, _) = lh.gradients(one, k, v, dout[:, h:h + 1], mask, d**-0.5)
+        near(dq[:, h:h + 1], x, 2.0**-8 * tq[0] + 2.0**-11 * tq[1] + 2.0**-8 * np.abs(x) + 1e-30, f"dq {h}")
