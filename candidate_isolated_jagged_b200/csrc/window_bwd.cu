@@ -66,6 +66,11 @@ constexpr int kStep = 64;        // inner rows of a step
 // Query rows of a kSink unit: 256 rows keep the longest unit short (16 users: 14 us alone, with 1024
 // rows 36 us; on 256 users 1024 rows took 7 % more).
 constexpr int kChunk = 256;
+// A unit's accumulators are taken over into fp32 sums in memory after so many steps. The tensor core
+// cuts each addition off, which costs a sum about 2^-25 of itself for every 16 products (a key seen by
+// 4,096 rows of 8,192 heads lost 3 % of dV); within 4,096 steps of four additions that is 2^-11.
+constexpr int kSpill = 4096;
+constexpr int kMaxSms = 160;     // no part of a launch has more blocks
 constexpr int kRing = 4;
 constexpr int kEntry = 6;        // ints of a ring entry
 
@@ -84,12 +89,13 @@ struct BwdArgs {
   int window_slot;            // slot of the window's own sums: this + the user's place in sink_users
   const int4* sinks;          // kSink units {first row, end, chunk, slot}
   const int4* sink_users;     // their users {first row, end, slot of the first unit, 0}
+  float* spill;               // [block][128][2][D], where a unit has more than kSpill steps
   const int32_t* n_sink_units;
   const int32_t* n_sink_users;
   int32_t* counter;           // [3] next unit of each part
   int32_t* status;
-  // Limit of the waits for a whole unit (the epilogue's, and that for room in the ring): the other
-  // waits are for one step, and an abort there ends these too. 10 us a step of the longest unit; a
+  // Limit of the wait for room in the ring, which is one for a whole unit: the other waits are for
+  // kSpill steps at most, and an abort there ends this one too. 10 us a step of the longest unit; a
   // step takes 0.8 to 1.
   uint64_t unit_ns;
   int T, H, Hkv, group, window, n_sinks;
@@ -438,7 +444,7 @@ __device__ void ts_role(const BwdArgs& a, uint32_t sbase, uint32_t bars, uint32_
   constexpr uint32_t kRows16 = (16 * C::SW) >> 4;
   const int infull = a.valid ? C::B_INREADY : C::B_INFULL;
   const uint64_t in = smem_desc(sbase + C::OFF_IN, C::IN_BLK, 8 * C::SW, C::LAYOUT);
-  uint32_t g = 0, units = 0;
+  uint32_t g = 0, sums = 0;
   bool ok = true;
   Unit u;
   Walk<MODE> w;
@@ -452,12 +458,17 @@ __device__ void ts_role(const BwdArgs& a, uint32_t sbase, uint32_t bars, uint32_
   };
   while (ok && ring_take<MODE>(ring, a, u, abort_flag, ok)) {
     w.begin(u, a);
-    for (bool more = true, first = true; more; ++g, first = false, more = w.next(u)) {
+    for (bool more = true; more; ++g, more = w.next(u)) {
       const int s = (int)(g % C::STAGES), b = (int)(g % C::BUFS);
+      const bool first = w.i % kSpill == 0;   // of the accumulators' sums
+      if (first && w.i > 0) {
+        tc_commit(bars + 8 * C::B_ACCFULL);
+        ++sums;
+      }
       // The tile has landed (S was formed from it); this thread sees that for itself.
       ok = mbar_wait_long(bars + 8 * (infull + s), (g / C::STAGES) & 1, abort_flag, a.status);
-      if (ok && first && units > 0)
-        ok = mbar_wait_long(bars + 8 * C::B_ACCFREE, (units - 1) & 1, abort_flag, a.status);
+      if (ok && first && sums > 0)
+        ok = mbar_wait_long(bars + 8 * C::B_ACCFREE, (sums - 1) & 1, abort_flag, a.status);
       if (ok)
         ok = mbar_wait_long(bars + 8 * (C::B_DSFULL + b), (g / C::BUFS) & 1, abort_flag, a.status);
       if (!ok) break;
@@ -476,7 +487,7 @@ __device__ void ts_role(const BwdArgs& a, uint32_t sbase, uint32_t bars, uint32_
     }
     if (!ok) break;
     tc_commit(bars + 8 * C::B_ACCFULL);
-    ++units;
+    ++sums;
   }
   if (!ok) {
     tc_commit(bars + 8 * (C::B_DRAIN + 1));
@@ -627,7 +638,25 @@ __device__ void compute_role(const BwdArgs& a, uint32_t bars, uint32_t tmem, flo
   }
 }
 
-// Writes a unit's accumulators out, a row a thread, while the compute warps are at the next unit.
+// 16 fp32 values in memory: written, and added to.
+__device__ __forceinline__ void put16(float* to, const uint32_t* x) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    reinterpret_cast<uint4*>(to)[k] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+}
+__device__ __forceinline__ void add16(uint32_t* x, const float* from) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float4 y = reinterpret_cast<const float4*>(from)[k];
+    x[4 * k] = __float_as_uint(__uint_as_float(x[4 * k]) + y.x);
+    x[4 * k + 1] = __float_as_uint(__uint_as_float(x[4 * k + 1]) + y.y);
+    x[4 * k + 2] = __float_as_uint(__uint_as_float(x[4 * k + 2]) + y.z);
+    x[4 * k + 3] = __float_as_uint(__uint_as_float(x[4 * k + 3]) + y.w);
+  }
+}
+
+// Writes a unit's accumulators out, a row a thread, while the compute warps are at the next unit. Of a
+// unit of more than kSpill steps they come several times; a thread adds its row up in its own place.
 template <int D, int MODE>
 __device__ void epilogue_role(const BwdArgs& a, uint32_t bars, uint32_t tmem,
                               volatile int* abort_flag, int warp, int lane, Ring ring) {
@@ -636,6 +665,7 @@ __device__ void epilogue_role(const BwdArgs& a, uint32_t bars, uint32_t tmem,
   const int r = (warp & 3) * 32 + lane;
   const uint32_t t_lane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
   const uint32_t t_a0 = t_lane + C::TMEM_A0, t_a1 = t_lane + C::TMEM_A1;
+  float* spill = a.spill + ((size_t)blockIdx.x * kTileM + r) * 2 * D;
   uint32_t seen = 0;
   bool ok = true;
   Unit u;
@@ -670,39 +700,45 @@ __device__ void epilogue_role(const BwdArgs& a, uint32_t bars, uint32_t tmem,
       }
     }
     const size_t base = ((size_t)row * (MODE == kDQ ? a.H : a.Hkv) + u.oh) * D;
-    ok = __all_sync(0xffffffffu,
-                    mbar_wait_long(bars + 8 * C::B_ACCFULL, seen & 1, abort_flag, a.status,
-                                   a.unit_ns));
-    if (!ok) break;
-    ++seen;
-    tc_fence_after();
+    for (int done = 0; done < u.n_in; done += kSpill) {
+      const bool last = u.n_in - done <= kSpill;
+      ok = __all_sync(0xffffffffu,
+                      mbar_wait_long(bars + 8 * C::B_ACCFULL, seen & 1, abort_flag, a.status));
+      if (!ok) break;
+      ++seen;
+      tc_fence_after();
 #pragma unroll 1
-    for (int c0 = 0; c0 < D; c0 += CW) {
-      uint32_t x[CW], y[CW];
-      tmem_ld_x16(t_a0 + c0, x);
-      if (MODE != kDQ) tmem_ld_x16(t_a1 + c0, y);
-      tmem_wait_ld();
-      reg_fence16(x);
-      if (MODE != kDQ) reg_fence16(y);
-      if (c0 + CW >= D) {
-        tc_fence_before();
-        mbar_arrive(bars + 8 * C::B_ACCFREE);
-      }
-      if (!writes) continue;
-      if (MODE == kDQ) {
-        put(a.dq + base + c0, x, a.scale);
-      } else if (mine) {
-        uint4* m = reinterpret_cast<uint4*>(mine + c0);
-#pragma unroll
-        for (int k = 0; k < CW / 4; ++k) {
-          m[k] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-          m[D / 4 + k] = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+      for (int c0 = 0; c0 < D; c0 += CW) {
+        uint32_t x[CW], y[CW];
+        tmem_ld_x16(t_a0 + c0, x);
+        if (MODE != kDQ) tmem_ld_x16(t_a1 + c0, y);
+        tmem_wait_ld();
+        reg_fence16(x);
+        if (MODE != kDQ) reg_fence16(y);
+        if (c0 + CW >= D) {
+          tc_fence_before();
+          mbar_arrive(bars + 8 * C::B_ACCFREE);
         }
-      } else if (MODE == kDKV) {
-        put(a.dv + base + c0, x, 1.f);
-        put(a.dk + base + c0, y, a.scale);
+        if (!writes) continue;
+        if (done > 0) {
+          add16(x, spill + c0);
+          if (MODE != kDQ) add16(y, spill + D + c0);
+        }
+        if (!last) {
+          put16(spill + c0, x);
+          if (MODE != kDQ) put16(spill + D + c0, y);
+        } else if (MODE == kDQ) {
+          put(a.dq + base + c0, x, a.scale);
+        } else if (mine) {
+          put16(mine + c0, x);
+          put16(mine + D + c0, y);
+        } else if (MODE == kDKV) {
+          put(a.dv + base + c0, x, 1.f);
+          put(a.dk + base + c0, y, a.scale);
+        }
       }
     }
+    if (!ok) break;
   }
 }
 
@@ -894,8 +930,9 @@ __global__ void __launch_bounds__(256) window_join_kernel(const BwdArgs a) {
 
 struct BwdLayout {
   size_t row_start = 0, row_end = 0, row_number = 0, lse2 = 0, dsum = 0, sinks = 0, users = 0,
-         part = 0, counters = 0, total = 0;
+         part = 0, spill = 0, counters = 0, total = 0;
   int64_t slots = 0, sink_users = 0;   // chunk partials, users that can have any
+  bool spills = false;                 // some unit may have more than kSpill steps
 };
 
 // Only users longer than the window leave partial sums: at most T / (window + 1) of them. Their rows
@@ -915,7 +952,9 @@ BwdLayout bwd_layout(int64_t B, int64_t T, int H, int Hkv, int d, int64_t window
   L.sinks = L.dsum + align_up(4 * (size_t)T * H, 256);
   L.users = L.sinks + align_up(16 * (size_t)L.slots, 256);
   L.part = L.users + align_up(16 * (size_t)L.sink_users, 256);
-  L.counters = L.part + align_up(8 * (size_t)(L.slots + L.sink_users) * Hkv * n_sinks * d, 256);
+  L.spill = L.part + align_up(8 * (size_t)(L.slots + L.sink_users) * Hkv * n_sinks * d, 256);
+  L.spills = std::max(T / kStep + 3, (T / kStep + 1) * (H / Hkv)) > kSpill;
+  L.counters = L.spill + (L.spills ? (size_t)3 * kMaxSms * kTileM * 2 * d * 4 : 0);
   L.total = L.counters + 256;
   return L;
 }
@@ -936,6 +975,7 @@ int launch_parts(BwdArgs a, const Maps& m, int64_t sink_units, int dev, int sms,
       return JCA_ERR_CUDA;
     set[dev].store(true, std::memory_order_release);
   }
+  sms = std::min(sms, kMaxSms);
   a.blocks_sink = (int)std::min<int64_t>(sink_units, sms);
   a.blocks_dkv = std::min(a.units_dkv, sms);
   const int grid = a.blocks_sink + a.blocks_dkv + std::min(a.units_dq, sms);
@@ -1033,6 +1073,7 @@ extern "C" int jagged_window_attn_bwd(const void* q, const void* k, const void* 
   a.lse2 = reinterpret_cast<float*>(ws + L.lse2);
   a.dsum = reinterpret_cast<float*>(ws + L.dsum);
   a.part = sinks ? reinterpret_cast<float*>(ws + L.part) : nullptr;
+  a.spill = L.spills ? reinterpret_cast<float*>(ws + L.spill) : nullptr;
   a.window_slot = (int)L.slots;
   a.sinks = reinterpret_cast<int4*>(ws + L.sinks);
   a.sink_users = reinterpret_cast<int4*>(ws + L.users);

@@ -1243,3 +1243,73 @@ def test_window_gradient_of_a_key_that_very_many_rows_see():
     for h in (0, H - 1):
         (x, _, _), (tq, _, _) = lh.gradients(one, k, v, dout[:, h:h + 1], mask, d**-0.5)
         near(dq[:, h:h + 1], x, 2.0**-8 * tq[0] + 2.0**-11 * tq[1] + 2.0**-8 * np.abs(x) + 1e-30, f"dq {h}")
+
+
+@pytest.mark.parametrize("window,sinks", [(1 << 40, 0), (4090, 4), (64, 4)])
+def test_window_gradient_of_long_sums(window, sinks):
+    """dK and dV of one key head over 8,192 query heads, all terms of dV of one sign: up to 33 million
+    products to a sum. In the tensor core's accumulators alone dV came out 3 % small."""
+    T, H, d = 4096, 8192, 16
+    torch.cuda.empty_cache()
+    g = torch.Generator(device=dev()).manual_seed(10)
+    one, k, v = (torch.randn(T, 1, d, generator=g, device=dev()).to(torch.bfloat16) for _ in range(3))
+    off, st = torch.tensor([0, T], device=dev()), jca.new_status(dev())
+    out1, lse1 = torch.empty_like(one), torch.empty(T, 1, device=dev())
+    jca.jagged_window_attn_fwd(one, k, v, out1, off, window, sinks, lse=lse1, status=st)
+    q, out, lse = (x.expand(T, H, *x.shape[2:]).contiguous() for x in (one, out1, lse1))
+    dout = torch.empty_like(q).normal_(generator=g).abs_()
+    dq, dk, dv = (torch.full_like(x, float("nan")) for x in (q, k, v))
+    jca.jagged_window_attn_bwd(q, k, v, out, dout, lse, dq, dk, dv, off, window, sinks, status=st)
+    jca.check_status(st)
+    mask = torch.tensor(lh.window_mask(T, window, sinks), device=dev())
+    q1, k1, v1, o1 = (x[:, 0].double() for x in (one, k, v, out1))
+    P = torch.where(mask, torch.exp(d**-0.5 * q1 @ k1.T - lse1.double()), 0.0)
+    total = dout.sum(1, dtype=torch.float64)
+    # All terms of dV are positive: P is rounded to bf16 (2^-8), scores and statistics are fp32 (2^-11),
+    # the accumulators are cut at most 2^14 times at 2^-23 of the sum (2^-9), the result is rounded.
+    ref = P.T @ total
+    near(dv[:, 0], ref.cpu().numpy(), (2 * 2.0**-8 + 2.0**-11 + 2.0**-9) * ref.cpu().numpy(), "dv")
+    dS = P * (total @ v1.T - (total * o1).sum(1, keepdim=True))
+    most = P * (total @ v1.abs().T + (total * o1.abs()).sum(1, keepdim=True))
+    ref, terms = d**-0.5 * dS.T @ q1, d**-0.5 * most.T @ q1.abs()
+    near(dk[:, 0], ref.cpu().numpy(), ((2.0**-8 + 2.0**-11 + 2.0**-9) * terms + 2.0**-8 * ref.abs()).cpu().numpy(), "dk")
+    assert bool(torch.isfinite(dq.sum(1, dtype=torch.float32)).all())
+
+
+def test_window_rows_that_see_very_many_keys():
+    """One user of 600,000 rows: dQ of the last rows and dK, dV of the first are sums over all of them."""
+    T, d = 600_000, 16
+    g = torch.Generator(device=dev()).manual_seed(11)
+    q, k, v, do = (torch.randn(T, 1, d, generator=g, device=dev()).to(torch.bfloat16) for _ in range(4))
+    off, st = torch.tensor([0, T], device=dev()), jca.new_status(dev())
+    out, lse = torch.empty_like(q), torch.empty(T, 1, device=dev())
+    jca.jagged_window_attn_fwd(q, k, v, out, off, T, 0, lse=lse, status=st)
+    jca.check_status(st)
+    grads = [torch.full_like(x, float("nan")) for x in (q, k, v)]
+    jca.jagged_window_attn_bwd(q, k, v, out, do, lse, *grads, off, T, 0, status=st)
+    jca.check_status(st)
+    q1, k1, v1, o1, do1 = (x[:, 0].double() for x in (q, k, v, out, do))
+    scale, D, E = d**-0.5, (do1 * o1).sum(1, keepdim=True), (do1 * o1).abs().sum(1, keepdim=True)
+    j = torch.arange(T, device=dev())
+    last = torch.tensor([T - 1, T - 100, T // 2, 300_001], device=dev())
+    S = scale * q1[last] @ k1.T
+    P = torch.where(j[None] <= last[:, None], torch.exp(S - S.amax(1, keepdim=True)), 0.0)
+    P /= P.sum(1, keepdim=True)
+    ref, A = P @ v1, P @ v1.abs()
+    near(out[last, 0], ref.cpu().numpy(), ((2.0**-8 + 2.0**-11) * A + 2.0**-8 * ref.abs()).cpu().numpy(), "out")
+    dS = P * (do1[last] @ v1.T - D[last])
+    soft, hard = dS.abs() + P * E[last], P * (do1[last].abs() @ v1.abs().T + D[last].abs() + E[last])
+    ref = scale * dS @ k1
+    tol = scale * (2.0**-8 * soft + 2.0**-11 * hard) @ k1.abs() + 2.0**-8 * ref.abs()
+    near(grads[0][last, 0], ref.cpu().numpy(), tol.cpu().numpy(), "dq")
+    first = torch.tensor([0, 1, 127, 128, T // 2], device=dev())
+    P = torch.where(j[:, None] >= first[None], torch.exp(scale * q1 @ k1[first].T - lse.double()), 0.0)
+    dS = P * (do1 @ v1[first].T - D)
+    soft, hard = dS.abs() + P * E, P * (do1.abs() @ v1[first].abs().T + D.abs() + E)
+    ref = P.T @ do1
+    tol = (2.0**-8 + 2.0**-11) * P.T @ do1.abs() + 2.0**-8 * ref.abs()
+    near(grads[2][first, 0], ref.cpu().numpy(), tol.cpu().numpy(), "dv")
+    ref = scale * dS.T @ q1
+    tol = scale * (2.0**-8 * soft + 2.0**-11 * hard).T @ q1.abs() + 2.0**-8 * ref.abs()
+    near(grads[1][first, 0], ref.cpu().numpy(), tol.cpu().numpy(), "dk")
+    assert all(bool(torch.isfinite(x.float().sum())) for x in grads)
