@@ -9,6 +9,7 @@
 namespace jca {
 
 constexpr int kWindowMaxSinks = 128;   // the visible first tokens of a user fit one key tile
+constexpr int kMaxSms = 160;           // no persistent launch, or part of one, has more blocks
 
 bool window_sizes_ok(int64_t B, int64_t T, int H, int Hkv, int n_sinks);
 

@@ -70,7 +70,6 @@ constexpr int kChunk = 256;
 // cuts each addition off, which costs a sum about 2^-25 of itself for every 16 products (a key seen by
 // 4,096 rows of 8,192 heads lost 3 % of dV); within 4,096 steps of four additions that is 2^-11.
 constexpr int kSpill = 4096;
-constexpr int kMaxSms = 160;     // no part of a launch has more blocks
 constexpr int kRing = 4;
 constexpr int kEntry = 6;        // ints of a ring entry
 

@@ -1313,3 +1313,36 @@ def test_window_rows_that_see_very_many_keys():
     tol = scale * (2.0**-8 * soft + 2.0**-11 * hard).T @ q1.abs() + 2.0**-8 * ref.abs()
     near(grads[1][first, 0], ref.cpu().numpy(), tol.cpu().numpy(), "dk")
     assert all(bool(torch.isfinite(x.float().sum())) for x in grads)
+
+
+@pytest.mark.parametrize("d,T,ramp", [(16, 2_400_000, None), (128, 2_400_000, None), (64, 500_000, (0.1, 3.0)),
+                                      (64, 500_000, (3.0, 0.1)), (128, 400_000, (0.1, 2.0)),
+                                      (128, 400_000, (2.0, 0.1))])
+def test_window_forward_of_long_sums(d, T, ramp):
+    """Rows that see up to 2.4 million keys. With values of one sign the accumulators of the tensor core
+    alone lose 1.4 % of them; with a ramp the largest scores come late or early."""
+    g = torch.Generator(device=dev()).manual_seed(12)
+    T += 130                                                # a short user before the long one
+    q, k, v = (torch.randn(T, 1, d, generator=g, device=dev()) for _ in range(3))
+    if ramp is None:
+        v = v.abs()
+    else:
+        k *= torch.linspace(*ramp, T, device=dev())[:, None, None]
+    q, k, v = (x.to(torch.bfloat16) for x in (q, k, v))
+    off, st = torch.tensor([0, 130, T], device=dev()), jca.new_status(dev())
+    out, lse = torch.full_like(q, float("nan")), torch.full((T, 1), float("nan"), device=dev())
+    jca.jagged_window_attn_fwd(q, k, v, out, off, 1 << 40, 0, lse=lse, status=st)
+    jca.check_status(st)
+    assert bool(torch.isfinite(out.float().sum()))
+    j = torch.arange(T, device=dev())
+    for rows in (torch.arange(T - 20, T, device=dev()), torch.arange(T // 2, T // 2 + 20, device=dev()),
+                 torch.tensor([130, 131, 131_000, 131_500, 262_400], device=dev())):
+        S = d**-0.5 * q[rows, 0].double() @ k[:, 0].double().T
+        S.masked_fill_((j[None] > rows[:, None]) | (j[None] < 130), -float("inf"))
+        want = torch.logsumexp(S, 1)
+        P = torch.exp(S - want[:, None])
+        ref, A = P @ v[:, 0].double(), P @ v[:, 0].double().abs()
+        # The file's tolerance, and 2^13 additions cut at 2^-23 of the sum.
+        tol = (2.0**-8 + 2.0**-11 + 2.0**-10) * A + 2.0**-8 * ref.abs()
+        near(out[rows, 0], ref.cpu().numpy(), tol.cpu().numpy(), "out")
+        assert float((lse[rows, 0].double() - want).abs().max()) <= 2.0**-11
