@@ -11,7 +11,6 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import functools
-import operator
 import os
 import re
 from typing import Optional
@@ -679,13 +678,14 @@ def _at(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
-@functools.lru_cache(maxsize=64)
-def _section_array(sections):
-    return (c_i32 * len(sections))(*(_clip(x, 32) for x in sections))
+@functools.lru_cache(maxsize=64, typed=True)   # typed: 8.0 is not taken for an 8 seen before
+def _section_array(*sections):
+    # ctypes refuses what is no integer.
+    return (c_i32 * len(sections))(*(_clip(x, 32) if isinstance(x, int) else x for x in sections))
 
 
 def _sections(sections):
-    return _section_array(tuple(map(operator.index, sections)))
+    return _section_array(*sections)
 
 
 def _rope_axes(fn, q, k, q_out, k_out, positions, sections, base, per_axis, stream) -> int:
