@@ -351,11 +351,12 @@ __device__ __forceinline__ void reg_fence_cols(uint32_t* r) {
   }
 }
 
-// One accumulator row (D columns) multiplied by alpha in place in TMEM.
-template <int D>
-__device__ __forceinline__ void rescale_o_row(uint32_t t_o, float alpha) {
+// One accumulator row (D columns) multiplied by alpha in place in TMEM, UNROLL runs of up to 32 columns
+// at a time; the caller waits for the stores.
+template <int D, int UNROLL>
+__device__ __forceinline__ void scale_row(uint32_t t_o, float alpha) {
   constexpr int CW = D < 32 ? D : 32;
-#pragma unroll
+#pragma unroll UNROLL
   for (int c0 = 0; c0 < D; c0 += CW) {
     uint32_t u[CW];
     tmem_ld_cols<CW>(t_o + c0, u);
@@ -365,6 +366,12 @@ __device__ __forceinline__ void rescale_o_row(uint32_t t_o, float alpha) {
     for (int i = 0; i < CW; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * alpha);
     tmem_st_cols<CW>(t_o + c0, u);
   }
+}
+
+// The same with the wait, all of it unrolled.
+template <int D>
+__device__ __forceinline__ void rescale_o_row(uint32_t t_o, float alpha) {
+  scale_row<D, 4>(t_o, alpha);
   tmem_wait_st();
 }
 

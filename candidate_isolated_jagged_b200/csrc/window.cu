@@ -205,11 +205,6 @@ __device__ __forceinline__ Item make_item(const volatile int* e, const FwdArgs& 
   return w;
 }
 
-struct Ring {
-  volatile int* slot;
-  uint32_t full, empty, k;
-};
-
 // Takes the next entry, and the user start of row `r` of the block; false when aborting or at the end.
 __device__ __forceinline__ bool ring_take(Ring& r, const FwdArgs& a, Item& w,
                                           volatile int* abort_flag, bool& ok, int row = 0,
@@ -312,7 +307,6 @@ template <int D>
 __device__ void padding_role(const FwdArgs& a, uint32_t sbase, uint32_t bars,
                              volatile int* abort_flag, int lane, Ring ring) {
   using C = Cfg<D>;
-  constexpr int CH = C::ROW_BYTES / 16, CB = C::SW / 16;
   uint32_t g = 0;
   bool ok = true;
   Item w;
@@ -331,17 +325,8 @@ __device__ void padding_role(const FwdArgs& a, uint32_t sbase, uint32_t bars,
       if (!__all_sync(0xffffffffu, ok)) return;
       const uint32_t tile = sbase + C::OFF_V + s * C::TILE_BYTES;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (!pad[c]) continue;
-        // A row's bytes of a column block are contiguous; the swizzle only reorders them.
-#pragma unroll 1
-        for (int i = lane; i < 32 * CH; i += 32) {
-          const int r = i / CH, x = i % CH;
-          if ((pad[c] >> r) & 1)
-            st_shared_v4(tile + (x / CB) * C::BLK_BYTES + (32 * c + r) * C::SW + (x % CB) * 16, 0u,
-                         0u, 0u, 0u);
-        }
-      }
+      for (int c = 0; c < 4; ++c)
+        if (pad[c]) zero_rows<C::ROW_BYTES, C::SW, C::BLK_BYTES>(tile, 32 * c, pad[c], lane);
       fence_proxy_async_smem();
       mbar_arrive(bars + 8 * (C::B_VREADY + s));
     }
@@ -466,14 +451,6 @@ __device__ void mma_role(const FwdArgs& a, uint32_t sbase, uint32_t bars, uint32
   }
 }
 
-// Bits [a, b) of a word, for any a and b.
-__device__ __forceinline__ uint32_t range_bits(int a, int b) {
-  a = min(max(a, 0), 32);
-  b = min(max(b, 0), 32);
-  const uint32_t below_b = b >= 32 ? 0xffffffffu : (1u << b) - 1u;
-  return a >= 32 ? 0u : below_b & (0xffffffffu << a);
-}
-
 // Weights p = 2^(scale_log2 s - m) of 32 scores, their sum added to (acc0, acc1), and the weights
 // rounded to bf16 pairs, the operand type of the PV product.
 __device__ __forceinline__ void weights32(const uint32_t* x, float2 sl2v, float2 negv, float2& acc0,
@@ -488,22 +465,6 @@ __device__ __forceinline__ void weights32(const uint32_t* x, float2 sl2v, float2
     if (k & 1) acc1 = __fadd2_rn(acc1, p);
     else acc0 = __fadd2_rn(acc0, p);
     pk[k] = pack_bf16x2(p.x, p.y);
-  }
-}
-
-// One row of O multiplied by alpha in place in TMEM.
-template <int D>
-__device__ __forceinline__ void rescale_row(uint32_t t_o, float alpha) {
-  constexpr int CW = D < 32 ? D : 32;
-#pragma unroll 1
-  for (int c0 = 0; c0 < D; c0 += CW) {
-    uint32_t u[CW];
-    tmem_ld_cols<CW>(t_o + c0, u);
-    tmem_wait_ld();
-    reg_fence_cols<CW>(u);
-#pragma unroll
-    for (int i = 0; i < CW; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * alpha);
-    tmem_st_cols<CW>(t_o + c0, u);
   }
 }
 
@@ -636,7 +597,7 @@ __device__ void softmax_role(const FwdArgs& a, uint32_t bars, uint32_t tmem,
         }
         // O is stable here: without SEP_P its last PV was issued before the QK that filled S, and a
         // commit fires only after every earlier MMA of its thread.
-        if (__any_sync(0xffffffffu, rescale && !fresh)) rescale_row<D>(t_o, alpha);
+        if (__any_sync(0xffffffffu, rescale && !fresh)) scale_row<D, 1>(t_o, alpha);
         l = l * alpha + ((acc0.x + acc0.y) + (acc1.x + acc1.y));
         m = m_use;
         fresh = false;

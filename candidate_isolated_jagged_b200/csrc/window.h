@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include "jca.h"
+#include "jca_device.cuh"
 
 namespace jca {
 
@@ -33,6 +34,33 @@ __device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.w
 // Lets the dependent kernel's blocks be placed once every block here has got this far.
 __device__ __forceinline__ void grid_dep_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// A ring of entries in shared memory from which every role of a block takes its next piece of work.
+struct Ring {
+  volatile int* slot;
+  uint32_t full, empty, k;
+};
+
+// Bits [a, b) of a word, for any a and b.
+__device__ __forceinline__ uint32_t range_bits(int a, int b) {
+  a = min(max(a, 0), 32);
+  b = min(max(b, 0), 32);
+  const uint32_t below_b = b >= 32 ? 0xffffffffu : (1u << b) - 1u;
+  return a >= 32 ? 0u : below_b & (0xffffffffu << a);
+}
+
+// Zeroes the rows r0 + i of a tile for which bit i is set; one warp. A row's bytes of a column block (SW
+// of them, blocks BLK bytes apart) are contiguous; the swizzle only reorders them.
+template <int ROW_BYTES, int SW, int BLK>
+__device__ __forceinline__ void zero_rows(uint32_t tile, int r0, uint32_t rows, int lane) {
+  constexpr int CH = ROW_BYTES / 16, CB = SW / 16;
+#pragma unroll 1
+  for (int i = lane; i < 32 * CH; i += 32) {
+    const int r = i / CH, x = i % CH;
+    if ((rows >> r) & 1)
+      st_shared_v4(tile + (x / CB) * BLK + (r0 + r) * SW + (x % CB) * 16, 0u, 0u, 0u, 0u);
+  }
 }
 
 template <typename... Params, typename... Args>

@@ -220,11 +220,6 @@ struct Walk {
   }
 };
 
-struct Ring {
-  volatile int* slot;
-  uint32_t full, empty, k;
-};
-
 template <int MODE>
 __device__ __forceinline__ bool ring_take(Ring& r, const BwdArgs& a, Unit& u,
                                           volatile int* abort_flag, bool& ok) {
@@ -337,7 +332,6 @@ template <int D, int MODE>
 __device__ void padding_role(const BwdArgs& a, uint32_t sbase, uint32_t bars,
                              volatile int* abort_flag, int lane, Ring ring) {
   using C = Cfg<D, MODE>;
-  constexpr int CH = C::ROW_BYTES / 16, CB = C::SW / 16;
   uint32_t g = 0;
   bool ok = true;
   Unit u;
@@ -360,15 +354,8 @@ __device__ void padding_role(const BwdArgs& a, uint32_t sbase, uint32_t bars,
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         if (!pad[c]) continue;
-        // A row's bytes of a column block are contiguous; the swizzle only reorders them.
-#pragma unroll 1
-        for (int y = lane; y < 32 * CH; y += 32) {
-          const int r = y / CH, x = y % CH;
-          if (!((pad[c] >> r) & 1)) continue;
-          const uint32_t at = tile + (x / CB) * C::IN_BLK + (32 * c + r) * C::SW + (x % CB) * 16;
-          st_shared_v4(at, 0u, 0u, 0u, 0u);
-          st_shared_v4(at + C::IN_TILE, 0u, 0u, 0u, 0u);
-        }
+        zero_rows<C::ROW_BYTES, C::SW, C::IN_BLK>(tile, 32 * c, pad[c], lane);
+        zero_rows<C::ROW_BYTES, C::SW, C::IN_BLK>(tile + C::IN_TILE, 32 * c, pad[c], lane);
       }
       fence_proxy_async_smem();
       mbar_arrive(bars + 8 * (C::B_INREADY + s));
@@ -492,14 +479,6 @@ __device__ void ts_role(const BwdArgs& a, uint32_t sbase, uint32_t bars, uint32_
     tc_commit(bars + 8 * (C::B_DRAIN + 1));
     mbar_wait_drain(bars + 8 * (C::B_DRAIN + 1), 0);
   }
-}
-
-// Bits [a, b) of a word, for any a and b.
-__device__ __forceinline__ uint32_t range_bits(int a, int b) {
-  a = min(max(a, 0), 32);
-  b = min(max(b, 0), 32);
-  const uint32_t below_b = b >= 32 ? 0xffffffffu : (1u << b) - 1u;
-  return a >= 32 ? 0u : below_b & (0xffffffffu << a);
 }
 
 template <int D, int MODE>
