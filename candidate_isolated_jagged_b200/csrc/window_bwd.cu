@@ -352,11 +352,8 @@ __device__ void padding_role(const BwdArgs& a, uint32_t sbase, uint32_t bars,
       if (!__all_sync(0xffffffffu, ok)) return;
       const uint32_t tile = sbase + C::OFF_IN + s * C::IN_STAGE;
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        if (!pad[c]) continue;
-        zero_rows<C::ROW_BYTES, C::SW, C::IN_BLK>(tile, 32 * c, pad[c], lane);
-        zero_rows<C::ROW_BYTES, C::SW, C::IN_BLK>(tile + C::IN_TILE, 32 * c, pad[c], lane);
-      }
+      for (int c = 0; c < 2; ++c)
+        if (pad[c]) zero_rows<C::ROW_BYTES, C::SW, C::IN_BLK, C::IN_TILE>(tile, 32 * c, pad[c], lane);
       fence_proxy_async_smem();
       mbar_arrive(bars + 8 * (C::B_INREADY + s));
     }
