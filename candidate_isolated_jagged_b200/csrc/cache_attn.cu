@@ -714,9 +714,10 @@ constexpr int kMaxDevices = 64;
 // `keys`: no unit walks more. The key list is split while the blocks fit the device at two per SM and
 // the longest list leaves each part a tile: with few units the longest list sets the time (4 users
 // with trees: 14.3 us whole, 11.2 in two parts, 9.7 in eight; one token over 4,096 keys: 24.6 us in
-// two parts, 10.9 in eight), with many the parts only cost (256 users with trees 222 us, in two
-// parts 284 us, and 290 us when only lists of more than 16 tiles are split; measured before users went
-// by length).
+// two parts, 10.9 in eight), with many the parts only cost (256 users with trees, longest first: 156
+// to 158 us whole, every list in two parts 242, in four 377). Parts for the few longest lists alone have
+// not been measured in this order; before users went by length, parts for lists of more than 16
+// tiles took 290 us against 222.
 template <int D, int RW, bool TREE, typename IdxT>
 int launch_cache(CacheArgs a, int64_t max_rows, int64_t keys, int dev, int sms, cudaStream_t st) {
   using C = CCfg<D, RW, TREE>;

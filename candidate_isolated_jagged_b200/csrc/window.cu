@@ -30,14 +30,19 @@
 //   warp 12      claims the next block from a counter, reads where its rows' users start and passes
 //                both to every role through a ring, several blocks ahead of the loads.
 // The roles' code is kept small: instruction fetch of a larger kernel cost more than the steps
-// themselves (256 users: 663 us with the softmax specialised by the number of visible chunks, which
-// is 350 us here).
+// themselves (256 users: 663 us with the softmax specialised by the number of visible chunks, against
+// 350 in the same short run).
 //
-// What bounds it (256 users, window 256, d = 128: 350 us, 0.49 of the copy bandwidth; 12 long users,
-// window 1024, d = 64: 515 us): the chain QK -> softmax -> PV of each query tile. At d = 64 a tile takes
-// a softmax group about 4100 cycles: 1600 to 2400 for its 16,384 exponentials (1024 at the unit's full
-// rate), 770 for the maximum, 250 to read the scores, the rest in waits that are short but many; TMEM
-// holds the scores of two tiles only. Exponential unit busy 0.42, tensor core 0.23. What did not help:
+// What bounds it (256 users, window 256, d = 128: 350 us in a short run, 360 to 400 in a long one, 0.49
+// to 0.43 of the copy bandwidth; 12 long users, window 1024, d = 64: 515 to 520 us): the chain
+// QK -> softmax -> PV of each query tile. Cycles of a softmax group per tile, with timestamps:
+//   d = 64    4,340: exponentials and weights 1,610 (1,024 at the unit's full rate), maximum 700, which
+//             columns are visible 690, scores awaited and read 460, PV awaited 270, weights stored 180;
+//             a block's output 2,520 of waiting and 1,410 of writing, over 9 tiles;
+//   d = 128   6,570: scores awaited 1,630 (the weights lie over them, so QK follows PV), exponentials
+//             1,215, visible columns 1,140, maximum 740; a block's output 2,570 and 2,940 over 3.3 tiles.
+// TMEM holds the scores of two tiles only. Exponential unit busy 0.42 (d = 64), tensor core 0.23. What
+// did not help, times of short runs:
 // eight warps on one tile at a time (64 columns a thread; 350 and 657 us), sixteen with two threads to a
 // row that exchange their maxima (460 and 745 us), one thread issuing both tiles' MMAs (350 and
 // 562 us), the two groups taking turns at their exponentials (363 and 540 us), the products of a

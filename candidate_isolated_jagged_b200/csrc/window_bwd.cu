@@ -29,13 +29,13 @@
 //   warps 4..11 compute, a row a thread, two warps per 32 rows (32 of the 64 columns each);
 //   warps 12..15 write a unit's accumulators out while the others are at the next unit.
 //
-// What bounds it (256 users, window 256, d = 128: dKV 437 us, dQ 373, first tokens 118; 0.33 of the copy
-// bandwidth with the statistics before and the joining behind; a tenth longer under the power limit of
-// a long run): the tensor core's part of the
-// chain S, dP -> dS -> products. Seven products are formed per pair instead of five (S and dP in both
+// What bounds it (256 users, window 256, d = 128, in a short run: dKV 437 us, dQ 373, first tokens 118,
+// 1.02 ms with the statistics before and the joining behind, 0.34 of the copy bandwidth; 1.10 to 1.22 ms
+// under the power limit of a long run, 0.31 to 0.28): the tensor core's part of the chain
+// S, dP -> dS -> products. Seven products are formed per pair instead of five (S and dP in both
 // passes), and those of 64 columns take nearly as long as those of 128 (about 60 cycles for 16 of
 // the head) but leave room for three score buffers, which overlap the exponentials and conversions
-// (256 users 1.10 ms in steps of 128 columns, 1.04 ms in steps of 64). For first tokens a 128-row
+// (256 users 1.10 ms in steps of 128 columns, 1.04 ms in steps of 64, short runs). For first tokens a 128-row
 // tile holds n_sinks keys.
 #include <algorithm>
 #include <atomic>

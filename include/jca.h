@@ -600,7 +600,9 @@ int jca_rope_axes_bwd(const void* dq_out, const void* dk_out, void* dq, void* dk
  *   scale    <= 0 selects 1/sqrt(d_head). H a multiple of Hkv.
  *   workspace >= jca_window_workspace_bytes(...) bytes, 256-byte aligned, no part of it needs to
  *            start at zero. Calls that may overlap on the GPU need a workspace each.
- * The outputs overlap no input.
+ * The outputs overlap no input. The weights enter their product with v as bf16, the tensor core's
+ * operand type, as in the other attention calls (each off by at most 2^-8 of itself); scores, softmax
+ * statistics and sums are fp32, and the result is rounded once.
  * A real token's q, k and v are finite. An Inf or NaN in q stays in its own row and one in k in the
  * rows that see it, but one in v may also reach rows that do not see it, those of other users
  * included, since a weight of 0 times Inf or NaN is NaN: every row of a tile that reads it. Tile n is
@@ -622,8 +624,8 @@ int jagged_window_attn_fwd(const void* q, const void* k, const void* v, void* ou
 
 /* Gradients of jagged_window_attn_fwd for the upstream gradient dout, as jagged_cand_attn_bwd: with P
  * the forward's probabilities, dV = P^T dO, dS = P * (dO V^T - rowsum(dO * O)), dQ = scale dS K,
- * dK = scale dS^T Q, where dK and dV of a key head collect those of its query heads. Sums run in a
- * fixed order, so equal calls give equal bits.
+ * dK = scale dS^T Q, where dK and dV of a key head collect those of its query heads. P and dS enter
+ * their products as bf16, the sums are fp32. Sums run in a fixed order, so equal calls give equal bits.
  *   out, lse from the forward on the same inputs; dout [T, H, d_head] bf16, packed, read (rows of
  *   padding may hold anything in out, dout and lse too).
  *   dq [T, H, d_head], dk and dv [T, Hkv, d_head] bf16, packed, written: every row, 0 for padding.
@@ -663,7 +665,9 @@ int jagged_window_attn_bwd(const void* q, const void* k, const void* v, const vo
  *   cache_offsets [B+1] and cache_len [B] in the idx_bits type, read; cache_offsets never falls,
  *     and lies in [0, R]. cache_len[b] = -1 marks an empty slot of the batch: out is 0 there and no
  *     row is written.
- *   window, n_sinks, scale as above, with any n_sinks >= 0.
+ *   window, n_sinks, scale as above, with any n_sinks >= 0. Weights are bf16 operands as above. The fp32
+ *   sums over the keys are the tensor core's own, which cuts additions off: values of one sign come
+ *   out 0.1 % small over 2 million keys, and more over more.
  * Rows that a user's token does not see may hold anything; an Inf or NaN in one that it sees reaches
  * no other user.
  * Device errors, each for its own user, whose rows are then not written while those of other users
@@ -692,7 +696,8 @@ int jagged_window_decode_fwd(const void* q, const void* k_new, const void* v_new
  *   out [Nc, H, d_head] bf16, packed, written.
  *   cand_offsets, hist_offsets [B+1], hist_len [B] in the idx_bits type, read; cand_offsets starts
  *     at 0 and ends at Nc, hist_offsets never falls and lies in [0, R].
- *   max_cand: no run is longer; 1 <= max_cand <= 1024. scale <= 0 selects 1/sqrt(d_head).
+ *   max_cand: no run is longer; 1 <= max_cand <= 1024. scale <= 0 selects 1/sqrt(d_head). Weights and
+ *   sums as in the call for one token. The history is seen whole: there is no window here.
  * Device errors, each for its own user, whose rows are then not written while those of other users
  * (some of their heads, too) may be: bad offsets -> JCA_STATUS_BAD_OFFSETS; hist_len[b] outside its
  * region -> JCA_STATUS_BAD_LENGTH; a bad parent or a run longer than max_cand -> JCA_STATUS_BAD_TREE.
