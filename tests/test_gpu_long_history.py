@@ -1346,3 +1346,116 @@ def test_window_forward_of_long_sums(d, T, ramp):
         tol = (2.0**-8 + 2.0**-11 + 2.0**-10) * A + 2.0**-8 * ref.abs()
         near(out[rows, 0], ref.cpu().numpy(), tol.cpu().numpy(), "out")
         assert float((lse[rows, 0].double() - want).abs().max()) <= 2.0**-11
+
+
+@pytest.mark.parametrize("d,window,sinks", [(16, 400_000, 3), (64, 300_000, 0), (128, 350_000, 70)])
+def test_window_long_rows_with_padding(d, window, sinks):
+    """Long sums together with what else a row may have: padding (not finite), first tokens behind a window
+    that is long itself, shared heads, short users around. Rows and keys sampled at the ends of tiles."""
+    n, H = 500_000, 2
+    off_np = np.array([0, 200, 200 + n, 200 + n + 77])
+    T, s, e = int(off_np[-1]), 200, 200 + n
+    g = torch.Generator(device=dev()).manual_seed(13)
+    x = torch.randn(T, H + 2, d, generator=g, device=dev()).to(torch.bfloat16)
+    do = torch.randn(T, H, d, generator=g, device=dev()).to(torch.bfloat16)
+    valid = (torch.rand(T, generator=g, device=dev()) > 0.1).to(torch.uint8)
+    valid[s:s + 2], valid[e - 1], valid[0] = 0, 1, 1
+    x[valid == 0], do[valid == 0] = float("nan"), float("inf")
+    q, k, v = x.split([H, 1, 1], 1)
+    off, st = torch.tensor(off_np, device=dev()), jca.new_status(dev())
+    out, lse = torch.full((T, H, d), float("nan"), dtype=torch.bfloat16, device=dev()), torch.empty(T, H, device=dev())
+    jca.jagged_window_attn_fwd(q, k, v, out, off, window, sinks, valid=valid, lse=lse, status=st)
+    grads = [torch.full((T, h, d), float("nan"), dtype=torch.bfloat16, device=dev()) for h in (H, 1, 1)]
+    jca.jagged_window_attn_bwd(q, k, v, out, do, lse, *grads, off, window, sinks, valid=valid, status=st)
+    jca.check_status(st)
+    real = valid.bool()
+    for y in [out] + grads:
+        assert bool(torch.isfinite(y.float().sum())) and bool((y[~real] == 0).all())
+    clean = torch.where(real[:, None, None], x, 0).double()
+    kk, vv = clean[:, H], clean[:, H + 1]
+    dd = torch.where(real[:, None, None], do, 0).double()
+    scale, j = d**-0.5, torch.arange(T, device=dev())
+    rows = torch.tensor([s + 2, s + window - 1, s + window + 1, e - 130, e - 1], device=dev())
+    rows = rows[real[rows]]
+    seen = real[None] & (j[None] >= s) & (j[None] <= rows[:, None])
+    seen &= (j[None] > rows[:, None] - window) | (j[None] < s + sinks)
+    keys = torch.tensor([s + 2, s + 3, s + 128, s + 70, e - window, e - 1], device=dev())
+    keys = keys[real[keys]]
+    sees = real[:, None] & (j[:, None] < e) & (j[:, None] >= keys[None])
+    sees &= (j[:, None] - window < keys[None]) | (keys[None] < s + sinks)
+    dk, dv, tk, tv = 0, 0, 0, 0
+    for h in range(H):
+        qq, o1, d1 = clean[:, h], out[:, h].double(), dd[:, h]
+        D, E = (d1 * o1).sum(1, keepdim=True), (d1 * o1).abs().sum(1, keepdim=True)
+        S = (scale * qq[rows] @ kk.T).masked_fill(~seen, -float("inf"))
+        want = torch.logsumexp(S, 1)
+        assert float((lse[rows, h].double() - want).abs().max()) <= 2.0**-11
+        P = torch.exp(S - want[:, None])
+        ref, A = P @ vv, P @ vv.abs()
+        near(out[rows, h], ref.cpu().numpy(), ((2.0**-8 + 2.0**-11) * A + 2.0**-8 * ref.abs()).cpu().numpy(), "out")
+        dS = P * (d1[rows] @ vv.T - D[rows])
+        soft, hard = dS.abs() + P * E[rows], P * (d1[rows].abs() @ vv.abs().T + D[rows].abs() + E[rows])
+        ref = scale * dS @ kk
+        tol = scale * (2.0**-8 * soft + 2.0**-11 * hard) @ kk.abs() + 2.0**-8 * ref.abs()
+        near(grads[0][rows, h], ref.cpu().numpy(), tol.cpu().numpy(), "dq")
+        P = torch.where(sees, torch.exp(scale * qq @ kk[keys].T - torch.where(real, lse[:, h].double(), 0)[:, None]), 0.0)
+        dS = P * (d1 @ vv[keys].T - D)
+        soft, hard = dS.abs() + P * E, P * (d1.abs() @ vv[keys].abs().T + D.abs() + E)
+        dk, dv = dk + scale * dS.T @ qq, dv + P.T @ d1
+        tk = tk + scale * (2.0**-8 * soft + 2.0**-11 * hard).T @ qq.abs()
+        tv = tv + (2.0**-8 + 2.0**-11) * P.T @ d1.abs()
+    near(grads[1][keys, 0], dk.cpu().numpy(), (tk + 2.0**-8 * dk.abs()).cpu().numpy(), "dk")
+    near(grads[2][keys, 0], dv.cpu().numpy(), (tv + 2.0**-8 * dv.abs()).cpu().numpy(), "dv")
+
+
+@pytest.mark.parametrize("op", ["rope", "fwd", "bwd", "decode", "tree"])
+def test_many_users_of_few_rows(op):
+    """1.3 million users, nearly all of them without a row: more than blocks of a grid dimension."""
+    rng = np.random.default_rng(4)
+    B = 1_300_000
+    lens = (rng.random(B) < 0.003) * rng.integers(1, 30, B)
+    off_np = np.concatenate([[0], np.cumsum(lens)])
+    T = int(off_np[-1])
+    g = torch.Generator(device=dev()).manual_seed(5)
+    q, k, v = (torch.randn(T, h, 16, generator=g, device=dev()).to(torch.bfloat16) for h in (2, 1, 1))
+    off, st, out = torch.tensor(off_np, device=dev()), jca.new_status(dev()), torch.full_like(q, float("nan"))
+    some = np.flatnonzero(lens)[rng.integers(0, (lens > 0).sum(), 40)]
+    runs = [(slice(int(off_np[u]), int(off_np[u + 1])), int(lens[u])) for u in some]
+    if op == "rope":
+        pos = torch.arange(T, device=dev())
+        jca.jca_rope_axes_fwd(q, None, out, None, pos, [8])
+        _rope_check(q.cpu(), out, pos.cpu().numpy()[:, None], [8], False, 1.0, op)
+        return
+    if op in ("fwd", "bwd"):
+        lse, grads = torch.empty(T, 2, device=dev()), [torch.full_like(x, float("nan")) for x in (q, k, v)]
+        jca.jagged_window_attn_fwd(q, k, v, out, off, 9, 2, lse=lse, status=st)
+        jca.jagged_window_attn_bwd(q, k, v, out, q, lse, *grads, off, 9, 2, status=st)
+        jca.check_status(st)
+        for r, n in runs:
+            mask = lh.window_mask(n, 9, 2)
+            ref, _, _, A = lh.masked(q[r], k[r], v[r], mask, 0.25)
+            near(out[r], ref, (2.0**-8 + 2.0**-11) * A + 2.0**-8 * np.abs(ref), op)
+            ref, tol = lh.gradients(q[r], k[r], v[r], q[r], mask, 0.25)
+            for got, x, (soft, hard) in zip(grads, ref, tol):
+                near(got[r], x, 2.0**-8 * soft + 2.0**-11 * hard + 2.0**-8 * np.abs(x) + 1e-30, op)
+        return
+    if op == "tree":
+        parent = torch.full((T,), -1, dtype=torch.int32, device=dev())
+        jca.cand_tree_attn_fwd(q, k, v, off, parent, v, k, off, out, 29, status=st)
+        jca.check_status(st)
+        for r, n in runs:
+            ref, _, _, A = lh.masked(q[r], torch.cat([v[r], k[r]]), torch.cat([k[r], v[r]]), lh.tree_mask([-1] * n, n), 0.25)
+            near(out[r], ref, (2.0**-8 + 2.0**-11) * A + 2.0**-8 * np.abs(ref), op)
+        return
+    coff = np.concatenate([[0], np.cumsum(lens + 1)])
+    kc, vc = (torch.randn(int(coff[-1]), 1, 16, generator=g, device=dev()).to(torch.bfloat16) for _ in range(2))
+    q, kn, vn = (torch.randn(B, h, 16, generator=g, device=dev()).to(torch.bfloat16) for h in (2, 1, 1))
+    out = torch.full_like(q, float("nan"))
+    jca.jagged_window_decode_fwd(q, kn, vn, kc, vc, out, torch.tensor(coff, device=dev()),
+                                 torch.tensor(lens, device=dev()), 9, 2, status=st)
+    jca.check_status(st)
+    for u in [0, B - 1] + list(some):
+        r, n = slice(int(coff[u]), int(coff[u + 1])), int(lens[u]) + 1
+        ref, _, _, A = lh.masked(q[u:u + 1], kc[r], vc[r], lh.window_mask(n, 9, 2)[-1:], 0.25)
+        near(out[u:u + 1], ref, (2.0**-8 + 2.0**-11) * A + 2.0**-8 * np.abs(ref), op)
+    assert torch.equal(kc[torch.tensor(coff[1:] - 1, device=dev())], kn)
